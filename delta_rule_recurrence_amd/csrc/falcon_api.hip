@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "falcon.h"
+#include "falcon_check.h"
 #include "falcon_launch.h"
 
 #ifdef FALCON_BOUNDS_CHECK
@@ -30,22 +31,13 @@ std::atomic<int32_t> g_wait_limit{falcon::kDefaultSpinLimit};
 // Form of the Falcon-1 bf16 chunked fast path (falcon_set_f1_launch_form).
 std::atomic<int32_t> g_f1_form{FALCON_F1_ONE_LAUNCH};
 
+using falcon::aligned16;
 using falcon::DecodeArgs;
+using falcon::overlap;
 using falcon::ProblemArgs;
+using falcon::Range;
 
 bool supported_width(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
-}
 
 falcon_status check_problem(const falcon_problem* p) {
   if (!p) return FALCON_ERR_NULL;

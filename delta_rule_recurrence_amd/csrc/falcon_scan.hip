@@ -1,0 +1,387 @@
+// Selective state space scan (gfx950): prompts, single tokens and gradients.
+//
+//   delta_t = softplus(dt_t + bias),  S_t = exp(delta_t A) S_{t-1} + delta_t x_t B_t,
+//   read_t = <C_t, S_t> + D x_t,      y_t = read_t silu(z_t)
+//
+// and backwards, with q_t = dy_t silu(z_t) and G_t the gradient of S_t:
+//
+//   G_t = q_t C_t + exp(delta_{t+1} A) G_{t+1},   m_t = G_t exp(delta_t A) S_{t-1},
+//   dC_t = sum_c q_t S_t,   dB_t = sum_c G_t delta_t x_t,   u_t = <G_t, B_t>,
+//   ddelta_t = <A, m_t> + u_t x_t,   dA = sum_t m_t delta_t,   dx_t = u_t delta_t + D q_t.
+//
+// A lane owns one channel and its N states; a wave 64 adjacent channels of one
+// group, so B_t and C_t are the same for all its lanes.
+
+#include <algorithm>
+
+#include "falcon_block_device.h"
+#include "falcon_launch.h"
+
+namespace falcon {
+
+namespace {
+
+constexpr int kLanes = 64;
+
+struct ScanDims {
+  int B, T, D, G, Dg, tiles;   // Dg channels a group, in `tiles` waves of 64
+  int64_t x_row, dt_row, z_row, b_row, c_row;
+};
+
+template <typename IO>
+struct ScanIn {
+  const IO* x;
+  const IO* dt;
+  const float* A;
+  const IO* Bm;
+  const IO* Cm;
+  const float* Dskip;
+  const float* dt_bias;
+  const IO* z;
+  const float* S0;
+  const int32_t* lengths;
+};
+
+// The wave's sequence, group and this lane's channel (clamped where the group
+// ends inside the wave; such lanes compute on a valid channel and store nothing).
+struct Place {
+  int b, g, c;
+  bool on;
+};
+__device__ __forceinline__ Place place_of(const ScanDims& d, int64_t wave) {
+  const int64_t per = int64_t(d.G) * d.tiles;
+  Place p;
+  p.b = int(wave / per);
+  const int r = int(wave % per);
+  p.g = r / d.tiles;
+  const int c = (r % d.tiles) * kLanes + int(threadIdx.x % kLanes);
+  p.on = c < d.Dg;
+  p.c = p.g * d.Dg + min(c, d.Dg - 1);
+  return p;
+}
+
+template <int N>
+__device__ __forceinline__ void load_state(const float* p, float (&s)[N]) {
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k) {
+    const float4 v = reinterpret_cast<const float4*>(p)[k];
+    s[4 * k] = v.x; s[4 * k + 1] = v.y; s[4 * k + 2] = v.z; s[4 * k + 3] = v.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_state(float* p, const float (&s)[N]) {
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k)
+    reinterpret_cast<float4*>(p)[k] = make_float4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
+}
+
+template <bool SOFTPLUS>
+__device__ __forceinline__ float step_of(float v) { return SOFTPLUS ? softplus_f32(v) : v; }
+
+// ---- prompts ----------------------------------------------------------------------
+// With `states` (the backward's recomputation) the state after every token goes
+// there ([B, T, D, N]) instead of the outputs.
+template <typename IO, int N, bool SOFTPLUS>
+__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanDims d, ScanIn<IO> in, IO* y, float* S_T, float* states) {
+  const Place p = place_of(d, blockIdx.x);
+  const int len = tokens_of(in.lengths, p.b, d.T);
+  const int64_t at = (int64_t(p.b) * d.D + p.c) * N;
+  float S[N], A2[N];
+  load_state<N>(in.A + int64_t(p.c) * N, A2);
+#pragma unroll
+  for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
+  if (in.S0) {
+    load_state<N>(in.S0 + at, S);
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n) S[n] = 0.0f;
+  }
+  const float skip = in.Dskip ? in.Dskip[p.c] : 0.0f, bias = in.dt_bias ? in.dt_bias[p.c] : 0.0f;
+  for (int t = 0; t < len; ++t) {
+    const int64_t token = int64_t(p.b) * d.T + t;
+    const float x = io<IO>::load(in.x, token * d.x_row + p.c);
+    const float delta = step_of<SOFTPLUS>(io<IO>::load(in.dt, token * d.dt_row + p.c) + bias);
+    const IO* pb = in.Bm + token * d.b_row + p.g * N;
+    const IO* pc = in.Cm + token * d.c_row + p.g * N;
+    const float u = delta * x;
+    float read = skip * x;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      S[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), S[n], u * io<IO>::load(pb, n));
+      read = __builtin_fmaf(io<IO>::load(pc, n), S[n], read);
+    }
+    if (states) {
+      if (p.on) store_state<N>(states + (token * d.D + p.c) * N, S);
+    } else if (p.on) {
+      if (in.z) read *= act_f32<kActSilu>(io<IO>::load(in.z, token * d.z_row + p.c));
+      io<IO>::store(y, token * d.D + p.c, read);
+    }
+  }
+  if (S_T && p.on) store_state<N>(S_T + at, S);
+}
+
+// ---- one token --------------------------------------------------------------------
+template <typename IO, int N, bool SOFTPLUS>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanDims d, ScanIn<IO> in, float* S_io, const uint8_t* is_first, IO* y) {
+  constexpr int kPer = N / 4;   // lanes of four states each share a channel
+  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t want = id / kPer;
+  const int q = int(id % kPer);
+  const int64_t cell = min(want, int64_t(d.B) * d.D - 1);
+  const int64_t b = cell / d.D;
+  const int c = int(cell - b * d.D), g = c / d.Dg;
+  float S[4], A2[4];
+  load_state<4>(S_io + cell * N + 4 * q, S);
+  load_state<4>(in.A + int64_t(c) * N + 4 * q, A2);
+  if (is_first && is_first[b]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) S[n] = 0.0f;
+  }
+  const float x = io<IO>::load(in.x, b * d.x_row + c);
+  const float delta = step_of<SOFTPLUS>(io<IO>::load(in.dt, b * d.dt_row + c) + (in.dt_bias ? in.dt_bias[c] : 0.0f));
+  const IO* pb = in.Bm + b * d.b_row + g * N + 4 * q;
+  const IO* pc = in.Cm + b * d.c_row + g * N + 4 * q;
+  float read = 0.0f;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    S[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * (A2[n] * kLog2e)), S[n], delta * x * io<IO>::load(pb, n));
+    read = __builtin_fmaf(io<IO>::load(pc, n), S[n], read);
+  }
+  read = lanes_sum<kPer>(read);
+  if (want < int64_t(d.B) * d.D) {
+    store_state<4>(S_io + cell * N + 4 * q, S);
+    if (q == 0) {
+      read = __builtin_fmaf(in.Dskip ? in.Dskip[c] : 0.0f, x, read);
+      if (in.z) read *= act_f32<kActSilu>(io<IO>::load(in.z, b * d.z_row + c));
+      io<IO>::store(y, b * d.D + c, read);
+    }
+  }
+}
+
+// ---- gradients ----------------------------------------------------------------------
+// One wave a sequence and 64 channels, from the last token to the first, with
+// every state from scan_fwd_kernel.  What sums over channels (dB, dC) leaves as
+// one row a wave, what sums over sequences (dA, dD, ddt_bias) as one a sequence.
+template <typename IO, typename DY, int N, bool SOFTPLUS>
+__global__ __launch_bounds__(64) void scan_bwd_kernel(ScanDims d, ScanIn<IO> in, const DY* dy, const float* dS_T, const float* states,
+                                                      float* dx, float* ddt, float* dz, float* dS0, float* bc_parts, float* par_parts) {
+  const Place p = place_of(d, blockIdx.x);
+  const int len = tokens_of(in.lengths, p.b, d.T);
+  const int tile = int(blockIdx.x % d.tiles);
+  const int64_t at = (int64_t(p.b) * d.D + p.c) * N;
+  const int lane = threadIdx.x;
+  float A[N], G[N], dA[N];
+  load_state<N>(in.A + int64_t(p.c) * N, A);
+#pragma unroll
+  for (int n = 0; n < N; ++n) G[n] = dA[n] = 0.0f;
+  if (dS_T) load_state<N>(dS_T + at, G);
+  const float skip = in.Dskip ? in.Dskip[p.c] : 0.0f, bias = in.dt_bias ? in.dt_bias[p.c] : 0.0f;
+  float dskip = 0.0f, dbias = 0.0f;
+  const float live = p.on ? 1.0f : 0.0f;
+  for (int t = d.T - 1; t >= 0; --t) {
+    const int64_t token = int64_t(p.b) * d.T + t;
+    float* part = bc_parts + ((token * d.G + p.g) * d.tiles + tile) * 2 * N;
+    if (t >= len) {
+      if (p.on) {
+        dx[token * d.D + p.c] = 0.0f;
+        ddt[token * d.D + p.c] = 0.0f;
+        if (dz) dz[token * d.D + p.c] = 0.0f;
+      }
+      if (lane < 2 * N) part[lane] = 0.0f;
+      if (2 * N > kLanes && lane + kLanes < 2 * N) part[lane + kLanes] = 0.0f;
+      continue;
+    }
+    const float x = io<IO>::load(in.x, token * d.x_row + p.c);
+    const float raw = io<IO>::load(in.dt, token * d.dt_row + p.c) + bias;
+    const float delta = step_of<SOFTPLUS>(raw);
+    const float up = io<DY>::load(dy, token * d.D + p.c);
+    const IO* pb = in.Bm + token * d.b_row + p.g * N;
+    const IO* pc = in.Cm + token * d.c_row + p.g * N;
+    const float z = in.z ? io<IO>::load(in.z, token * d.z_row + p.c) : 0.0f;
+    const float q = in.z ? up * act_f32<kActSilu>(z) : up;
+    float S[N], P[N];
+    load_state<N>(states + (token * d.D + p.c) * N, S);
+    if (t > 0) {
+      load_state<N>(states + ((token - 1) * d.D + p.c) * N, P);
+    } else if (in.S0) {
+      load_state<N>(in.S0 + at, P);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) P[n] = 0.0f;
+    }
+    float read = skip * x, u = 0.0f, turn = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float bn = io<IO>::load(pb, n), cn = io<IO>::load(pc, n);
+      read = __builtin_fmaf(cn, S[n], read);
+      G[n] = __builtin_fmaf(q, cn, G[n]);
+      u = __builtin_fmaf(G[n], bn, u);
+      const float db = lanes_sum<kLanes>(live * G[n] * delta * x), dc = lanes_sum<kLanes>(live * q * S[n]);
+      if (lane == 0) {
+        part[n] = db;
+        part[N + n] = dc;
+      }
+      G[n] *= __builtin_amdgcn_exp2f(delta * (A[n] * kLog2e));
+      const float m = G[n] * P[n];
+      turn = __builtin_fmaf(A[n], m, turn);
+      dA[n] = __builtin_fmaf(m, delta, dA[n]);
+    }
+    const float dd = (turn + u * x) * (SOFTPLUS ? sigmoid_f32(raw) : 1.0f);
+    dskip = __builtin_fmaf(q, x, dskip);
+    dbias += dd;
+    if (p.on) {
+      dx[token * d.D + p.c] = __builtin_fmaf(u, delta, skip * q);
+      ddt[token * d.D + p.c] = dd;
+      if (dz) dz[token * d.D + p.c] = up * read * act_slope_f32<kActSilu>(z);
+    }
+  }
+  if (p.on) {
+    if (dS0) store_state<N>(dS0 + at, G);
+    // a sequence's row: [D, N] of dA, [D] of dD, [D] of ddt_bias
+    float* row = par_parts + int64_t(p.b) * d.D * (N + 2);
+    store_state<N>(row + int64_t(p.c) * N, dA);
+    row[int64_t(d.D) * N + p.c] = dskip;
+    row[int64_t(d.D) * (N + 1) + p.c] = dbias;
+  }
+}
+
+// dB, dC of every token and group from its waves' rows.
+__global__ __launch_bounds__(256) void scan_bc_kernel(const float* __restrict__ parts, int tiles, int N, int64_t n, float* __restrict__ dB,
+                                                      float* __restrict__ dC) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+    const int64_t tg = i / (2 * N);
+    const int k = int(i % (2 * N));
+    float s = 0.0f;
+    for (int j = 0; j < tiles; ++j) s += parts[(tg * tiles + j) * 2 * N + k];
+    if (k < N) {
+      dB[tg * N + k] = s;
+    } else {
+      dC[tg * N + k - N] = s;
+    }
+  }
+}
+
+// dA, dD and ddt_bias from the sequences' rows.
+__global__ __launch_bounds__(256) void scan_params_kernel(const float* __restrict__ parts, int rows, int D, int N, float* __restrict__ dA,
+                                                          float* __restrict__ dD, float* __restrict__ ddt_bias) {
+  const int64_t n = int64_t(D) * (N + 2);
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+    double s = 0.0;
+    for (int r = 0; r < rows; ++r) s += parts[r * n + i];
+    if (i < int64_t(D) * N) {
+      dA[i] = float(s);
+    } else if (i < int64_t(D) * (N + 1)) {
+      if (dD) dD[i - int64_t(D) * N] = float(s);
+    } else if (ddt_bias) {
+      ddt_bias[i - int64_t(D) * (N + 1)] = float(s);
+    }
+  }
+}
+
+ScanDims dims_of(const ScanArgs& a) {
+  ScanDims d{};
+  d.B = a.B; d.T = a.T; d.D = a.D; d.G = a.G;
+  d.Dg = a.D / a.G;
+  d.tiles = (d.Dg + kLanes - 1) / kLanes;
+  d.x_row = a.x_row; d.dt_row = a.dt_row; d.z_row = a.z_row; d.b_row = a.b_row; d.c_row = a.c_row;
+  return d;
+}
+
+template <typename IO>
+ScanIn<IO> inputs_of(const ScanArgs& a) {
+  return {static_cast<const IO*>(a.x), static_cast<const IO*>(a.dt), a.A, static_cast<const IO*>(a.Bm), static_cast<const IO*>(a.Cm),
+          a.Dskip, a.dt_bias, static_cast<const IO*>(a.z), a.S0, a.lengths};
+}
+
+constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
+
+template <typename IO, int N, bool SP>
+hipError_t fwd_typed(const ScanArgs& a, float* S_T, float* states, hipStream_t st) {
+  const ScanDims d = dims_of(a);
+  const int64_t waves = int64_t(a.B) * a.G * d.tiles;
+  if (waves > kMaxGrid) return hipErrorInvalidValue;
+  scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), static_cast<IO*>(a.y), S_T, states);
+  return hipGetLastError();
+}
+
+template <typename IO, int N, bool SP>
+hipError_t step_typed(const ScanArgs& a, hipStream_t st) {
+  const int64_t blocks = (int64_t(a.B) * a.D * (N / 4) + 255) / 256;
+  if (blocks > kMaxGrid) return hipErrorInvalidValue;
+  scan_step_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(256), 0, st>>>(dims_of(a), inputs_of<IO>(a), a.S, a.is_first,
+                                                                           static_cast<IO*>(a.y));
+  return hipGetLastError();
+}
+
+int64_t states_floats(const ScanArgs& a) { return int64_t(a.B) * a.T * a.D * a.N; }
+int64_t bc_floats(const ScanArgs& a) { return int64_t(a.B) * a.T * a.G * dims_of(a).tiles * 2 * a.N; }
+int64_t params_floats(const ScanArgs& a) { return int64_t(a.B) * a.D * (a.N + 2); }
+
+template <typename IO, typename DY, int N, bool SP>
+hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
+  const ScanDims d = dims_of(a);
+  const int64_t waves = int64_t(a.B) * a.G * d.tiles;
+  float* states = a.workspace;
+  float* bc = states + states_floats(a);
+  float* par = bc + bc_floats(a);
+  hipError_t e = hipSuccess;
+  if (waves > 0) {
+    e = fwd_typed<IO, N, SP>(a, nullptr, states, st);
+    if (e != hipSuccess) return e;
+    scan_bwd_kernel<IO, DY, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), static_cast<const DY*>(a.dy), a.dS_T,
+                                                                              states, a.dx, a.ddt, a.dz, a.dS0, bc, par);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  const int64_t n = int64_t(a.B) * a.T * a.G * 2 * N;
+  if (n > 0) {
+    scan_bc_kernel<<<dim3(unsigned(std::min<int64_t>((n + 255) / 256, 1 << 16))), dim3(256), 0, st>>>(bc, d.tiles, N, n, a.dB, a.dC);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  scan_params_kernel<<<dim3(unsigned(std::min<int64_t>((int64_t(a.D) * (N + 2) + 255) / 256, 1 << 16))), dim3(256), 0, st>>>(
+      par, a.B, a.D, N, a.dA, a.dD, a.ddt_bias);
+  return hipGetLastError();
+}
+
+// Calls go(N, softplus) with compile-time values.
+template <typename Go>
+hipError_t by_size(const ScanArgs& a, Go go) {
+  auto sp = [&](auto n) { return a.softplus ? go(n, std::true_type{}) : go(n, std::false_type{}); };
+  switch (a.N) {
+    case 8: return sp(std::integral_constant<int, 8>{});
+    case 16: return sp(std::integral_constant<int, 16>{});
+    case 32: return sp(std::integral_constant<int, 32>{});
+    default: return sp(std::integral_constant<int, 64>{});
+  }
+}
+
+}  // namespace
+
+size_t scan_workspace_bytes(const ScanArgs&) { return 0; }
+
+hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st) {
+  if (a.T == 0) return launch_state_copy(a.S0, a.S_T, int64_t(a.B) * a.D * a.N, st);
+  return by_size(a, [&](auto n, auto sp) {
+    return a.bf16 ? fwd_typed<bf16_t, n(), sp()>(a, a.S_T, nullptr, st) : fwd_typed<float, n(), sp()>(a, a.S_T, nullptr, st);
+  });
+}
+
+hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st) {
+  return by_size(a, [&](auto n, auto sp) {
+    return a.bf16 ? step_typed<bf16_t, n(), sp()>(a, st) : step_typed<float, n(), sp()>(a, st);
+  });
+}
+
+size_t scan_bwd_workspace_bytes(const ScanArgs& a) {
+  return size_t(states_floats(a) + bc_floats(a) + params_floats(a)) * sizeof(float);
+}
+
+hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st) {
+  return by_size(a, [&](auto n, auto sp) {
+    if (a.bf16) return a.dy_bf16 ? bwd_typed<bf16_t, bf16_t, n(), sp()>(a, st) : bwd_typed<bf16_t, float, n(), sp()>(a, st);
+    return a.dy_bf16 ? bwd_typed<float, bf16_t, n(), sp()>(a, st) : bwd_typed<float, float, n(), sp()>(a, st);
+  });
+}
+
+}  // namespace falcon

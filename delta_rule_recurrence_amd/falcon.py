@@ -30,6 +30,25 @@ class FalconProblem(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("eps_gamma", ctypes.c_float)]
 
 
+class FalconConvProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32), ("W", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("x_row", ctypes.c_int64)]
+
+
+class FalconNormProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("G", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("center", ctypes.c_int32),
+                ("x_heads", ctypes.c_int32), ("y_heads", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("x_row", ctypes.c_int64)]
+
+
+class FalconScanProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("G", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("softplus", ctypes.c_int32),
+                ("x_row", ctypes.c_int64), ("dt_row", ctypes.c_int64), ("z_row", ctypes.c_int64),
+                ("b_row", ctypes.c_int64), ("c_row", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "falcon_abi_version": (ctypes.c_int32, []),
@@ -48,6 +67,21 @@ _SIGNATURES = {
     "falcon_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconProblem)]),
     "falcon_bwd_chunked": (ctypes.c_int32, [ctypes.POINTER(FalconProblem)] + [_P] * 17
                            + [ctypes.c_size_t, _P]),
+    "falcon_conv_fwd": (ctypes.c_int32, [ctypes.POINTER(FalconConvProblem)] + [_P] * 8),
+    "falcon_conv_step": (ctypes.c_int32, [ctypes.POINTER(FalconConvProblem)] + [_P] * 7),
+    "falcon_conv_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconConvProblem)]),
+    "falcon_conv_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconConvProblem)] + [_P] * 6 + [ctypes.c_int32]
+                        + [_P] * 6 + [ctypes.c_size_t, _P]),
+    "falcon_norm_fwd": (ctypes.c_int32, [ctypes.POINTER(FalconNormProblem)] + [_P] * 5),
+    "falcon_norm_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconNormProblem)]),
+    "falcon_norm_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconNormProblem)] + [_P] * 4 + [ctypes.c_int32]
+                        + [_P] * 4 + [ctypes.c_size_t, _P]),
+    "falcon_scan_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconScanProblem)]),
+    "falcon_scan_fwd": (ctypes.c_int32, [ctypes.POINTER(FalconScanProblem)] + [_P] * 13 + [ctypes.c_size_t, _P]),
+    "falcon_scan_step": (ctypes.c_int32, [ctypes.POINTER(FalconScanProblem)] + [_P] * 12),
+    "falcon_scan_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconScanProblem)]),
+    "falcon_scan_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconScanProblem)] + [_P] * 11 + [ctypes.c_int32]
+                        + [_P] * 11 + [ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -331,4 +365,402 @@ def falcon_bwd_chunked(phi_k, phi_q, v, beta, lam, dO, *, S0=None, k_prev=None, 
         _ptr(k_prev), _ptr(dO), _ptr(dS_T), _ptr(g["dphi_k"]), _ptr(g["dphi_q"]), _ptr(g["dv"]),
         _ptr(g["dbeta"]), _ptr(g["dlam"]), _ptr(g["dS0"]), _ptr(g["dk_prev"]), _ptr(workspace),
         wbytes, _stream(stream)))
+    return g
+
+
+# ---- around the recurrence: short convolution, group norm, selective scan ------
+#
+# Channels-last "rows" inputs ([B, T, width], or [B, width] for single tokens)
+# may be some of the columns of a wider contiguous projection; everything else
+# is contiguous.  The calls run on ``stream`` (default: the current stream of
+# the inputs' device); what they allocate belongs to that stream.
+
+ACTIVATIONS = {"none": 0, "silu": 1, "elu1": 2}
+_LAYOUTS = ("rows", "heads")
+_F32 = (torch.float32,)
+
+
+def _row_step(t, name, shape, dtype, device, tail=1):
+    """Checks a rows tensor ([..., width], the last ``tail`` axes dense) and
+    returns the elements from one row to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    width = 1
+    for size in shape[len(shape) - tail:]:
+        width *= size
+    if t.is_contiguous():
+        return width
+    stride = t.stride()
+    lead = len(shape) - tail
+    dense = 1
+    for axis in range(len(shape) - 1, lead - 1, -1):
+        if shape[axis] != 1 and stride[axis] != dense:
+            raise ValueError(f"{name}: the last {tail} axes must be dense")
+        dense *= shape[axis]
+    # rows one step apart: every leading axis continues the one below it
+    row = next((stride[axis] // _count(shape[axis + 1:lead]) for axis in range(lead) if shape[axis] != 1), width)
+    for axis in range(lead):
+        if shape[axis] != 1 and stride[axis] != row * _count(shape[axis + 1:lead]):
+            raise ValueError(f"{name}: rows must be evenly spaced (columns of one contiguous projection)")
+    if row < width:
+        raise ValueError(f"{name}: rows overlap")
+    return row
+
+
+def _count(sizes):
+    n = 1
+    for size in sizes:
+        n *= size
+    return n
+
+
+def _activation(name, allowed):
+    if name not in allowed:
+        raise ValueError(f"unknown activation {name!r}: expected one of {sorted(allowed)}")
+    return ACTIVATIONS[name]
+
+
+class _on_stream:
+    """The device and stream of one call: allocations and the launch use them."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("expected a device tensor")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream: on {stream.device}, the inputs are on {device}")
+        self._device = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self._stream = torch.cuda.stream(stream) if stream is not None else None
+        self._of = device
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self._of).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+        return False
+
+
+def _ref(t):
+    """Address of a checked tensor, or NULL."""
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _workspace(given, need, device):
+    """The given workspace or a new one, and its size."""
+    if need == ctypes.c_size_t(-1).value:
+        raise FalconError(-2)
+    _expect_bytes(given, "workspace", need, device)
+    if given is None and need > 0:
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    return given, (0 if given is None else given.numel() * given.element_size())
+
+
+def _new(shape, dtype, device, lengths=None):
+    """An output; zeros behind the sequences' ends, which calls leave alone."""
+    return (torch.empty if lengths is None else torch.zeros)(shape, dtype=dtype, device=device)
+
+
+def _grads(given, shapes, device):
+    """Checked gradients by name; those not given are allocated by the caller."""
+    g = dict(given or {})
+    unknown = set(g) - set(shapes)
+    if unknown:
+        raise ValueError(f"grads: unknown names {sorted(unknown)}")
+    for name, shape in shapes.items():
+        _expect(g.get(name), f"grads[{name!r}]", shape, _F32, device, optional=True)
+    return g
+
+
+def _dy_dtype(dy, shape, device):
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError(f"dy: expected a torch.Tensor, got {type(dy).__name__}")
+    _expect(dy, "dy", shape, tuple(DTYPES), device)
+    return DTYPES[dy.dtype]
+
+
+def _conv_setup(x, weight, bias, activation, dims):
+    act = _activation(activation, ("none", "silu"))
+    if not isinstance(x, torch.Tensor) or x.dim() != dims:
+        raise ValueError("x: expected a [B, T, C] tensor" if dims == 3 else "x: expected a [B, C] tensor")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight: expected a [C, W] tensor")
+    io, dev, C, W = _io_dtype(x, "x"), x.device, x.shape[-1], weight.shape[1]
+    _expect(weight, "weight", (C, W), _F32, dev)
+    _expect(bias, "bias", (C,), _F32, dev, optional=True)
+    row = _row_step(x, "x", x.shape, io, dev)
+    T = x.shape[1] if dims == 3 else 1
+    return io, dev, W, FalconConvProblem(x.shape[0], T, C, W, DTYPES[io], act, row)
+
+
+def falcon_conv_fwd(x, weight, bias=None, *, activation="silu", state=None, lengths=None, y=None,
+                    state_out=None, return_state=False, stream=None):
+    """Short causal convolution of ``x [B, T, C]`` with ``weight [C, W]``
+    (W in 2, 3, 4) and an activation ("silu" or "none"); returns
+    ``(y, state_out)``.
+
+    ``state`` holds the W - 1 rows before the first token (``[B, W - 1, C]``,
+    default zero); ``state_out`` (given, or allocated with ``return_state``)
+    gets the last W - 1 up to each sequence's end.  ``lengths`` (``[B]`` int32)
+    marks padded sequences: rows of ``y`` behind the end stay as they were, or
+    zero when ``y`` is allocated here.
+    """
+    io, dev, W, p = _conv_setup(x, weight, bias, activation, 3)
+    B, T, C = x.shape
+    _expect(state, "state", (B, W - 1, C), (io,), dev, optional=True)
+    _expect(lengths, "lengths", (B,), (torch.int32,), dev, optional=True)
+    _expect(y, "y", (B, T, C), (io,), dev, optional=True)
+    _expect(state_out, "state_out", (B, W - 1, C), (io,), dev, optional=True)
+    with _on_stream(dev, stream) as st:
+        if y is None:
+            y = _new((B, T, C), io, dev, lengths)
+        if state_out is None and return_state:
+            state_out = torch.empty((B, W - 1, C), dtype=io, device=dev)
+        _check(load_library().falcon_conv_fwd(ctypes.byref(p), _ref(x), _ref(weight), _ref(bias), _ref(state),
+                                              _ref(lengths), _ref(y), _ref(state_out), st))
+    return y, state_out
+
+
+def falcon_conv_step(x, weight, state, bias=None, *, activation="silu", is_first=None, y=None, stream=None):
+    """One token ``x [B, C]`` of every sequence; moves ``state [B, W - 1, C]``
+    on in place and returns ``y [B, C]``.  ``is_first`` (``[B]`` bytes) marks
+    sequences whose earlier rows count as zero."""
+    io, dev, W, p = _conv_setup(x, weight, bias, activation, 2)
+    B, C = x.shape
+    _expect(state, "state", (B, W - 1, C), (io,), dev)
+    _expect(is_first, "is_first", (B,), (torch.uint8, torch.bool), dev, optional=True)
+    _expect(y, "y", (B, C), (io,), dev, optional=True)
+    with _on_stream(dev, stream) as st:
+        if y is None:
+            y = torch.empty((B, C), dtype=io, device=dev)
+        _check(load_library().falcon_conv_step(ctypes.byref(p), _ref(x), _ref(weight), _ref(bias), _ref(state),
+                                               _ref(is_first), _ref(y), st))
+    return y
+
+
+def falcon_conv_bwd_workspace_bytes(problem: FalconConvProblem) -> int:
+    return int(load_library().falcon_conv_bwd_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_conv_bwd(x, weight, dy, bias=None, *, activation="silu", state=None, lengths=None, dstate_out=None,
+                    grads=None, workspace=None, stream=None):
+    """Gradients of ``<dy, y> + <dstate_out, state_out>``: a dict of float32
+    tensors dx (zero behind the sequences' ends), dweight, dbias (None without
+    a bias) and dstate (None without a state, unless ``grads`` holds one)."""
+    io, dev, W, p = _conv_setup(x, weight, bias, activation, 3)
+    B, T, C = x.shape
+    _expect(state, "state", (B, W - 1, C), (io,), dev, optional=True)
+    _expect(lengths, "lengths", (B,), (torch.int32,), dev, optional=True)
+    _expect(dstate_out, "dstate_out", (B, W - 1, C), _F32, dev, optional=True)
+    dy_dtype = _dy_dtype(dy, (B, T, C), dev)
+    shapes = {"dx": (B, T, C), "dweight": (C, W), "dbias": (C,), "dstate": (B, W - 1, C)}
+    g = _grads(grads, shapes, dev)
+    need = falcon_conv_bwd_workspace_bytes(p)
+    wanted = {"dx": True, "dweight": True, "dbias": bias is not None, "dstate": state is not None}
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    with _on_stream(dev, stream) as st:
+        for name, shape in shapes.items():
+            if g.get(name) is None:
+                g[name] = torch.empty(shape, dtype=torch.float32, device=dev) if wanted[name] else None
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_conv_bwd(
+            ctypes.byref(p), _ref(x), _ref(weight), _ref(bias), _ref(state), _ref(lengths), _ref(dy), dy_dtype,
+            _ref(dstate_out), _ref(g["dx"]), _ref(g["dweight"]), _ref(g["dbias"]), _ref(g["dstate"]),
+            _ref(workspace), have, st))
+    return g
+
+
+def _norm_setup(x, groups, weight, bias, center, activation, eps, scale, x_layout, y_layout):
+    act = _activation(activation, tuple(ACTIVATIONS))
+    for name, layout in (("x_layout", x_layout), ("y_layout", y_layout)):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"{name}: expected \"rows\" or \"heads\", got {layout!r}")
+    heads = x_layout == "heads"
+    if not isinstance(x, torch.Tensor) or x.dim() != (4 if heads else 3):
+        raise ValueError("x: expected a [B, G, T, d] tensor" if heads else "x: expected a [B, T, C] tensor")
+    G = int(groups)
+    if G < 1 or (x.shape[1] != G if heads else x.shape[2] % G != 0):
+        raise ValueError(f"groups: {groups} does not divide x of shape {tuple(x.shape)}")
+    io, dev = _io_dtype(x, "x"), x.device
+    B, T = x.shape[0], x.shape[2] if heads else x.shape[1]
+    d = x.shape[3] if heads else x.shape[2] // G
+    if heads:
+        _expect(x, "x", (B, G, T, d), (io,), dev)
+    row = G * d if heads else _row_step(x, "x", x.shape, io, dev)
+    _expect(weight, "weight", (G * d,), _F32, dev, optional=True)
+    _expect(bias, "bias", (G * d,), _F32, dev, optional=True)
+    rows, by_head = (B, T, G * d), (B, G, T, d)
+    p = FalconNormProblem(B, T, G, d, DTYPES[io], act, int(bool(center)), int(heads), int(y_layout == "heads"),
+                          eps, scale, row)
+    return io, dev, p, (by_head if y_layout == "heads" else rows)
+
+
+def falcon_norm_fwd(x, groups, weight=None, bias=None, *, center=False, activation="none", eps=1e-6, scale=1.0,
+                    x_layout="rows", y_layout="rows", y=None, stream=None):
+    """Group norm with an activation, a token's group (head) of d channels at a
+    time: ``scale * f(weight * xhat + bias)``, with ``xhat`` the group over its
+    root mean square (``center``: less its mean, over its deviation).
+
+    ``x`` and ``y`` are ``[B, T, G d]`` ("rows") or ``[B, G, T, d]`` ("heads",
+    the layout of the recurrences); ``activation`` is "none", "silu" or "elu1"
+    (elu + 1, a positive feature map); ``weight`` and ``bias`` are ``[G d]``.
+    """
+    io, dev, p, y_shape = _norm_setup(x, groups, weight, bias, center, activation, eps, scale, x_layout, y_layout)
+    _expect(y, "y", y_shape, (io,), dev, optional=True)
+    with _on_stream(dev, stream) as st:
+        if y is None:
+            y = torch.empty(y_shape, dtype=io, device=dev)
+        _check(load_library().falcon_norm_fwd(ctypes.byref(p), _ref(x), _ref(weight), _ref(bias), _ref(y), st))
+    return y
+
+
+def falcon_norm_bwd_workspace_bytes(problem: FalconNormProblem) -> int:
+    return int(load_library().falcon_norm_bwd_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_norm_bwd(x, groups, dy, weight=None, bias=None, *, center=False, activation="none", eps=1e-6, scale=1.0,
+                    x_layout="rows", y_layout="rows", grads=None, workspace=None, stream=None):
+    """Gradients of ``<dy, y>``: a dict of float32 tensors dx (x's layout),
+    dweight and dbias (None where weight or bias is None, unless ``grads``
+    holds them).  ``dy`` has y's layout."""
+    io, dev, p, y_shape = _norm_setup(x, groups, weight, bias, center, activation, eps, scale, x_layout, y_layout)
+    dy_dtype = _dy_dtype(dy, y_shape, dev)
+    C = p.G * p.d
+    shapes = {"dx": tuple(x.shape), "dweight": (C,), "dbias": (C,)}
+    g = _grads(grads, shapes, dev)
+    need = falcon_norm_bwd_workspace_bytes(p)
+    wanted = {"dx": True, "dweight": weight is not None, "dbias": bias is not None}
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    with _on_stream(dev, stream) as st:
+        for name, shape in shapes.items():
+            if g.get(name) is None:
+                g[name] = torch.empty(shape, dtype=torch.float32, device=dev) if wanted[name] else None
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_norm_bwd(
+            ctypes.byref(p), _ref(x), _ref(weight), _ref(bias), _ref(dy), dy_dtype, _ref(g["dx"]),
+            _ref(g["dweight"]), _ref(g["dbias"]), _ref(workspace), have, st))
+    return g
+
+
+def _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, dims):
+    if not isinstance(x, torch.Tensor) or x.dim() != dims:
+        raise ValueError("x: expected a [B, T, D] tensor" if dims == 3 else "x: expected a [B, D] tensor")
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A: expected a [D, N] tensor")
+    if not isinstance(B, torch.Tensor) or B.dim() != dims + 1:
+        raise ValueError("B: expected a [B, T, G, N] tensor" if dims == 3 else "B: expected a [B, G, N] tensor")
+    io, dev, width, N, G = _io_dtype(x, "x"), x.device, x.shape[-1], A.shape[1], B.shape[-2]
+    _expect(A, "A", (width, N), _F32, dev)
+    _expect(D, "D", (width,), _F32, dev, optional=True)
+    _expect(dt_bias, "dt_bias", (width,), _F32, dev, optional=True)
+    shared = tuple(x.shape[:-1]) + (G, N)
+    rows = [_row_step(x, "x", x.shape, io, dev), _row_step(dt, "dt", x.shape, io, dev),
+            _row_step(z, "z", x.shape, io, dev) if z is not None else width,
+            _row_step(B, "B", shared, io, dev, 2), _row_step(C, "C", shared, io, dev, 2)]
+    p = FalconScanProblem(x.shape[0], x.shape[1] if dims == 3 else 1, width, N, G, DTYPES[io], int(bool(softplus)), *rows)
+    return io, dev, p
+
+
+def falcon_scan_workspace_bytes(problem: FalconScanProblem) -> int:
+    return int(load_library().falcon_scan_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_scan_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, z=None, S0=None, lengths=None, y=None,
+                    S_T=None, workspace=None, return_state=True, stream=None):
+    """Selective state space scan of ``x, dt [B, T, D]`` with ``A [D, N]``
+    (N in 8, 16, 32, 64) and ``B, C [B, T, G, N]``; returns ``(y, S_T)``.
+
+    ``S_t = exp(delta_t A) S_(t-1) + delta_t x_t B_t`` and
+    ``y_t = (<C_t, S_t> + D x_t) silu(z_t)``, with ``delta = softplus(dt +
+    dt_bias)`` (or without the softplus) and the gate only where ``z`` is given.
+    ``S0`` and ``S_T`` are ``[B, D, N]`` float32; ``lengths`` (``[B]`` int32)
+    marks padded sequences: ``S_T`` is the state at the end, rows of ``y``
+    behind it stay as they were, or zero when ``y`` is allocated here.
+    """
+    io, dev, p = _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, 3)
+    nb, T, width = x.shape
+    state = (nb, width, p.N)
+    _expect(S0, "S0", state, _F32, dev, optional=True)
+    _expect(lengths, "lengths", (nb,), (torch.int32,), dev, optional=True)
+    _expect(y, "y", (nb, T, width), (io,), dev, optional=True)
+    _expect(S_T, "S_T", state, _F32, dev, optional=True)
+    need = falcon_scan_workspace_bytes(p)
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    with _on_stream(dev, stream) as st:
+        if y is None:
+            y = _new((nb, T, width), io, dev, lengths)
+        if S_T is None and return_state:
+            S_T = torch.empty(state, dtype=torch.float32, device=dev)
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_scan_fwd(
+            ctypes.byref(p), _ref(x), _ref(dt), _ref(A), _ref(B), _ref(C), _ref(D), _ref(dt_bias), _ref(z), _ref(S0),
+            _ref(lengths), _ref(y), _ref(S_T), _ref(workspace), have, st))
+    return y, S_T
+
+
+def falcon_scan_step(x, dt, A, B, C, S, *, D=None, dt_bias=None, softplus=True, z=None, is_first=None, y=None,
+                     stream=None):
+    """One token of every sequence (``x, dt, z [B, D]``, ``B, C [B, G, N]``);
+    moves ``S [B, D, N]`` on in place and returns ``y [B, D]``.  ``is_first``
+    (``[B]`` bytes) marks sequences whose state so far counts as zero."""
+    io, dev, p = _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, 2)
+    nb, width = x.shape
+    _expect(S, "S", (nb, width, p.N), _F32, dev)
+    _expect(is_first, "is_first", (nb,), (torch.uint8, torch.bool), dev, optional=True)
+    _expect(y, "y", (nb, width), (io,), dev, optional=True)
+    with _on_stream(dev, stream) as st:
+        if y is None:
+            y = torch.empty((nb, width), dtype=io, device=dev)
+        _check(load_library().falcon_scan_step(
+            ctypes.byref(p), _ref(x), _ref(dt), _ref(A), _ref(B), _ref(C), _ref(D), _ref(dt_bias), _ref(z), _ref(S),
+            _ref(is_first), _ref(y), st))
+    return y
+
+
+def falcon_scan_bwd_workspace_bytes(problem: FalconScanProblem) -> int:
+    return int(load_library().falcon_scan_bwd_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_scan_bwd(x, dt, A, B, C, dy, *, D=None, dt_bias=None, softplus=True, z=None, S0=None, lengths=None,
+                    dS_T=None, grads=None, workspace=None, stream=None):
+    """Gradients of ``<dy, y> + <dS_T, S_T>``: a dict of float32 tensors dx,
+    ddt, dA, dB, dC, dD, ddt_bias, dz and dS0; dD, ddt_bias, dz and dS0 are
+    None where D, dt_bias, z or S0 is None (all but dz may still be asked for
+    through ``grads``).  Rows behind the sequences' ends get zero."""
+    io, dev, p = _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, 3)
+    nb, T, width = x.shape
+    state, shared = (nb, width, p.N), (nb, T, p.G, p.N)
+    _expect(S0, "S0", state, _F32, dev, optional=True)
+    _expect(lengths, "lengths", (nb,), (torch.int32,), dev, optional=True)
+    _expect(dS_T, "dS_T", state, _F32, dev, optional=True)
+    dy_dtype = _dy_dtype(dy, (nb, T, width), dev)
+    shapes = {"dx": (nb, T, width), "ddt": (nb, T, width), "dz": (nb, T, width), "dA": (width, p.N), "dB": shared,
+              "dC": shared, "dD": (width,), "ddt_bias": (width,), "dS0": state}
+    g = _grads(grads, shapes, dev)
+    if z is None and g.get("dz") is not None:
+        raise ValueError("grads['dz']: there is no z")
+    missing = {"dz": z is None, "dD": D is None, "ddt_bias": dt_bias is None, "dS0": S0 is None}
+    need = falcon_scan_bwd_workspace_bytes(p)
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    with _on_stream(dev, stream) as st:
+        for name, shape in shapes.items():
+            if g.get(name) is None:
+                g[name] = None if missing.get(name) else torch.empty(shape, dtype=torch.float32, device=dev)
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_scan_bwd(
+            ctypes.byref(p), _ref(x), _ref(dt), _ref(A), _ref(B), _ref(C), _ref(D), _ref(dt_bias), _ref(z), _ref(S0),
+            _ref(lengths), _ref(dy), dy_dtype, _ref(dS_T), _ref(g["dx"]), _ref(g["ddt"]), _ref(g["dz"]), _ref(g["dA"]),
+            _ref(g["dB"]), _ref(g["dC"]), _ref(g["dD"]), _ref(g["ddt_bias"]), _ref(g["dS0"]), _ref(workspace), have, st))
     return g

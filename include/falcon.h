@@ -289,6 +289,218 @@ falcon_status falcon_bwd_chunked(const falcon_problem* p,
  * unsupported problem. */
 size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
 
+/*
+ * ---- around the recurrence ---------------------------------------------------
+ *
+ * What a fast-weight block runs before and after its recurrence, and the
+ * recurrence's sibling with a decay of its own for every channel and state:
+ *   falcon_conv_*  the short causal convolution of the projections;
+ *   falcon_norm_*  the group norm with an activation, a token's head at a time:
+ *                  it makes phi(k) and phi(q) in the [B, H, T, dk] layout that
+ *                  falcon_fwd_* read, and norms the [B, H, T, dv] outputs;
+ *   falcon_scan_*  the selective state space scan.
+ * Status codes, streams, the order of checks and launches and the absence of
+ * allocation are those of the entry points above.  Also:
+ *  - "Rows" tensors are channels last, [B, T, width].  Where a field *_row is
+ *    named for an input, row (b, t) starts at element (b T + t) *_row, so the
+ *    input may be some of the columns of a wider projection (*_row >= width);
+ *    every other tensor is contiguous.  Base pointers are 16-byte aligned.
+ *    An input's range, for the check of overlaps, runs from its first row's
+ *    first element to its last row's last one: columns of one projection may
+ *    interleave among inputs, but an output may not lie between them.
+ *  - lengths, [B] int32 or NULL, gives each sequence's number of tokens
+ *    (clamped to [0, T]).  Rows behind a sequence's end are never read.
+ *    Forward calls leave the output rows behind it as they were and take the
+ *    carried state at the end; backward calls write zero gradients there.
+ *  - Parameters (weights, biases, A, D) and states of the scan are float32;
+ *    gradients are float32.  Incoming gradients dy have dy_dtype, a
+ *    falcon_dtype of its own (falcon_bwd_chunked gives float32 ones).
+ *  - Sums over tokens (parameter gradients) are made in a fixed order: results
+ *    are the same from call to call.
+ */
+
+typedef enum {
+  FALCON_ACT_NONE = 0,  /* f(p) = p                                   */
+  FALCON_ACT_SILU = 1,  /* f(p) = p / (1 + exp(-p))                   */
+  FALCON_ACT_ELU1 = 2   /* f(p) = p + 1 for p > 0, exp(p) otherwise;
+                           falcon_norm_* only                         */
+} falcon_activation;
+
+/*
+ * falcon_conv_fwd -- the short causal convolution, a channel at a time:
+ *
+ *     y_t = f( bias + sum_{j < W} weight_j x_{t - (W - 1) + j} )
+ *
+ * where the rows before the first token are those of `state` (the last W - 1
+ * rows that came before, oldest first), or zero.
+ *
+ *  x          : [B, T, C] io dtype, rows of x_row elements.
+ *  weight     : [C, W] float32, W in {2, 3, 4}; the last tap is this token's.
+ *  bias       : [C] float32 or NULL for zero.
+ *  state      : [B, W - 1, C] io dtype, or NULL for zero rows.
+ *  y          : [B, T, C] io dtype.
+ *  state_out  : [B, W - 1, C] io dtype: the last W - 1 rows up to each
+ *               sequence's end (rows of `state` among them where it has fewer
+ *               tokens), to go on from; or NULL.  May not overlap `state`.
+ */
+typedef struct {
+  int32_t B, T, C, W;
+  int32_t io_dtype;     /* a falcon_dtype                     */
+  int32_t activation;   /* FALCON_ACT_NONE or FALCON_ACT_SILU */
+  int64_t x_row;        /* elements from one row of x to the next */
+} falcon_conv_problem;
+
+falcon_status falcon_conv_fwd(const falcon_conv_problem* p, const void* x, const float* weight,
+                              const float* bias, const void* state, const int32_t* lengths,
+                              void* y, void* state_out, hipStream_t stream);
+
+/*
+ * falcon_conv_step -- one token of every sequence.  p->T is ignored; x is
+ * [B, C] with rows of x_row, y is [B, C], and `state` ([B, W - 1, C] io dtype)
+ * moves on by this token IN PLACE.  is_first, [B] bytes or NULL: a nonzero
+ * entry marks a sequence whose rows before this token count as zero,
+ * whatever `state` holds.
+ */
+falcon_status falcon_conv_step(const falcon_conv_problem* p, const void* x, const float* weight,
+                               const float* bias, void* state, const uint8_t* is_first, void* y,
+                               hipStream_t stream);
+
+/*
+ * falcon_conv_bwd -- gradients of <dy, y> + <dstate_out, state_out>.
+ *  dy         : [B, T, C] dy_dtype.
+ *  dstate_out : [B, W - 1, C] float32, or NULL for zero.
+ *  dx         : [B, T, C] float32.
+ *  dweight    : [C, W] float32;  dbias : [C] float32, or NULL to skip.
+ *  dstate     : [B, W - 1, C] float32, the gradient of `state`, or NULL to
+ *               skip (it may be asked for where `state` is NULL, too).
+ *  workspace  : at least falcon_conv_bwd_workspace_bytes(p) bytes, 16-byte
+ *               aligned, overlapping nothing else.
+ */
+falcon_status falcon_conv_bwd(const falcon_conv_problem* p, const void* x, const float* weight,
+                              const float* bias, const void* state, const int32_t* lengths,
+                              const void* dy, int32_t dy_dtype, const float* dstate_out,
+                              float* dx, float* dweight, float* dbias, float* dstate,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Device scratch of falcon_conv_bwd; (size_t)-1 for an invalid problem. */
+size_t falcon_conv_bwd_workspace_bytes(const falcon_conv_problem* p);
+
+/*
+ * falcon_norm_fwd -- group norm with an activation.  Every token's C = G d
+ * channels are G groups (the heads) of d, and each group is normed by itself:
+ *
+ *     xhat = (x - mu) / sqrt( mean((x - mu)^2) + eps ),   mu = mean(x) if center, else 0
+ *     y    = scale f( weight xhat + bias )
+ *
+ * With center = 0 this is the root-mean-square norm (the paper's QK-RMSNorm),
+ * with f = FALCON_ACT_ELU1 a positive feature map phi.
+ *
+ *  x          : rows [B, T, C] of x_row elements, or heads [B, G, T, d]
+ *               (x_heads; contiguous, x_row is ignored), io dtype.
+ *  weight     : [C] float32, or NULL for one;  bias : [C] float32, or NULL.
+ *  y          : rows [B, T, C] or heads [B, G, T, d] (y_heads), contiguous.
+ *  1 <= d <= 4096.
+ */
+typedef struct {
+  int32_t B, T, G, d;
+  int32_t io_dtype;
+  int32_t activation;
+  int32_t center;             /* 0 or 1 */
+  int32_t x_heads, y_heads;   /* 0: rows, 1: heads */
+  float eps;                  /* >= 0, finite */
+  float scale;                /* finite */
+  int64_t x_row;
+} falcon_norm_problem;
+
+falcon_status falcon_norm_fwd(const falcon_norm_problem* p, const void* x, const float* weight,
+                              const float* bias, void* y, hipStream_t stream);
+
+/*
+ * falcon_norm_bwd -- gradients of <dy, y>.
+ *  dy         : dy_dtype, in y's layout;  dx : float32, contiguous, in x's.
+ *  dweight, dbias : [C] float32, or NULL to skip either (they may be asked for
+ *               where weight or bias is NULL, too).
+ *  workspace  : at least falcon_norm_bwd_workspace_bytes(p) bytes.
+ */
+falcon_status falcon_norm_bwd(const falcon_norm_problem* p, const void* x, const float* weight,
+                              const float* bias, const void* dy, int32_t dy_dtype, float* dx,
+                              float* dweight, float* dbias, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+size_t falcon_norm_bwd_workspace_bytes(const falcon_norm_problem* p);
+
+/*
+ * falcon_scan_fwd -- the selective state space scan.  Channel c of D, in group
+ * g = c / (D / G), has a state S of N numbers:
+ *
+ *     delta_t = softplus(dt_t + dt_bias), or dt_t + dt_bias
+ *     S_t     = exp(delta_t A_c) * S_{t-1} + delta_t x_t B_{t,g}
+ *     y_t     = ( <C_{t,g}, S_t> + D_c x_t ) silu(z_t)
+ *
+ * (products of vectors of N elementwise).  The read comes after the write.
+ *
+ *  x, dt, z   : [B, T, D] io dtype, rows of x_row, dt_row, z_row elements; z
+ *               may be NULL (no gate).
+ *  A          : [D, N] float32, N in {8, 16, 32, 64}.
+ *  Bm, Cm     : [B, T, G, N] io dtype, rows of b_row, c_row elements; G
+ *               divides D.
+ *  Dskip, dt_bias : [D] float32, or NULL for zero.
+ *  S0         : [B, D, N] float32, or NULL for zero.
+ *  y          : [B, T, D] io dtype.
+ *  S_T        : [B, D, N] float32, the state at each sequence's end, or NULL;
+ *               may alias S0 exactly.
+ *  workspace  : at least falcon_scan_workspace_bytes(p) bytes (may be NULL
+ *               when that is 0), 16-byte aligned, overlapping nothing else.
+ * Arithmetic is float32 throughout.
+ */
+typedef struct {
+  int32_t B, T, D, N, G;
+  int32_t io_dtype;
+  int32_t softplus;           /* 0 or 1 */
+  int64_t x_row, dt_row, z_row, b_row, c_row;
+} falcon_scan_problem;
+
+falcon_status falcon_scan_fwd(const falcon_scan_problem* p, const void* x, const void* dt,
+                              const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                              const float* dt_bias, const void* z, const float* S0,
+                              const int32_t* lengths, void* y, float* S_T, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+size_t falcon_scan_workspace_bytes(const falcon_scan_problem* p);
+
+/*
+ * falcon_scan_step -- one token of every sequence: x, dt, z, y are [B, D], Bm
+ * and Cm [B, G, N] (rows as above, p->T is ignored), S [B, D, N] float32 moves
+ * on IN PLACE.  is_first, [B] bytes or NULL: a nonzero entry marks a sequence
+ * whose state before this token counts as zero, whatever S holds.
+ */
+falcon_status falcon_scan_step(const falcon_scan_problem* p, const void* x, const void* dt,
+                               const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                               const float* dt_bias, const void* z, float* S,
+                               const uint8_t* is_first, void* y, hipStream_t stream);
+
+/*
+ * falcon_scan_bwd -- gradients of <dy, y> + <dS_T, S_T>; the forward is
+ * recomputed.
+ *  dy         : [B, T, D] dy_dtype;  dS_T : [B, D, N] float32 or NULL.
+ *  dx, ddt    : [B, T, D] float32;  dz : the same, required where z is given,
+ *               ignored where it is not.
+ *  dA         : [D, N] float32;  dB, dC : [B, T, G, N] float32, summed over
+ *               the channels of each group.
+ *  dD, ddt_bias : [D] float32, or NULL to skip.
+ *  dS0        : [B, D, N] float32, or NULL to skip.
+ *  workspace  : at least falcon_scan_bwd_workspace_bytes(p) bytes.
+ */
+falcon_status falcon_scan_bwd(const falcon_scan_problem* p, const void* x, const void* dt,
+                              const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                              const float* dt_bias, const void* z, const float* S0,
+                              const int32_t* lengths, const void* dy, int32_t dy_dtype,
+                              const float* dS_T, float* dx, float* ddt, float* dz, float* dA,
+                              float* dB, float* dC, float* dD, float* ddt_bias, float* dS0,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t falcon_scan_bwd_workspace_bytes(const falcon_scan_problem* p);
+
 #ifdef __cplusplus
 }
 #endif
