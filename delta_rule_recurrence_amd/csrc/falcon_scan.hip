@@ -9,10 +9,9 @@
 //   dC_t = sum_c q_t S_t,   dB_t = sum_c G_t delta_t x_t,   u_t = <G_t, B_t>,
 //   ddelta_t = <A, m_t> + u_t x_t,   dA = sum_t m_t delta_t,   dx_t = u_t delta_t + D q_t.
 //
-// A lane owns one channel and its N states; a wave 64 adjacent channels of one
-// group, so B_t and C_t are the same for all its lanes.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "falcon_block_device.h"
 #include "falcon_launch.h"
@@ -79,10 +78,223 @@ template <bool SOFTPLUS>
 __device__ __forceinline__ float step_of(float v) { return SOFTPLUS ? softplus_f32(v) : v; }
 
 // ---- prompts ----------------------------------------------------------------------
-// With `states` (the backward's recomputation) the state after every token goes
-// there ([B, T, D, N]) instead of the outputs.
+// A lane owns four states of one channel: S = N / 4 lanes a channel, 64 / S
+// channels a wave.  A wave takes kTok = 16 tokens at a time and a workgroup's
+// kWaves waves consecutive sixteens, so a sequence's tokens run in parallel:
+//   1. each wave scans its tokens from a zero state, the decays a_t kept in
+//      registers, which gives its map S -> P S + E (P = exp(A sum of delta));
+//   2. the maps meet in LDS, and each wave folds those before it onto the
+//      state that entered the workgroup's step;
+//   3. each wave scans again from there, with the same a_t, and reads.
+// The exponentials, which with the multiply-adds bound the scan (4 + 8 cycles a
+// wave for the argument and exp2, 4 for each of the others), are so computed
+// once.  What a token and a channel need once (step size, gate) is worked out by
+// one lane of a quad for every fourth token and handed round by quad permutes.
+constexpr int kTok = 16;
+
+template <int N>
+struct Lanes {
+  static constexpr int kPer = N / 4;                    // lanes a channel
+  static constexpr int kChannels = 64 / kPer;           // channels a wave
+  static constexpr int kQuad = kPer < 4 ? kPer : 4;     // lanes that share the tokens' work
+  static constexpr int kRegs = kTok / kQuad;            // tokens a lane works out
+};
+
+// Value of lane J of this lane's group of Q (2 or 4) lanes.
+template <int Q, int J>
+__device__ __forceinline__ float from_lane(float v) {
+  constexpr int kCtrl = Q == 4 ? J * 0x55 : (J | (J << 2) | ((2 + J) << 4) | ((2 + J) << 6));
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false));
+}
+
+// Four consecutive elements, in one access where `wide`.
+template <typename IO>
+__device__ __forceinline__ void load_four(const IO* p, bool wide, float (&v)[4]) {
+  if (wide) {
+    load_vec<IO, 4>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = io<IO>::load(p, i);
+  }
+}
+
+// The raw inputs of a wave's sixteen tokens, loaded a step ahead.
+template <typename IO, int N>
+struct Tokens {
+  static constexpr int kUnits = (kTok * N / 4 + 63) / 64;   // fours of B (and C) a lane loads
+  float x[Lanes<N>::kRegs], dt[Lanes<N>::kRegs], z[Lanes<N>::kRegs];
+  float b[kUnits][4], c[kUnits][4];
+};
+
+// Tokens behind the sequence's end are read as its last one (which exists) and
+// then count as no step at all: delta, x, B and C zero.
+template <typename IO, int N>
+__device__ __forceinline__ void load_tokens(const ScanDims& d, const ScanIn<IO>& in, int64_t b, int g, int c, int t0, int len,
+                                            bool wide, Tokens<IO, N>& k) {
+  using L = Lanes<N>;
+  const int lane = threadIdx.x % 64;
+#pragma unroll
+  for (int i = 0; i < L::kRegs; ++i) {
+    const int64_t token = b * d.T + min(t0 + L::kQuad * i + lane % L::kQuad, len - 1);
+    k.x[i] = io<IO>::load(in.x, token * d.x_row + c);
+    k.dt[i] = io<IO>::load(in.dt, token * d.dt_row + c);
+    if (in.z) k.z[i] = io<IO>::load(in.z, token * d.z_row + c);
+  }
+#pragma unroll
+  for (int u = 0; u < Tokens<IO, N>::kUnits; ++u) {
+    const int unit = min(u * 64 + lane, kTok * L::kPer - 1);
+    const int64_t token = b * d.T + min(t0 + unit / L::kPer, len - 1);
+    const int at = g * N + 4 * (unit % L::kPer);
+    load_four(in.Bm + token * d.b_row + at, wide, k.b[u]);
+    load_four(in.Cm + token * d.c_row + at, wide, k.c[u]);
+  }
+}
+
+// B and C of the wave's tokens to its part of LDS, [kTok][N] each.
+template <typename IO, int N>
+__device__ __forceinline__ void stage_shared(const Tokens<IO, N>& k, int t0, int len, float* Bs, float* Cs) {
+  using L = Lanes<N>;
+  const int lane = threadIdx.x % 64;
+#pragma unroll
+  for (int u = 0; u < Tokens<IO, N>::kUnits; ++u) {
+    const int unit = u * 64 + lane;
+    const bool live = t0 + unit / L::kPer < len;
+    if (kTok * L::kPer % 64 == 0 || unit < kTok * L::kPer) {
+      *reinterpret_cast<float4*>(Bs + 4 * unit) =
+          live ? make_float4(k.b[u][0], k.b[u][1], k.b[u][2], k.b[u][3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      *reinterpret_cast<float4*>(Cs + 4 * unit) =
+          live ? make_float4(k.c[u][0], k.c[u][1], k.c[u][2], k.c[u][3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  }
+}
+
+__device__ __forceinline__ void four(const float* p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+
+// f(t, j, i) for t = 0 .. 15 in order, with t = kQuad i + j known at compile time.
+template <int Q, int I = 0, typename F>
+__device__ __forceinline__ void each_token(F f) {
+  if constexpr (I < kTok) {
+    f(std::integral_constant<int, I>{}, std::integral_constant<int, I % Q>{}, std::integral_constant<int, I / Q>{});
+    if constexpr (I % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    each_token<Q, I + 1>(f);
+  }
+}
+
+// Workgroups b, b + 8, b + 16, ... run on one XCD: neighbours in channels, which
+// share cache lines of every row, follow one another there.
+__device__ __forceinline__ int64_t by_xcd(int64_t block, int64_t blocks) {
+  const int64_t each = blocks / 8, more = blocks % 8, x = block % 8;
+  return x * each + min(x, more) + block / 8;
+}
+
+constexpr int kFwdWaves = 4;
+
 template <typename IO, int N, bool SOFTPLUS>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanDims d, ScanIn<IO> in, IO* y, float* S_T, float* states) {
+__global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void scan_fwd_kernel(ScanDims d, ScanIn<IO> in, bool wide, IO* __restrict__ y,
+                                                                    float* __restrict__ S_T) {
+  using L = Lanes<N>;
+  __shared__ float shared[kFwdWaves][2][kTok * N];      // B, C
+  __shared__ float4 maps[2][kFwdWaves][2][64];          // by parity of the step: P, E
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int64_t id = by_xcd(blockIdx.x, gridDim.x);
+  const int tile = int(id % d.tiles), g = int(id / d.tiles % d.G);
+  const int64_t b = id / (int64_t(d.tiles) * d.G);
+  const int in_group = tile * L::kChannels + lane / L::kPer;
+  const bool on = in_group < d.Dg;
+  const int c = g * d.Dg + min(in_group, d.Dg - 1), s = lane % L::kPer, j = lane % L::kQuad;
+  const int len = tokens_of(in.lengths, int(b), d.T);
+  const int64_t at = (b * d.D + c) * N + 4 * s;
+  float H[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A2[4];
+  if (in.S0) four(in.S0 + at, H);
+  four(in.A + int64_t(c) * N + 4 * s, A2);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) A2[n] *= kLog2e;
+  const float skip = in.Dskip ? in.Dskip[c] : 0.0f, bias = in.dt_bias ? in.dt_bias[c] : 0.0f;
+  float* Bs = shared[wave][0];
+  float* Cs = shared[wave][1];
+
+  Tokens<IO, N> next;
+  if (len > 0) load_tokens<IO, N>(d, in, b, g, c, wave * kTok, len, wide, next);
+  int parity = 0;
+  for (int base = 0; base < len; base += kFwdWaves * kTok, parity ^= 1) {
+    const int t0 = base + wave * kTok;
+    float delta[L::kRegs], x[L::kRegs], gate[L::kRegs], u[L::kRegs], sum = 0.0f;
+    stage_shared<IO, N>(next, t0, len, Bs, Cs);
+#pragma unroll
+    for (int i = 0; i < L::kRegs; ++i) {
+      const bool live = t0 + L::kQuad * i + j < len;
+      x[i] = next.x[i];
+      delta[i] = live ? step_of<SOFTPLUS>(next.dt[i] + bias) : 0.0f;
+      u[i] = live ? delta[i] * x[i] : 0.0f;
+      gate[i] = in.z ? act_f32<kActSilu>(next.z[i]) : 1.0f;
+      sum += delta[i];
+    }
+    sum = lanes_sum<L::kQuad>(sum);
+    if (base + kFwdWaves * kTok < len) load_tokens<IO, N>(d, in, b, g, c, t0 + kFwdWaves * kTok, len, wide, next);
+    __builtin_amdgcn_wave_barrier();
+
+    // 1. the wave's map
+    float a[kTok][4], E[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    each_token<L::kQuad>([&](auto t, auto jj, auto i) {
+      const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
+      float bt[4];
+      four(Bs + t() * N + 4 * s, bt);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        a[t()][n] = __builtin_amdgcn_exp2f(dt * A2[n]);
+        E[n] = __builtin_fmaf(a[t()][n], E[n], ut * bt[n]);
+      }
+    });
+    maps[parity][wave][0][lane] = make_float4(__builtin_amdgcn_exp2f(sum * A2[0]), __builtin_amdgcn_exp2f(sum * A2[1]),
+                                              __builtin_amdgcn_exp2f(sum * A2[2]), __builtin_amdgcn_exp2f(sum * A2[3]));
+    maps[parity][wave][1][lane] = make_float4(E[0], E[1], E[2], E[3]);
+    __syncthreads();
+    // 2. the state that enters the wave's tokens, and the one that leaves the step
+    float h[4] = {H[0], H[1], H[2], H[3]};
+#pragma unroll
+    for (int w = 0; w < kFwdWaves; ++w) {
+      if (w == wave) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) h[n] = H[n];
+      }
+      float Pw[4], Ew[4];
+      four(reinterpret_cast<const float*>(&maps[parity][w][0][lane]), Pw);
+      four(reinterpret_cast<const float*>(&maps[parity][w][1][lane]), Ew);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) H[n] = __builtin_fmaf(Pw[n], H[n], Ew[n]);
+    }
+    // 3. the scan from there, and the reads
+    float read[L::kRegs];
+    each_token<L::kQuad>([&](auto t, auto jj, auto i) {
+      const float ut = from_lane<L::kQuad, jj()>(u[i()]);
+      float bt[4], ct[4], r = 0.0f;
+      four(Bs + t() * N + 4 * s, bt);
+      four(Cs + t() * N + 4 * s, ct);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        h[n] = __builtin_fmaf(a[t()][n], h[n], ut * bt[n]);
+        r = __builtin_fmaf(ct[n], h[n], r);
+      }
+      r = lanes_sum<L::kPer>(r);
+      read[i()] = jj() == 0 || j == jj() ? r : read[i()];
+    });
+#pragma unroll
+    for (int i = 0; i < L::kRegs; ++i) {
+      const int t = t0 + L::kQuad * i + j;
+      if (on && s < L::kQuad && t < len)
+        io<IO>::store(y, (b * d.T + t) * d.D + c, __builtin_fmaf(skip, x[i], read[i]) * gate[i]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (S_T && wave == 0 && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(H[0], H[1], H[2], H[3]);
+}
+
+// Every state, one token after another: [B, T, D, N], for the gradients.
+template <typename IO, int N, bool SOFTPLUS>
+__global__ __launch_bounds__(64) void scan_states_kernel(ScanDims d, ScanIn<IO> in, float* states) {
   const Place p = place_of(d, blockIdx.x);
   const int len = tokens_of(in.lengths, p.b, d.T);
   const int64_t at = (int64_t(p.b) * d.D + p.c) * N;
@@ -96,28 +308,17 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanDims d, ScanIn<IO> in,
 #pragma unroll
     for (int n = 0; n < N; ++n) S[n] = 0.0f;
   }
-  const float skip = in.Dskip ? in.Dskip[p.c] : 0.0f, bias = in.dt_bias ? in.dt_bias[p.c] : 0.0f;
+  const float bias = in.dt_bias ? in.dt_bias[p.c] : 0.0f;
   for (int t = 0; t < len; ++t) {
     const int64_t token = int64_t(p.b) * d.T + t;
     const float x = io<IO>::load(in.x, token * d.x_row + p.c);
     const float delta = step_of<SOFTPLUS>(io<IO>::load(in.dt, token * d.dt_row + p.c) + bias);
     const IO* pb = in.Bm + token * d.b_row + p.g * N;
-    const IO* pc = in.Cm + token * d.c_row + p.g * N;
     const float u = delta * x;
-    float read = skip * x;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      S[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), S[n], u * io<IO>::load(pb, n));
-      read = __builtin_fmaf(io<IO>::load(pc, n), S[n], read);
-    }
-    if (states) {
-      if (p.on) store_state<N>(states + (token * d.D + p.c) * N, S);
-    } else if (p.on) {
-      if (in.z) read *= act_f32<kActSilu>(io<IO>::load(in.z, token * d.z_row + p.c));
-      io<IO>::store(y, token * d.D + p.c, read);
-    }
+    for (int n = 0; n < N; ++n) S[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), S[n], u * io<IO>::load(pb, n));
+    if (p.on) store_state<N>(states + (token * d.D + p.c) * N, S);
   }
-  if (S_T && p.on) store_state<N>(S_T + at, S);
 }
 
 // ---- one token --------------------------------------------------------------------
@@ -295,12 +496,17 @@ ScanIn<IO> inputs_of(const ScanArgs& a) {
 
 constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
 
+// Fours of B and C lie on multiples of a four's size.
+bool fours_wide(const ScanArgs& a) { return a.b_row % 4 == 0 && a.c_row % 4 == 0; }
+
 template <typename IO, int N, bool SP>
-hipError_t fwd_typed(const ScanArgs& a, float* S_T, float* states, hipStream_t st) {
-  const ScanDims d = dims_of(a);
-  const int64_t waves = int64_t(a.B) * a.G * d.tiles;
-  if (waves > kMaxGrid) return hipErrorInvalidValue;
-  scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), static_cast<IO*>(a.y), S_T, states);
+hipError_t fwd_typed(const ScanArgs& a, hipStream_t st) {
+  ScanDims d = dims_of(a);
+  d.tiles = (d.Dg + Lanes<N>::kChannels - 1) / Lanes<N>::kChannels;
+  const int64_t blocks = int64_t(a.B) * a.G * d.tiles;
+  if (blocks > kMaxGrid) return hipErrorInvalidValue;
+  scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kFwdWaves), 0, st>>>(d, inputs_of<IO>(a), fours_wide(a),
+                                                                                     static_cast<IO*>(a.y), a.S_T);
   return hipGetLastError();
 }
 
@@ -325,9 +531,9 @@ hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
   float* bc = states + states_floats(a);
   float* par = bc + bc_floats(a);
   hipError_t e = hipSuccess;
+  if (waves > kMaxGrid) return hipErrorInvalidValue;
   if (waves > 0) {
-    e = fwd_typed<IO, N, SP>(a, nullptr, states, st);
-    if (e != hipSuccess) return e;
+    scan_states_kernel<IO, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), states);
     scan_bwd_kernel<IO, DY, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), static_cast<const DY*>(a.dy), a.dS_T,
                                                                               states, a.dx, a.ddt, a.dz, a.dS0, bc, par);
     e = hipGetLastError();
@@ -363,7 +569,7 @@ size_t scan_workspace_bytes(const ScanArgs&) { return 0; }
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st) {
   if (a.T == 0) return launch_state_copy(a.S0, a.S_T, int64_t(a.B) * a.D * a.N, st);
   return by_size(a, [&](auto n, auto sp) {
-    return a.bf16 ? fwd_typed<bf16_t, n(), sp()>(a, a.S_T, nullptr, st) : fwd_typed<float, n(), sp()>(a, a.S_T, nullptr, st);
+    return a.bf16 ? fwd_typed<bf16_t, n(), sp()>(a, st) : fwd_typed<float, n(), sp()>(a, st);
   });
 }
 
