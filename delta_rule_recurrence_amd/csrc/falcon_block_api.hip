@@ -21,6 +21,9 @@ using falcon::ScanArgs;
 // room to spare, and every grid its 32 bits.
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 
+// Longest row of the scan's inputs: 16 rows of float32 stay within 32 bits of bytes.
+constexpr int64_t kMaxScanRow = int64_t(1) << 24;
+
 // a b c (each >= 0), or -1 beyond kMaxElems.
 int64_t elems(int64_t a, int64_t b, int64_t c = 1) {
   const __int128 n = static_cast<__int128>(a) * b * c;
@@ -108,9 +111,9 @@ falcon_status check_scan(const falcon_scan_problem* p, bool step, bool gate, Sca
   if (p->D % p->G != 0) return FALCON_ERR_SHAPE;
   const int64_t rows = int64_t(p->B) * T, GN = int64_t(p->G) * p->N;
   if (rows > (int64_t(1) << 31) || elems(p->B, int64_t(T) + 1, int64_t(p->D) * p->N) < 0) return FALCON_ERR_SHAPE;
-  if (!rows_ok(rows, p->x_row, p->D) || !rows_ok(rows, p->dt_row, p->D) || (gate && !rows_ok(rows, p->z_row, p->D)) ||
-      !rows_ok(rows, p->b_row, GN) || !rows_ok(rows, p->c_row, GN))
-    return FALCON_ERR_SHAPE;
+  const int64_t steps[] = {p->x_row, p->dt_row, gate ? p->z_row : p->D, p->b_row, p->c_row};
+  for (int i = 0; i < 5; ++i)
+    if (!rows_ok(rows, steps[i], i < 3 ? p->D : GN) || steps[i] > kMaxScanRow) return FALCON_ERR_SHAPE;
   if (step && int64_t(p->B) * p->D > (int64_t(1) << 27)) return FALCON_ERR_SHAPE;
   if (!dtype_ok(p->io_dtype)) return FALCON_ERR_DTYPE;
   *a = ScanArgs{};

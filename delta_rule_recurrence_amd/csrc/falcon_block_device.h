@@ -121,7 +121,7 @@ __device__ __forceinline__ float softplus_f32(float v) {
 // ---- sums over lanes ---------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ float dpp_plus(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 // Sum over aligned groups of LANES (a power of two up to 64) lanes, in every
 // lane; the whole wave must be active.

@@ -107,63 +107,112 @@ __device__ __forceinline__ float from_lane(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false));
 }
 
-// Four consecutive elements, in one access where `wide`.
-template <typename IO>
-__device__ __forceinline__ void load_four(const IO* p, bool wide, float (&v)[4]) {
-  if (wide) {
-    load_vec<IO, 4>(p, v);
+// Sixteen (or fewer) rows of one tensor as a buffer: an access behind its rows
+// reads zero or is dropped, so no address is clamped, and a lane's offsets are
+// the same 32-bit numbers at every step.  Rows have at most 2^24 elements.
+template <typename E>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const E* p, int64_t row, int64_t token, int rows) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(p + token * row), 0, max(rows, 0) * int(row) * int(sizeof(E)), 0x00020000);
+}
+template <typename E>
+__device__ __forceinline__ float load_one(__amdgpu_buffer_rsrc_t r, int offset) {
+  if constexpr (sizeof(E) == 2) {
+    return bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r, offset, 0, 0));
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = io<IO>::load(p, i);
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0));
   }
 }
+template <typename E>
+__device__ __forceinline__ void store_one(__amdgpu_buffer_rsrc_t r, int offset, float v) {
+  if constexpr (sizeof(E) == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), r, offset, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, offset, 0, 0);
+  }
+}
+// Four consecutive elements, in one access where `wide`.
+template <typename E>
+__device__ __forceinline__ void load_four(__amdgpu_buffer_rsrc_t r, int offset, bool wide, float (&v)[4]) {
+  if (!wide) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = load_one<E>(r, offset + i * int(sizeof(E)));
+  } else if constexpr (sizeof(E) == 2) {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0);
+    v[0] = __uint_as_float(w[0] << 16);
+    v[1] = __uint_as_float(w[0] & 0xffff0000u);
+    v[2] = __uint_as_float(w[1] << 16);
+    v[3] = __uint_as_float(w[1] & 0xffff0000u);
+  } else {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  }
+}
+constexpr int kNowhere = 0x7ffffff0;   // an offset behind every buffer
 
-// The raw inputs of a wave's sixteen tokens, loaded a step ahead.
+// A lane's byte offsets into sixteen rows: its tokens' rows of the tensors a
+// channel wide, and its fours of B and C.
 template <typename IO, int N>
-struct Tokens {
-  static constexpr int kUnits = (kTok * N / 4 + 63) / 64;   // fours of B (and C) a lane loads
-  float x[Lanes<N>::kRegs], dt[Lanes<N>::kRegs], z[Lanes<N>::kRegs];
-  float b[kUnits][4], c[kUnits][4];
+struct Offsets {
+  using L = Lanes<N>;
+  static constexpr int kUnits = (kTok * L::kPer + 63) / 64;   // fours of B (and C) a lane loads
+  int x, dt, z, b[kUnits], c[kUnits];
+  __device__ __forceinline__ Offsets(const ScanDims& d, int g, int c_) {
+    const int lane = threadIdx.x % 64, j = lane % L::kQuad;
+    x = (j * int(d.x_row) + c_) * int(sizeof(IO));
+    dt = (j * int(d.dt_row) + c_) * int(sizeof(IO));
+    z = (j * int(d.z_row) + c_) * int(sizeof(IO));
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int unit = u * 64 + lane, token = unit / L::kPer, at = g * N + 4 * (unit % L::kPer);
+      b[u] = unit < kTok * L::kPer ? (token * int(d.b_row) + at) * int(sizeof(IO)) : kNowhere;
+      c[u] = unit < kTok * L::kPer ? (token * int(d.c_row) + at) * int(sizeof(IO)) : kNowhere;
+    }
+  }
 };
 
-// Tokens behind the sequence's end are read as its last one (which exists) and
-// then count as no step at all: delta, x, B and C zero.
+// The inputs of a wave's sixteen tokens, loaded a step ahead; zero behind the
+// sequence's end.
 template <typename IO, int N>
-__device__ __forceinline__ void load_tokens(const ScanDims& d, const ScanIn<IO>& in, int64_t b, int g, int c, int t0, int len,
-                                            bool wide, Tokens<IO, N>& k) {
+struct Tokens {
+  float x[Lanes<N>::kRegs], dt[Lanes<N>::kRegs], z[Lanes<N>::kRegs];
+  float b[Offsets<IO, N>::kUnits][4], c[Offsets<IO, N>::kUnits][4];
+};
+template <typename IO, int N>
+__device__ __forceinline__ void load_tokens(const ScanDims& d, const ScanIn<IO>& in, int64_t b, int t0, int len, bool wide,
+                                            const Offsets<IO, N>& o, Tokens<IO, N>& k) {
   using L = Lanes<N>;
-  const int lane = threadIdx.x % 64;
+  const int64_t token = b * d.T + t0;
+  const int rows = min(len - t0, kTok);
+  const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows);
 #pragma unroll
   for (int i = 0; i < L::kRegs; ++i) {
-    const int64_t token = b * d.T + min(t0 + L::kQuad * i + lane % L::kQuad, len - 1);
-    k.x[i] = io<IO>::load(in.x, token * d.x_row + c);
-    k.dt[i] = io<IO>::load(in.dt, token * d.dt_row + c);
-    if (in.z) k.z[i] = io<IO>::load(in.z, token * d.z_row + c);
+    k.x[i] = load_one<IO>(rx, o.x + i * L::kQuad * int(d.x_row) * int(sizeof(IO)));
+    k.dt[i] = load_one<IO>(rdt, o.dt + i * L::kQuad * int(d.dt_row) * int(sizeof(IO)));
   }
+  if (in.z) {
+    const auto rz = rows_at(in.z, d.z_row, token, rows);
 #pragma unroll
-  for (int u = 0; u < Tokens<IO, N>::kUnits; ++u) {
-    const int unit = min(u * 64 + lane, kTok * L::kPer - 1);
-    const int64_t token = b * d.T + min(t0 + unit / L::kPer, len - 1);
-    const int at = g * N + 4 * (unit % L::kPer);
-    load_four(in.Bm + token * d.b_row + at, wide, k.b[u]);
-    load_four(in.Cm + token * d.c_row + at, wide, k.c[u]);
+    for (int i = 0; i < L::kRegs; ++i) k.z[i] = load_one<IO>(rz, o.z + i * L::kQuad * int(d.z_row) * int(sizeof(IO)));
+  }
+  const auto rb = rows_at(in.Bm, d.b_row, token, rows), rc = rows_at(in.Cm, d.c_row, token, rows);
+#pragma unroll
+  for (int u = 0; u < Offsets<IO, N>::kUnits; ++u) {
+    load_four<IO>(rb, o.b[u], wide, k.b[u]);
+    load_four<IO>(rc, o.c[u], wide, k.c[u]);
   }
 }
 
 // B and C of the wave's tokens to its part of LDS, [kTok][N] each.
 template <typename IO, int N>
-__device__ __forceinline__ void stage_shared(const Tokens<IO, N>& k, int t0, int len, float* Bs, float* Cs) {
-  using L = Lanes<N>;
+__device__ __forceinline__ void stage_shared(const Tokens<IO, N>& k, float* Bs, float* Cs) {
   const int lane = threadIdx.x % 64;
 #pragma unroll
-  for (int u = 0; u < Tokens<IO, N>::kUnits; ++u) {
+  for (int u = 0; u < Offsets<IO, N>::kUnits; ++u) {
     const int unit = u * 64 + lane;
-    const bool live = t0 + unit / L::kPer < len;
-    if (kTok * L::kPer % 64 == 0 || unit < kTok * L::kPer) {
-      *reinterpret_cast<float4*>(Bs + 4 * unit) =
-          live ? make_float4(k.b[u][0], k.b[u][1], k.b[u][2], k.b[u][3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      *reinterpret_cast<float4*>(Cs + 4 * unit) =
-          live ? make_float4(k.c[u][0], k.c[u][1], k.c[u][2], k.c[u][3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (kTok * N / 4 % 64 == 0 || unit < kTok * N / 4) {
+      *reinterpret_cast<float4*>(Bs + 4 * unit) = make_float4(k.b[u][0], k.b[u][1], k.b[u][2], k.b[u][3]);
+      *reinterpret_cast<float4*>(Cs + 4 * unit) = make_float4(k.c[u][0], k.c[u][1], k.c[u][2], k.c[u][3]);
     }
   }
 }
@@ -216,13 +265,15 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   float* Bs = shared[wave][0];
   float* Cs = shared[wave][1];
 
+  const Offsets<IO, N> offsets(d, g, c);
+  const int y_at = on && s < L::kQuad ? (j * d.D + c) * int(sizeof(IO)) : kNowhere;
   Tokens<IO, N> next;
-  if (len > 0) load_tokens<IO, N>(d, in, b, g, c, wave * kTok, len, wide, next);
+  if (len > 0) load_tokens<IO, N>(d, in, b, wave * kTok, len, wide, offsets, next);
   int parity = 0;
   for (int base = 0; base < len; base += kFwdWaves * kTok, parity ^= 1) {
     const int t0 = base + wave * kTok;
     float delta[L::kRegs], x[L::kRegs], gate[L::kRegs], u[L::kRegs], sum = 0.0f;
-    stage_shared<IO, N>(next, t0, len, Bs, Cs);
+    stage_shared<IO, N>(next, Bs, Cs);
 #pragma unroll
     for (int i = 0; i < L::kRegs; ++i) {
       const bool live = t0 + L::kQuad * i + j < len;
@@ -233,7 +284,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
       sum += delta[i];
     }
     sum = lanes_sum<L::kQuad>(sum);
-    if (base + kFwdWaves * kTok < len) load_tokens<IO, N>(d, in, b, g, c, t0 + kFwdWaves * kTok, len, wide, next);
+    if (base + kFwdWaves * kTok < len) load_tokens<IO, N>(d, in, b, t0 + kFwdWaves * kTok, len, wide, offsets, next);
     __builtin_amdgcn_wave_barrier();
 
     // 1. the wave's map
@@ -281,12 +332,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
       r = lanes_sum<L::kPer>(r);
       read[i()] = jj() == 0 || j == jj() ? r : read[i()];
     });
+    const auto ry = rows_at(y, d.D, b * d.T + t0, min(len - t0, kTok));
 #pragma unroll
-    for (int i = 0; i < L::kRegs; ++i) {
-      const int t = t0 + L::kQuad * i + j;
-      if (on && s < L::kQuad && t < len)
-        io<IO>::store(y, (b * d.T + t) * d.D + c, __builtin_fmaf(skip, x[i], read[i]) * gate[i]);
-    }
+    for (int i = 0; i < L::kRegs; ++i)
+      store_one<IO>(ry, y_at == kNowhere ? kNowhere : y_at + i * L::kQuad * d.D * int(sizeof(IO)),
+                    __builtin_fmaf(skip, x[i], read[i]) * gate[i]);
     __builtin_amdgcn_wave_barrier();
   }
   if (S_T && wave == 0 && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(H[0], H[1], H[2], H[3]);
