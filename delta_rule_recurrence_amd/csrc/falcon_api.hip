@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "falcon.h"
+#include "falcon_block.h"
 #include "falcon_check.h"
 #include "falcon_launch.h"
 
@@ -228,6 +229,10 @@ ProblemArgs sequence_slice(const ProblemArgs& a, int64_t s0, int n) {
 }
 
 }  // namespace
+
+namespace falcon {
+int wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+}  // namespace falcon
 
 extern "C" {
 

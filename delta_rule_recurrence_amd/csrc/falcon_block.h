@@ -37,6 +37,9 @@ struct ConvArgs {
   const uint8_t* is_first;  // may be null
 };
 
+// Polls a bounded wait makes before giving up (falcon_set_wait_limit).
+int wait_limit();
+
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st);
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st);
 size_t conv_bwd_workspace_bytes(const ConvArgs& a);
@@ -82,6 +85,7 @@ struct ScanArgs {
   void* y;
   float* S_T;              // may be null; may be S0
   float* workspace;
+  int spin_limit;          // polls before a wait between waves gives up
   // single token
   float* S;
   const uint8_t* is_first;

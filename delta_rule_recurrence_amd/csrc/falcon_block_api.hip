@@ -122,6 +122,7 @@ falcon_status check_scan(const falcon_scan_problem* p, bool step, bool gate, Sca
   a->softplus = p->softplus != 0;
   a->x_row = p->x_row; a->dt_row = p->dt_row; a->z_row = p->z_row;
   a->b_row = p->b_row; a->c_row = p->c_row;
+  a->spin_limit = falcon::wait_limit();
   return FALCON_OK;
 }
 

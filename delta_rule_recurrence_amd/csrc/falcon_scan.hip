@@ -78,18 +78,16 @@ template <bool SOFTPLUS>
 __device__ __forceinline__ float step_of(float v) { return SOFTPLUS ? softplus_f32(v) : v; }
 
 // ---- prompts ----------------------------------------------------------------------
-// A lane owns four states of one channel: S = N / 4 lanes a channel, 64 / S
-// channels a wave.  A wave takes kTok = 16 tokens at a time and a workgroup's
-// kWaves waves consecutive sixteens, so a sequence's tokens run in parallel:
-//   1. each wave scans its tokens from a zero state, the decays a_t kept in
-//      registers, which gives its map S -> P S + E (P = exp(A sum of delta));
-//   2. the maps meet in LDS, and each wave folds those before it onto the
-//      state that entered the workgroup's step;
-//   3. each wave scans again from there, with the same a_t, and reads.
-// The exponentials, which with the multiply-adds bound the scan (4 + 8 cycles a
-// wave for the argument and exp2, 4 for each of the others), are so computed
-// once.  What a token and a channel need once (step size, gate) is worked out by
-// one lane of a quad for every fourth token and handed round by quad permutes.
+// A lane owns four states of one channel: N / 4 lanes a channel, 256 / N channels
+// a wave.  A workgroup's kFwdWaves waves take sixteen tokens in turn.  What does
+// not need the state (step sizes, gates, decays, B and C) a wave works out ahead;
+// then it takes the state from the wave before, runs its sixteen steps, hands the
+// state on and makes the reads, while the next wave is at its steps.  So a
+// channel's tokens keep several waves busy with no operation done twice.
+// Bound by the vector units: an exp2 (8 cycles a wave) and its argument, the
+// product u B and a multiply-add for the state and one for the read (4 each).
+// What a token and a channel need once is worked out by one lane of a quad for
+// every fourth token and handed round by quad permutes.
 constexpr int kTok = 16;
 
 template <int N>
@@ -114,14 +112,24 @@ template <typename E>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const E* p, int64_t row, int64_t token, int rows) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(p + token * row), 0, max(rows, 0) * int(row) * int(sizeof(E)), 0x00020000);
 }
+// Loads leave the bits as they are, so that nothing waits for them before their
+// use; widen() then gives the value.
+template <typename E> struct bits_of { using type = uint32_t; };
+template <> struct bits_of<bf16_t> { using type = uint16_t; };
 template <typename E>
-__device__ __forceinline__ float load_one(__amdgpu_buffer_rsrc_t r, int offset) {
+using bits_t = typename bits_of<E>::type;
+template <typename E>
+__device__ __forceinline__ bits_t<E> load_bits(__amdgpu_buffer_rsrc_t r, int offset) {
   if constexpr (sizeof(E) == 2) {
-    return bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r, offset, 0, 0));
+    return __builtin_amdgcn_raw_buffer_load_b16(r, offset, 0, 0);
   } else {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0));
+    return __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0);
   }
 }
+__device__ __forceinline__ float widen(uint16_t bits) { return bf16_to_f32(bits); }
+__device__ __forceinline__ float widen(uint32_t bits) { return __uint_as_float(bits); }
+// v, or zero: by its bits, so that the compiler makes no branch of it.
+__device__ __forceinline__ float kept(float v, bool keep) { return __uint_as_float(__float_as_uint(v) & (keep ? 0xffffffffu : 0u)); }
 template <typename E>
 __device__ __forceinline__ void store_one(__amdgpu_buffer_rsrc_t r, int offset, float v) {
   if constexpr (sizeof(E) == 2) {
@@ -130,22 +138,37 @@ __device__ __forceinline__ void store_one(__amdgpu_buffer_rsrc_t r, int offset, 
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, offset, 0, 0);
   }
 }
-// Four consecutive elements, in one access where `wide`.
+// Four consecutive elements, bf16 ones as two words: one access where `wide`,
+// else one each (and a wait, to pair them: rows of such widths are rare).
 template <typename E>
-__device__ __forceinline__ void load_four(__amdgpu_buffer_rsrc_t r, int offset, bool wide, float (&v)[4]) {
-  if (!wide) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = load_one<E>(r, offset + i * int(sizeof(E)));
-  } else if constexpr (sizeof(E) == 2) {
-    const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0);
-    v[0] = __uint_as_float(w[0] << 16);
-    v[1] = __uint_as_float(w[0] & 0xffff0000u);
-    v[2] = __uint_as_float(w[1] << 16);
-    v[3] = __uint_as_float(w[1] & 0xffff0000u);
-  } else {
+constexpr int kFourWords = sizeof(E) == 2 ? 2 : 4;
+template <typename E>
+__device__ __forceinline__ void load_four_bits(__amdgpu_buffer_rsrc_t r, int offset, bool wide, uint32_t (&v)[kFourWords<E>]) {
+  if constexpr (sizeof(E) == 2) {
+    if (wide) {
+      const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0);
+      v[0] = w[0];
+      v[1] = w[1];
+    } else {
+      v[0] = load_bits<E>(r, offset) | (uint32_t(load_bits<E>(r, offset + 2)) << 16);
+      v[1] = load_bits<E>(r, offset + 4) | (uint32_t(load_bits<E>(r, offset + 6)) << 16);
+    }
+  } else if (wide) {
     const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i) v[i] = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = load_bits<E>(r, offset + 4 * i);
+  }
+}
+template <typename E>
+__device__ __forceinline__ float4 widen_four(const uint32_t (&v)[kFourWords<E>]) {
+  if constexpr (sizeof(E) == 2) {
+    return make_float4(__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
+                       __uint_as_float(v[1] & 0xffff0000u));
+  } else {
+    return make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
   }
 }
 constexpr int kNowhere = 0x7ffffff0;   // an offset behind every buffer
@@ -171,12 +194,12 @@ struct Offsets {
   }
 };
 
-// The inputs of a wave's sixteen tokens, loaded a step ahead; zero behind the
-// sequence's end.
+// The bits of a wave's sixteen tokens' inputs, loaded a turn ahead; zero behind
+// the sequence's end.
 template <typename IO, int N>
 struct Tokens {
-  float x[Lanes<N>::kRegs], dt[Lanes<N>::kRegs], z[Lanes<N>::kRegs];
-  float b[Offsets<IO, N>::kUnits][4], c[Offsets<IO, N>::kUnits][4];
+  bits_t<IO> x[Lanes<N>::kRegs], dt[Lanes<N>::kRegs], z[Lanes<N>::kRegs];
+  uint32_t b[Offsets<IO, N>::kUnits][kFourWords<IO>], c[Offsets<IO, N>::kUnits][kFourWords<IO>];
 };
 template <typename IO, int N>
 __device__ __forceinline__ void load_tokens(const ScanDims& d, const ScanIn<IO>& in, int64_t b, int t0, int len, bool wide,
@@ -187,19 +210,19 @@ __device__ __forceinline__ void load_tokens(const ScanDims& d, const ScanIn<IO>&
   const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows);
 #pragma unroll
   for (int i = 0; i < L::kRegs; ++i) {
-    k.x[i] = load_one<IO>(rx, o.x + i * L::kQuad * int(d.x_row) * int(sizeof(IO)));
-    k.dt[i] = load_one<IO>(rdt, o.dt + i * L::kQuad * int(d.dt_row) * int(sizeof(IO)));
+    k.x[i] = load_bits<IO>(rx, o.x + i * L::kQuad * int(d.x_row) * int(sizeof(IO)));
+    k.dt[i] = load_bits<IO>(rdt, o.dt + i * L::kQuad * int(d.dt_row) * int(sizeof(IO)));
   }
   if (in.z) {
     const auto rz = rows_at(in.z, d.z_row, token, rows);
 #pragma unroll
-    for (int i = 0; i < L::kRegs; ++i) k.z[i] = load_one<IO>(rz, o.z + i * L::kQuad * int(d.z_row) * int(sizeof(IO)));
+    for (int i = 0; i < L::kRegs; ++i) k.z[i] = load_bits<IO>(rz, o.z + i * L::kQuad * int(d.z_row) * int(sizeof(IO)));
   }
   const auto rb = rows_at(in.Bm, d.b_row, token, rows), rc = rows_at(in.Cm, d.c_row, token, rows);
 #pragma unroll
   for (int u = 0; u < Offsets<IO, N>::kUnits; ++u) {
-    load_four<IO>(rb, o.b[u], wide, k.b[u]);
-    load_four<IO>(rc, o.c[u], wide, k.c[u]);
+    load_four_bits<IO>(rb, o.b[u], wide, k.b[u]);
+    load_four_bits<IO>(rc, o.c[u], wide, k.c[u]);
   }
 }
 
@@ -211,8 +234,8 @@ __device__ __forceinline__ void stage_shared(const Tokens<IO, N>& k, float* Bs, 
   for (int u = 0; u < Offsets<IO, N>::kUnits; ++u) {
     const int unit = u * 64 + lane;
     if (kTok * N / 4 % 64 == 0 || unit < kTok * N / 4) {
-      *reinterpret_cast<float4*>(Bs + 4 * unit) = make_float4(k.b[u][0], k.b[u][1], k.b[u][2], k.b[u][3]);
-      *reinterpret_cast<float4*>(Cs + 4 * unit) = make_float4(k.c[u][0], k.c[u][1], k.c[u][2], k.c[u][3]);
+      *reinterpret_cast<float4*>(Bs + 4 * unit) = widen_four<IO>(k.b[u]);
+      *reinterpret_cast<float4*>(Cs + 4 * unit) = widen_four<IO>(k.c[u]);
     }
   }
 }
@@ -220,6 +243,28 @@ __device__ __forceinline__ void stage_shared(const Tokens<IO, N>& k, float* Bs, 
 __device__ __forceinline__ void four(const float* p, float (&v)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+
+// A lane's fours of rows 4 k .. 4 k + 3 of a [kTok][N] array.
+template <int N>
+__device__ __forceinline__ void four_rows(const float* p, int k, float (&v)[4][4]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) four(p + (4 * k + r) * N, v[r]);
+}
+
+// f(t, row) for t = 0 .. 15 in order, `row` this lane's four of row t of the
+// [kTok][N] array p; the rows come four at a time, four ahead, the first of
+// them already in `first`.
+template <int N, int K = 0, typename F>
+__device__ __forceinline__ void each_row(const float* p, float (&first)[4][4], F f) {
+  float ahead[4][4];
+  if constexpr (K + 1 < kTok / 4) four_rows<N>(p, K + 1, ahead);
+  __builtin_amdgcn_sched_barrier(0);
+  f(std::integral_constant<int, 4 * K>{}, first[0]);
+  f(std::integral_constant<int, 4 * K + 1>{}, first[1]);
+  f(std::integral_constant<int, 4 * K + 2>{}, first[2]);
+  f(std::integral_constant<int, 4 * K + 3>{}, first[3]);
+  if constexpr (K + 1 < kTok / 4) each_row<N, K + 1>(p, ahead, f);
 }
 
 // f(t, j, i) for t = 0 .. 15 in order, with t = kQuad i + j known at compile time.
@@ -241,12 +286,23 @@ __device__ __forceinline__ int64_t by_xcd(int64_t block, int64_t blocks) {
 
 constexpr int kFwdWaves = 4;
 
+// A turn of a wave: token block `turn` may start once *at has reached it.  False
+// if that did not happen within `limit` polls (then the caller poisons its
+// results; see falcon_set_wait_limit).
+__device__ __forceinline__ bool wait_turn(const int* at, int turn, int limit) {
+  for (int polls = 0; __hip_atomic_load(at, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < turn; ++polls) {
+    if (polls >= limit) return false;
+  }
+  return true;
+}
+
 template <typename IO, int N, bool SOFTPLUS>
-__global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void scan_fwd_kernel(ScanDims d, ScanIn<IO> in, bool wide, IO* __restrict__ y,
-                                                                    float* __restrict__ S_T) {
+__global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void scan_fwd_kernel(
+    ScanDims d, ScanIn<IO> in, bool wide, IO* __restrict__ y, float* __restrict__ S_T, int limit) {
   using L = Lanes<N>;
-  __shared__ float shared[kFwdWaves][2][kTok * N];      // B, C
-  __shared__ float4 maps[2][kFwdWaves][2][64];          // by parity of the step: P, E
+  __shared__ float shared[kFwdWaves][2][kTok * N];      // B, C of a wave's tokens
+  __shared__ float4 passed[64];                         // the state on its way to the next wave
+  __shared__ int turns;                                 // token blocks whose steps are done
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int64_t id = by_xcd(blockIdx.x, gridDim.x);
   const int tile = int(id % d.tiles), g = int(id / d.tiles % d.G);
@@ -256,81 +312,72 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   const int c = g * d.Dg + min(in_group, d.Dg - 1), s = lane % L::kPer, j = lane % L::kQuad;
   const int len = tokens_of(in.lengths, int(b), d.T);
   const int64_t at = (b * d.D + c) * N + 4 * s;
-  float H[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A2[4];
-  if (in.S0) four(in.S0 + at, H);
+  float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A2[4];
+  if (in.S0 && wave == 0) four(in.S0 + at, h);
   four(in.A + int64_t(c) * N + 4 * s, A2);
 #pragma unroll
   for (int n = 0; n < 4; ++n) A2[n] *= kLog2e;
   const float skip = in.Dskip ? in.Dskip[c] : 0.0f, bias = in.dt_bias ? in.dt_bias[c] : 0.0f;
   float* Bs = shared[wave][0];
   float* Cs = shared[wave][1];
-
   const Offsets<IO, N> offsets(d, g, c);
   const int y_at = on && s < L::kQuad ? (j * d.D + c) * int(sizeof(IO)) : kNowhere;
+
   Tokens<IO, N> next;
-  if (len > 0) load_tokens<IO, N>(d, in, b, wave * kTok, len, wide, offsets, next);
-  int parity = 0;
-  for (int base = 0; base < len; base += kFwdWaves * kTok, parity ^= 1) {
-    const int t0 = base + wave * kTok;
-    float delta[L::kRegs], x[L::kRegs], gate[L::kRegs], u[L::kRegs], sum = 0.0f;
+  if (wave * kTok < len) load_tokens<IO, N>(d, in, b, wave * kTok, len, wide, offsets, next);
+  if (threadIdx.x == 0) turns = 0;
+  __syncthreads();
+  for (int turn = wave; turn * kTok < len; turn += kFwdWaves) {
+    const int t0 = turn * kTok;
+    float delta[L::kRegs], x[L::kRegs], gate[L::kRegs], u[L::kRegs];
     stage_shared<IO, N>(next, Bs, Cs);
 #pragma unroll
     for (int i = 0; i < L::kRegs; ++i) {
       const bool live = t0 + L::kQuad * i + j < len;
-      x[i] = next.x[i];
-      delta[i] = live ? step_of<SOFTPLUS>(next.dt[i] + bias) : 0.0f;
-      u[i] = live ? delta[i] * x[i] : 0.0f;
-      gate[i] = in.z ? act_f32<kActSilu>(next.z[i]) : 1.0f;
-      sum += delta[i];
+      x[i] = widen(next.x[i]);
+      delta[i] = kept(step_of<SOFTPLUS>(widen(next.dt[i]) + bias), live);
+      u[i] = delta[i] * x[i];
+      gate[i] = in.z ? act_f32<kActSilu>(widen(next.z[i])) : 1.0f;
     }
-    sum = lanes_sum<L::kQuad>(sum);
-    if (base + kFwdWaves * kTok < len) load_tokens<IO, N>(d, in, b, t0 + kFwdWaves * kTok, len, wide, offsets, next);
-    __builtin_amdgcn_wave_barrier();
-
-    // 1. the wave's map
-    float a[kTok][4], E[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (t0 + kFwdWaves * kTok < len) load_tokens<IO, N>(d, in, b, t0 + kFwdWaves * kTok, len, wide, offsets, next);
+    // the decays
+    float v[kTok][4];
     each_token<L::kQuad>([&](auto t, auto jj, auto i) {
-      const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
-      float bt[4];
-      four(Bs + t() * N + 4 * s, bt);
+      const float dt = from_lane<L::kQuad, jj()>(delta[i()]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) v[t()][n] = __builtin_amdgcn_exp2f(dt * A2[n]);
+    });
+    __builtin_amdgcn_wave_barrier();
+    float rows[4][4];
+    four_rows<N>(Bs + 4 * s, 0, rows);
+    // the steps, each decay giving way to its state
+    if (turn > 0) {
+      const bool came = wait_turn(&turns, turn, limit);
+      four(reinterpret_cast<const float*>(&passed[lane]), h);
+      if (!came) h[0] = h[1] = h[2] = h[3] = __builtin_nanf("");
+    }
+    __builtin_amdgcn_s_setprio(2);
+    each_row<N>(Bs + 4 * s, rows, [&](auto t, const float (&bt)[4]) {
+      const float ut = from_lane<L::kQuad, t() % L::kQuad>(u[t() / L::kQuad]);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        a[t()][n] = __builtin_amdgcn_exp2f(dt * A2[n]);
-        E[n] = __builtin_fmaf(a[t()][n], E[n], ut * bt[n]);
+        h[n] = __builtin_fmaf(v[t()][n], h[n], ut * bt[n]);
+        v[t()][n] = h[n];
       }
     });
-    maps[parity][wave][0][lane] = make_float4(__builtin_amdgcn_exp2f(sum * A2[0]), __builtin_amdgcn_exp2f(sum * A2[1]),
-                                              __builtin_amdgcn_exp2f(sum * A2[2]), __builtin_amdgcn_exp2f(sum * A2[3]));
-    maps[parity][wave][1][lane] = make_float4(E[0], E[1], E[2], E[3]);
-    __syncthreads();
-    // 2. the state that enters the wave's tokens, and the one that leaves the step
-    float h[4] = {H[0], H[1], H[2], H[3]};
-#pragma unroll
-    for (int w = 0; w < kFwdWaves; ++w) {
-      if (w == wave) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) h[n] = H[n];
-      }
-      float Pw[4], Ew[4];
-      four(reinterpret_cast<const float*>(&maps[parity][w][0][lane]), Pw);
-      four(reinterpret_cast<const float*>(&maps[parity][w][1][lane]), Ew);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) H[n] = __builtin_fmaf(Pw[n], H[n], Ew[n]);
-    }
-    // 3. the scan from there, and the reads
+    passed[lane] = make_float4(h[0], h[1], h[2], h[3]);
+    if (lane == 0) __hip_atomic_store(&turns, turn + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __builtin_amdgcn_s_setprio(0);
+    // the reads
     float read[L::kRegs];
-    each_token<L::kQuad>([&](auto t, auto jj, auto i) {
-      const float ut = from_lane<L::kQuad, jj()>(u[i()]);
-      float bt[4], ct[4], r = 0.0f;
-      four(Bs + t() * N + 4 * s, bt);
-      four(Cs + t() * N + 4 * s, ct);
+    four_rows<N>(Cs + 4 * s, 0, rows);
+    each_row<N>(Cs + 4 * s, rows, [&](auto t, const float (&ct)[4]) {
+      constexpr int jj = t() % L::kQuad;
+      float r = ct[0] * v[t()][0];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        h[n] = __builtin_fmaf(a[t()][n], h[n], ut * bt[n]);
-        r = __builtin_fmaf(ct[n], h[n], r);
-      }
+      for (int n = 1; n < 4; ++n) r = __builtin_fmaf(ct[n], v[t()][n], r);
       r = lanes_sum<L::kPer>(r);
-      read[i()] = jj() == 0 || j == jj() ? r : read[i()];
+      read[t() / L::kQuad] = jj == 0 || j == jj ? r : read[t() / L::kQuad];
     });
     const auto ry = rows_at(y, d.D, b * d.T + t0, min(len - t0, kTok));
 #pragma unroll
@@ -339,7 +386,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
                     __builtin_fmaf(skip, x[i], read[i]) * gate[i]);
     __builtin_amdgcn_wave_barrier();
   }
-  if (S_T && wave == 0 && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(H[0], H[1], H[2], H[3]);
+  // the wave that ran the last tokens (wave 0 where there are none) has the end
+  const int last = len > 0 ? (len - 1) / kTok % kFwdWaves : 0;
+  if (S_T && wave == last && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(h[0], h[1], h[2], h[3]);
 }
 
 // Every state, one token after another: [B, T, D, N], for the gradients.
@@ -556,7 +605,7 @@ hipError_t fwd_typed(const ScanArgs& a, hipStream_t st) {
   const int64_t blocks = int64_t(a.B) * a.G * d.tiles;
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
   scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kFwdWaves), 0, st>>>(d, inputs_of<IO>(a), fours_wide(a),
-                                                                                     static_cast<IO*>(a.y), a.S_T);
+                                                                                     static_cast<IO*>(a.y), a.S_T, a.spin_limit);
   return hipGetLastError();
 }
 
