@@ -110,9 +110,15 @@ hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st);
 size_t scan_bwd_workspace_bytes(const ScanArgs& a);
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st);
 
-// out[i] = sum over p < parts of in[p n + i], p ascending, in double.  Columns
-// [n_first, n) may go to a second array.
-hipError_t launch_sum_parts(const float* in, int64_t parts, int64_t n, float* out, int64_t n_first,
-                            float* out2, hipStream_t st);
+// Columns of `parts` rows of n partial sums, summed in a fixed order: column i goes
+// to out[0][i] below ends[0], to out[1][i - ends[0]] below ends[1], else to
+// out[2][i - ends[1]]; a null output is skipped.
+struct PartSums {
+  const float* in;
+  int64_t parts, n;
+  float* out[3];
+  int64_t ends[2];
+};
+hipError_t launch_sum_parts(const PartSums& s, hipStream_t st);
 
 }  // namespace falcon

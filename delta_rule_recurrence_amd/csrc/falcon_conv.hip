@@ -256,20 +256,6 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
   }
 }
 
-// out[i] = the sum of column i over the rows of partial sums, in double.
-__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ in, int64_t parts, int64_t n, float* __restrict__ out,
-                                                        int64_t n_first, float* __restrict__ out2) {
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-    double s = 0.0;
-    for (int64_t p = 0; p < parts; ++p) s += in[p * n + i];
-    if (i < n_first) {
-      if (out) out[i] = float(s);
-    } else if (out2) {
-      out2[i - n_first] = float(s);
-    }
-  }
-}
-
 // Elements a thread owns: 16 bytes' worth where every row starts on a multiple
 // of 16 bytes, else one.
 bool rows_wide(const ConvArgs& a, int v) { return a.C % v == 0 && a.x_row % v == 0; }
@@ -375,12 +361,6 @@ hipError_t bwd_by_vec(const ConvArgs& a, const ConvBwdShape& s, hipStream_t st) 
 
 }  // namespace
 
-hipError_t launch_sum_parts(const float* in, int64_t parts, int64_t n, float* out, int64_t n_first, float* out2, hipStream_t st) {
-  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 1 << 16);
-  sum_parts_kernel<<<dim3(unsigned(blocks)), dim3(256), 0, st>>>(in, parts, n, out, n_first, out2);
-  return hipGetLastError();
-}
-
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st) { return by_type<Form::kFwd>(a, st); }
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) { return by_type<Form::kStep>(a, st); }
 
@@ -398,7 +378,8 @@ hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
       e = a.dy_bf16 ? bwd_by_vec<float, bf16_t>(a, s, st) : bwd_by_vec<float, float>(a, s, st);
   }
   if (e != hipSuccess) return e;
-  return launch_sum_parts(a.workspace, s.rblocks, int64_t(a.C) * (a.W + 1), a.dweight, int64_t(a.C) * a.W, a.dbias, st);
+  const int64_t taps = int64_t(a.C) * a.W;
+  return launch_sum_parts({a.workspace, s.rblocks, taps + a.C, {a.dweight, a.dbias, nullptr}, {taps, taps + a.C}}, st);
 }
 
 }  // namespace falcon

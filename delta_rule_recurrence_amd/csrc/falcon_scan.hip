@@ -20,10 +20,8 @@ namespace falcon {
 
 namespace {
 
-constexpr int kLanes = 64;
-
 struct ScanDims {
-  int B, T, D, G, Dg, tiles;   // Dg channels a group, in `tiles` waves of 64
+  int B, T, D, G, Dg, tiles;   // Dg channels a group, in `tiles` waves of 256 / N
   int64_t x_row, dt_row, z_row, b_row, c_row;
 };
 
@@ -40,24 +38,6 @@ struct ScanIn {
   const float* S0;
   const int32_t* lengths;
 };
-
-// The wave's sequence, group and this lane's channel (clamped where the group
-// ends inside the wave; such lanes compute on a valid channel and store nothing).
-struct Place {
-  int b, g, c;
-  bool on;
-};
-__device__ __forceinline__ Place place_of(const ScanDims& d, int64_t wave) {
-  const int64_t per = int64_t(d.G) * d.tiles;
-  Place p;
-  p.b = int(wave / per);
-  const int r = int(wave % per);
-  p.g = r / d.tiles;
-  const int c = (r % d.tiles) * kLanes + int(threadIdx.x % kLanes);
-  p.on = c < d.Dg;
-  p.c = p.g * d.Dg + min(c, d.Dg - 1);
-  return p;
-}
 
 template <int N>
 __device__ __forceinline__ void load_state(const float* p, float (&s)[N]) {
@@ -110,7 +90,8 @@ __device__ __forceinline__ float from_lane(float v) {
 // the same 32-bit numbers at every step.  Rows have at most 2^24 elements.
 template <typename E>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const E* p, int64_t row, int64_t token, int rows) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(p + token * row), 0, max(rows, 0) * int(row) * int(sizeof(E)), 0x00020000);
+  const int bytes = __builtin_amdgcn_readfirstlane(max(rows, 0)) * int(row) * int(sizeof(E));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(p + token * row), 0, bytes, 0x00020000);
 }
 // Loads leave the bits as they are, so that nothing waits for them before their
 // use; widen() then gives the value.
@@ -226,17 +207,18 @@ __device__ __forceinline__ void load_tokens(const ScanDims& d, const ScanIn<IO>&
   }
 }
 
-// B and C of the wave's tokens to its part of LDS, [kTok][N] each.
+// B and C of the wave's tokens to its part of LDS, [kTok][N] each (and zeros up to
+// a whole wave's fours).
+template <int N>
+constexpr int kShared = kTok * N < 256 ? 256 : kTok * N;
 template <typename IO, int N>
 __device__ __forceinline__ void stage_shared(const Tokens<IO, N>& k, float* Bs, float* Cs) {
   const int lane = threadIdx.x % 64;
 #pragma unroll
   for (int u = 0; u < Offsets<IO, N>::kUnits; ++u) {
     const int unit = u * 64 + lane;
-    if (kTok * N / 4 % 64 == 0 || unit < kTok * N / 4) {
-      *reinterpret_cast<float4*>(Bs + 4 * unit) = widen_four<IO>(k.b[u]);
-      *reinterpret_cast<float4*>(Cs + 4 * unit) = widen_four<IO>(k.c[u]);
-    }
+    *reinterpret_cast<float4*>(Bs + 4 * unit) = widen_four<IO>(k.b[u]);
+    *reinterpret_cast<float4*>(Cs + 4 * unit) = widen_four<IO>(k.c[u]);
   }
 }
 
@@ -300,7 +282,7 @@ template <typename IO, int N, bool SOFTPLUS>
 __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void scan_fwd_kernel(
     ScanDims d, ScanIn<IO> in, bool wide, IO* __restrict__ y, float* __restrict__ S_T, int limit) {
   using L = Lanes<N>;
-  __shared__ float shared[kFwdWaves][2][kTok * N];      // B, C of a wave's tokens
+  __shared__ float shared[kFwdWaves][2][kShared<N>];      // B, C of a wave's tokens
   __shared__ float4 passed[64];                         // the state on its way to the next wave
   __shared__ int turns;                                 // token blocks whose steps are done
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
@@ -310,7 +292,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   const int in_group = tile * L::kChannels + lane / L::kPer;
   const bool on = in_group < d.Dg;
   const int c = g * d.Dg + min(in_group, d.Dg - 1), s = lane % L::kPer, j = lane % L::kQuad;
-  const int len = tokens_of(in.lengths, int(b), d.T);
+  const int len = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T));
   const int64_t at = (b * d.D + c) * N + 4 * s;
   float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A2[4];
   if (in.S0 && wave == 0) four(in.S0 + at, h);
@@ -391,35 +373,6 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   if (S_T && wave == last && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(h[0], h[1], h[2], h[3]);
 }
 
-// Every state, one token after another: [B, T, D, N], for the gradients.
-template <typename IO, int N, bool SOFTPLUS>
-__global__ __launch_bounds__(64) void scan_states_kernel(ScanDims d, ScanIn<IO> in, float* states) {
-  const Place p = place_of(d, blockIdx.x);
-  const int len = tokens_of(in.lengths, p.b, d.T);
-  const int64_t at = (int64_t(p.b) * d.D + p.c) * N;
-  float S[N], A2[N];
-  load_state<N>(in.A + int64_t(p.c) * N, A2);
-#pragma unroll
-  for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
-  if (in.S0) {
-    load_state<N>(in.S0 + at, S);
-  } else {
-#pragma unroll
-    for (int n = 0; n < N; ++n) S[n] = 0.0f;
-  }
-  const float bias = in.dt_bias ? in.dt_bias[p.c] : 0.0f;
-  for (int t = 0; t < len; ++t) {
-    const int64_t token = int64_t(p.b) * d.T + t;
-    const float x = io<IO>::load(in.x, token * d.x_row + p.c);
-    const float delta = step_of<SOFTPLUS>(io<IO>::load(in.dt, token * d.dt_row + p.c) + bias);
-    const IO* pb = in.Bm + token * d.b_row + p.g * N;
-    const float u = delta * x;
-#pragma unroll
-    for (int n = 0; n < N; ++n) S[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), S[n], u * io<IO>::load(pb, n));
-    if (p.on) store_state<N>(states + (token * d.D + p.c) * N, S);
-  }
-}
-
 // ---- one token --------------------------------------------------------------------
 template <typename IO, int N, bool SOFTPLUS>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanDims d, ScanIn<IO> in, float* S_io, const uint8_t* is_first, IO* y) {
@@ -458,101 +411,439 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanDims d, ScanIn<IO> i
   }
 }
 
-// ---- gradients ----------------------------------------------------------------------
-// One wave a sequence and 64 channels, from the last token to the first, with
-// every state from scan_fwd_kernel.  What sums over channels (dB, dC) leaves as
-// one row a wave, what sums over sequences (dA, dD, ddt_bias) as one a sequence.
-template <typename IO, typename DY, int N, bool SOFTPLUS>
-__global__ __launch_bounds__(64) void scan_bwd_kernel(ScanDims d, ScanIn<IO> in, const DY* dy, const float* dS_T, const float* states,
-                                                      float* dx, float* ddt, float* dz, float* dS0, float* bc_parts, float* par_parts) {
-  const Place p = place_of(d, blockIdx.x);
-  const int len = tokens_of(in.lengths, p.b, d.T);
-  const int tile = int(blockIdx.x % d.tiles);
-  const int64_t at = (int64_t(p.b) * d.D + p.c) * N;
-  const int lane = threadIdx.x;
-  float A[N], G[N], dA[N];
-  load_state<N>(in.A + int64_t(p.c) * N, A);
-#pragma unroll
-  for (int n = 0; n < N; ++n) G[n] = dA[n] = 0.0f;
-  if (dS_T) load_state<N>(dS_T + at, G);
-  const float skip = in.Dskip ? in.Dskip[p.c] : 0.0f, bias = in.dt_bias ? in.dt_bias[p.c] : 0.0f;
-  float dskip = 0.0f, dbias = 0.0f;
-  const float live = p.on ? 1.0f : 0.0f;
-  for (int t = d.T - 1; t >= 0; --t) {
-    const int64_t token = int64_t(p.b) * d.T + t;
-    float* part = bc_parts + ((token * d.G + p.g) * d.tiles + tile) * 2 * N;
-    if (t >= len) {
-      if (p.on) {
-        dx[token * d.D + p.c] = 0.0f;
-        ddt[token * d.D + p.c] = 0.0f;
-        if (dz) dz[token * d.D + p.c] = 0.0f;
-      }
-      if (lane < 2 * N) part[lane] = 0.0f;
-      if (2 * N > kLanes && lane + kLanes < 2 * N) part[lane + kLanes] = 0.0f;
-      continue;
-    }
-    const float x = io<IO>::load(in.x, token * d.x_row + p.c);
-    const float raw = io<IO>::load(in.dt, token * d.dt_row + p.c) + bias;
-    const float delta = step_of<SOFTPLUS>(raw);
-    const float up = io<DY>::load(dy, token * d.D + p.c);
-    const IO* pb = in.Bm + token * d.b_row + p.g * N;
-    const IO* pc = in.Cm + token * d.c_row + p.g * N;
-    const float z = in.z ? io<IO>::load(in.z, token * d.z_row + p.c) : 0.0f;
-    const float q = in.z ? up * act_f32<kActSilu>(z) : up;
-    float S[N], P[N];
-    load_state<N>(states + (token * d.D + p.c) * N, S);
-    if (t > 0) {
-      load_state<N>(states + ((token - 1) * d.D + p.c) * N, P);
-    } else if (in.S0) {
-      load_state<N>(in.S0 + at, P);
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n) P[n] = 0.0f;
-    }
-    float read = skip * x, u = 0.0f, turn = 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const float bn = io<IO>::load(pb, n), cn = io<IO>::load(pc, n);
-      read = __builtin_fmaf(cn, S[n], read);
-      G[n] = __builtin_fmaf(q, cn, G[n]);
-      u = __builtin_fmaf(G[n], bn, u);
-      const float db = lanes_sum<kLanes>(live * G[n] * delta * x), dc = lanes_sum<kLanes>(live * q * S[n]);
-      if (lane == 0) {
-        part[n] = db;
-        part[N + n] = dc;
-      }
-      G[n] *= __builtin_amdgcn_exp2f(delta * (A[n] * kLog2e));
-      const float m = G[n] * P[n];
-      turn = __builtin_fmaf(A[n], m, turn);
-      dA[n] = __builtin_fmaf(m, delta, dA[n]);
-    }
-    const float dd = (turn + u * x) * (SOFTPLUS ? sigmoid_f32(raw) : 1.0f);
-    dskip = __builtin_fmaf(q, x, dskip);
-    dbias += dd;
-    if (p.on) {
-      dx[token * d.D + p.c] = __builtin_fmaf(u, delta, skip * q);
-      ddt[token * d.D + p.c] = dd;
-      if (dz) dz[token * d.D + p.c] = up * read * act_slope_f32<kActSilu>(z);
-    }
+// ---- chunks --------------------------------------------------------------------------
+// A span of tokens cut into chunks, worked on at once: scan_ends_kernel gives each
+// chunk's map S -> exp(A sum delta) S + E (and, for the gradients, the map
+// G -> exp(A sum delta) G + R from the chunk's end to its start, R = sum_t
+// exp(A sum_{s <= t} delta_s) q_t C_t); scan_carry_kernel runs through the chunks
+// and leaves, in their places, the state that enters each chunk and the gradient
+// that enters it from behind.
+struct Chunks {
+  int tokens, count;      // tokens of a chunk (a multiple of kTok), chunks of a sequence
+  float* sums;            // [B, count, D]     sum of delta
+  float* E;               // [B, count, D, N]  E, then the state before the chunk
+  float* R;               // [B, count, D, N]  R, then the gradient behind it (gradients only)
+};
+
+// dy of either type: bits as loaded, shifted into place where it is bf16.
+struct Incoming {
+  const void* dy;
+  bool bf16;
+};
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const Incoming& in, int64_t row, int64_t token, int rows) {
+  return in.bf16 ? rows_at(static_cast<const bf16_t*>(in.dy), row, token, rows) : rows_at(static_cast<const float*>(in.dy), row, token, rows);
+}
+__device__ __forceinline__ float widen(const Incoming& in, uint32_t bits) { return __uint_as_float(in.bf16 ? bits << 16 : bits); }
+
+// Where a wave of scan_ends_kernel or scan_bwd_kernel stands in its channels.
+template <int N>
+struct Cell {
+  int c, s, j;        // channel, four of its states, token of the quad
+  bool on;
+  __device__ __forceinline__ Cell(const ScanDims& d, int g, int tile) {
+    using L = Lanes<N>;
+    const int lane = threadIdx.x % 64, in_group = tile * L::kChannels + lane / L::kPer;
+    on = in_group < d.Dg;
+    c = g * d.Dg + min(in_group, d.Dg - 1);
+    s = lane % L::kPer;
+    j = lane % L::kQuad;
   }
-  if (p.on) {
-    if (dS0) store_state<N>(dS0 + at, G);
-    // a sequence's row: [D, N] of dA, [D] of dD, [D] of ddt_bias
-    float* row = par_parts + int64_t(p.b) * d.D * (N + 2);
-    store_state<N>(row + int64_t(p.c) * N, dA);
-    row[int64_t(d.D) * N + p.c] = dskip;
-    row[int64_t(d.D) * (N + 1) + p.c] = dbias;
+};
+
+constexpr int kEndsWaves = 4;
+
+// One wave a chunk and 256 / N channels.
+template <typename IO, int N, bool SOFTPLUS, bool GRAD>
+__global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, ScanIn<IO> in, bool wide, Incoming up, Chunks k,
+                                                                    int64_t waves) {
+  using L = Lanes<N>;
+  __shared__ float shared[kEndsWaves][2][kShared<N>];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t id = by_xcd(blockIdx.x, gridDim.x) * kEndsWaves + wave;
+  if (id >= waves) return;
+  const int tile = int(id % d.tiles), g = int(id / d.tiles % d.G);
+  const int64_t bc = id / (int64_t(d.tiles) * d.G);     // b count + chunk
+  const int64_t b = bc / k.count;
+  const int first = int(bc % k.count) * k.tokens;
+  const Cell<N> cell(d, g, tile);
+  const int len = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T)), end = min(first + k.tokens, len);
+  float A2[4], E[4] = {0.0f, 0.0f, 0.0f, 0.0f}, R[4] = {0.0f, 0.0f, 0.0f, 0.0f}, P[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sum = 0.0f;
+  four(in.A + int64_t(cell.c) * N + 4 * cell.s, A2);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) A2[n] *= kLog2e;
+  const float bias = in.dt_bias ? in.dt_bias[cell.c] : 0.0f;
+  float* Bs = shared[wave][0];
+  float* Cs = shared[wave][1];
+  const Offsets<IO, N> offsets(d, g, cell.c);
+  const int up_size = up.bf16 ? 2 : 4, up_at = (cell.j * d.D + cell.c) * up_size;
+  Tokens<IO, N> next;
+  uint32_t up_next[L::kRegs] = {};
+  auto load = [&](int t0) {
+    load_tokens<IO, N>(d, in, b, t0, end, wide, offsets, next);
+    if constexpr (GRAD) {
+      const auto r = rows_at(up, d.D, b * d.T + t0, min(end - t0, kTok));
+      if (up.bf16) {
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) up_next[i] = load_bits<bf16_t>(r, up_at + i * L::kQuad * d.D * 2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) up_next[i] = load_bits<float>(r, up_at + i * L::kQuad * d.D * 4);
+      }
+    }
+  };
+  if (first < end) load(first);
+  for (int t0 = first; t0 < end; t0 += kTok) {
+    float delta[L::kRegs], u[L::kRegs], q[L::kRegs];
+    stage_shared<IO, N>(next, Bs, Cs);
+#pragma unroll
+    for (int i = 0; i < L::kRegs; ++i) {
+      delta[i] = kept(step_of<SOFTPLUS>(widen(next.dt[i]) + bias), t0 + L::kQuad * i + cell.j < end);
+      u[i] = delta[i] * widen(next.x[i]);
+      sum += delta[i];
+      if constexpr (GRAD) {
+        q[i] = widen(up, up_next[i]);
+        if (in.z) q[i] *= act_f32<kActSilu>(widen(next.z[i]));
+      }
+    }
+    if (t0 + kTok < end) load(t0 + kTok);
+    __builtin_amdgcn_wave_barrier();
+    each_token<L::kQuad>([&](auto t, auto jj, auto i) {
+      const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
+      float bt[4], a[4];
+      four(Bs + t() * N + 4 * cell.s, bt);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        a[n] = __builtin_amdgcn_exp2f(dt * A2[n]);
+        E[n] = __builtin_fmaf(a[n], E[n], ut * bt[n]);
+      }
+      if constexpr (GRAD) {
+        const float qt = from_lane<L::kQuad, jj()>(q[i()]);
+        float ct[4];
+        four(Cs + t() * N + 4 * cell.s, ct);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          P[n] *= a[n];
+          R[n] = __builtin_fmaf(P[n], qt * ct[n], R[n]);
+        }
+      }
+    });
+    __builtin_amdgcn_wave_barrier();
+  }
+  sum = lanes_sum<L::kQuad>(sum);
+  if (cell.on) {
+    const int64_t at = (bc * d.D + cell.c) * N + 4 * cell.s;
+    *reinterpret_cast<float4*>(k.E + at) = make_float4(E[0], E[1], E[2], E[3]);
+    if constexpr (GRAD) *reinterpret_cast<float4*>(k.R + at) = make_float4(R[0], R[1], R[2], R[3]);
+    if (cell.s == 0) k.sums[bc * d.D + cell.c] = sum;
   }
 }
 
-// dB, dC of every token and group from its waves' rows.
-__global__ __launch_bounds__(256) void scan_bc_kernel(const float* __restrict__ parts, int tiles, int N, int64_t n, float* __restrict__ dB,
+// One thread a state.  Loads run kAhead chunks in front.
+constexpr int kAhead = 8;
+template <bool GRAD>
+__global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t states, Chunks k, const float* __restrict__ A,
+                                                         const float* __restrict__ S0, const float* __restrict__ dS_T,
+                                                         float* __restrict__ dS0) {
+  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= states) return;
+  const int64_t DN = int64_t(D) * N, b = id / DN, dn = id - b * DN;
+  const int c = int(dn / N);
+  const float A2 = A[dn] * kLog2e;
+  const int64_t first = b * k.count;
+  float H = S0 ? S0[id] : 0.0f;
+  for (int k0 = 0; k0 < k.count; k0 += kAhead) {
+    float sum[kAhead], E[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = first + min(k0 + i, k.count - 1);
+      sum[i] = k.sums[at * D + c];
+      E[i] = k.E[at * DN + dn];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i < k.count) {
+        k.E[(first + k0 + i) * DN + dn] = H;
+        H = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * sum[i]), H, E[i]);
+      }
+  }
+  if constexpr (GRAD) {
+    float G = dS_T ? dS_T[id] : 0.0f;
+    for (int k0 = k.count - 1; k0 >= 0; k0 -= kAhead) {
+      float sum[kAhead], R[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t at = first + max(k0 - i, 0);
+        sum[i] = k.sums[at * D + c];
+        R[i] = k.R[at * DN + dn];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (k0 - i >= 0) {
+          k.R[(first + k0 - i) * DN + dn] = G;
+          G = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * sum[i]), G, R[i]);
+        }
+    }
+    if (dS0) dS0[id] = G;
+  }
+}
+
+// ---- gradients ----------------------------------------------------------------------
+// A workgroup takes one chunk of one group and, four waves side by side, its
+// channels, 4 x 256 / N at a time.  A wave first runs forward over the chunk for
+// the state before each sixteen tokens, then takes the sixteens from the last to
+// the first: forward again (decays and states in registers), then back with G.
+// What sums over channels (dB, dC) is summed over the wave's lanes by lane swaps
+// and over its channel tiles in LDS, over the waves at the end, in this order;
+// workgroups of other channels leave rows of partial sums.  What sums over tokens
+// (dA, dD, ddt_bias) leaves as one row a chunk.
+constexpr int kBwdWaves = 4;
+template <int N>
+constexpr int kChunkTokens = N <= 16 ? 64 : 1024 / N;   // so that LDS holds the sums of 2 N a token and wave
+
+// Sum of v[0..3] over the wave's channels, one of the four sums in each row of 16
+// lanes: row r gets v[kRowOf[r]], in every lane of the same state four.
+template <int N>
+__device__ __forceinline__ float channels_sum(const float (&v)[4]) {
+  auto swap32 = [](float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  auto swap16 = [](float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  float w = swap16(swap32(v[0], v[1]), swap32(v[2], v[3]));
+  if constexpr (Lanes<N>::kPer <= 2) w = dpp_plus<0x4e>(w);    // quad_perm [2, 3, 0, 1]
+  if constexpr (Lanes<N>::kPer <= 4) w = dpp_plus<0x124>(w);   // row_ror 4
+  if constexpr (Lanes<N>::kPer <= 8) w = dpp_plus<0x128>(w);   // row_ror 8
+  return w;
+}
+// The state of its four that a lane's row of 16 holds after channels_sum.
+__device__ __forceinline__ int row_state(int lane) {
+  const int r = lane / 16;
+  return (r & 1) * 2 + (r >> 1);
+}
+
+struct ScanGrads {
+  float* dx;
+  float* ddt;
+  float* dz;
+  float* bc;       // dB and dC, or rows of partial sums: [sets][B T][G][2][N]
+  float* params;   // [B count][D (N + 2)]: dA, dD, ddt_bias of a chunk
+};
+
+template <typename IO, int N, bool SOFTPLUS>
+__global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d, ScanIn<IO> in, bool wide, Incoming up, Chunks k,
+                                                                    ScanGrads out, int sets) {
+  using L = Lanes<N>;
+  constexpr int kTokens = kChunkTokens<N>, kSub = kTokens / kTok;
+  __shared__ float shared[2][kTokens * N];                  // B, C of the chunk
+  __shared__ float bc[kBwdWaves][kTokens][2][N];            // dB, dC
+  __shared__ float4 before[kBwdWaves][kSub][64];            // the state before each sixteen
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int64_t id = by_xcd(blockIdx.x, gridDim.x);
+  const int set = int(id % sets), g = int(id / sets % d.G);
+  const int64_t chunk = id / (int64_t(sets) * d.G), b = chunk / k.count;
+  const int first = int(chunk % k.count) * kTokens;
+  const int len = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T));
+
+  for (int i = threadIdx.x; i < kTokens * N; i += 64 * kBwdWaves) {
+    const int t = first + i / N;
+    const bool live = t < len;
+    const int64_t token = b * d.T + min(t, len - 1);
+    shared[0][i] = live ? io<IO>::load(in.Bm, token * d.b_row + g * N + i % N) : 0.0f;
+    shared[1][i] = live ? io<IO>::load(in.Cm, token * d.c_row + g * N + i % N) : 0.0f;
+  }
+  for (int i = threadIdx.x; i < kBwdWaves * kTokens * 2 * N; i += 64 * kBwdWaves) (&bc[0][0][0][0])[i] = 0.0f;
+  __syncthreads();
+
+  const int groups = (d.tiles + kBwdWaves - 1) / kBwdWaves;      // of kBwdWaves tiles each
+  for (int tg = set; tg < groups; tg += sets) {
+    const int tile = tg * kBwdWaves + wave;
+    if (tile >= d.tiles) continue;
+    const Cell<N> cell(d, g, tile);
+    const int s = cell.s, j = cell.j;
+    const int64_t at = (chunk * d.D + cell.c) * N + 4 * s;
+    float A[4], A2[4], h[4], G[4], dA[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dskip = 0.0f, dbias = 0.0f;
+    four(in.A + int64_t(cell.c) * N + 4 * s, A);
+    four(k.E + at, h);
+    four(k.R + at, G);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) A2[n] = A[n] * kLog2e;
+    const float skip = in.Dskip ? in.Dskip[cell.c] : 0.0f, bias = in.dt_bias ? in.dt_bias[cell.c] : 0.0f;
+    const int es = sizeof(IO);
+    const int x_at = (j * int(d.x_row) + cell.c) * es, dt_at = (j * int(d.dt_row) + cell.c) * es, z_at = (j * int(d.z_row) + cell.c) * es;
+    const int up_at = (j * d.D + cell.c) * (up.bf16 ? 2 : 4);
+    const int out_at = cell.on && s < L::kQuad ? (j * d.D + cell.c) * 4 : kNowhere;
+
+    // the state before each sixteen
+    for (int m = 0; m < kSub; ++m) {
+      before[wave][m][lane] = make_float4(h[0], h[1], h[2], h[3]);
+      if (m == kSub - 1) break;
+      const int t0 = first + m * kTok;
+      const auto rx = rows_at(in.x, d.x_row, b * d.T + t0, min(len - t0, kTok)), rdt = rows_at(in.dt, d.dt_row, b * d.T + t0, min(len - t0, kTok));
+      float delta[L::kRegs], u[L::kRegs];
+      bits_t<IO> xb[L::kRegs], db[L::kRegs];
+#pragma unroll
+      for (int i = 0; i < L::kRegs; ++i) {
+        xb[i] = load_bits<IO>(rx, x_at + i * L::kQuad * int(d.x_row) * es);
+        db[i] = load_bits<IO>(rdt, dt_at + i * L::kQuad * int(d.dt_row) * es);
+      }
+#pragma unroll
+      for (int i = 0; i < L::kRegs; ++i) {
+        delta[i] = kept(step_of<SOFTPLUS>(widen(db[i]) + bias), t0 + L::kQuad * i + j < len);
+        u[i] = delta[i] * widen(xb[i]);
+      }
+      each_token<L::kQuad>([&](auto t, auto jj, auto i) {
+        const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
+        float bt[4];
+        four(&shared[0][(m * kTok + t()) * N + 4 * s], bt);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * A2[n]), h[n], ut * bt[n]);
+      });
+    }
+
+    for (int m = kSub - 1; m >= 0; --m) {
+      const int t0 = first + m * kTok;
+      const int64_t token = b * d.T + t0;
+      const int rows = min(len - t0, kTok);
+      float delta[L::kRegs], x[L::kRegs], u[L::kRegs], q[L::kRegs], dy[L::kRegs], z[L::kRegs], raw[L::kRegs];
+      {
+        const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows), ru = rows_at(up, d.D, token, rows);
+        bits_t<IO> xb[L::kRegs], db[L::kRegs], zb[L::kRegs];
+        uint32_t ub[L::kRegs];
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) {
+          xb[i] = load_bits<IO>(rx, x_at + i * L::kQuad * int(d.x_row) * es);
+          db[i] = load_bits<IO>(rdt, dt_at + i * L::kQuad * int(d.dt_row) * es);
+        }
+        if (up.bf16) {
+#pragma unroll
+          for (int i = 0; i < L::kRegs; ++i) ub[i] = load_bits<bf16_t>(ru, up_at + i * L::kQuad * d.D * 2);
+        } else {
+#pragma unroll
+          for (int i = 0; i < L::kRegs; ++i) ub[i] = load_bits<float>(ru, up_at + i * L::kQuad * d.D * 4);
+        }
+        if (in.z) {
+          const auto rz = rows_at(in.z, d.z_row, token, rows);
+#pragma unroll
+          for (int i = 0; i < L::kRegs; ++i) zb[i] = load_bits<IO>(rz, z_at + i * L::kQuad * int(d.z_row) * es);
+        }
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) {
+          x[i] = widen(xb[i]);
+          raw[i] = widen(db[i]) + bias;
+          delta[i] = kept(step_of<SOFTPLUS>(raw[i]), t0 + L::kQuad * i + j < len);
+          u[i] = delta[i] * x[i];
+          dy[i] = widen(up, ub[i]);
+          z[i] = in.z ? widen(zb[i]) : 0.0f;
+          q[i] = in.z ? dy[i] * act_f32<kActSilu>(z[i]) : dy[i];
+        }
+      }
+      // forward: the decays, and the state before every token
+      float a[kTok][4], prev[kTok][4];
+      four(reinterpret_cast<const float*>(&before[wave][m][lane]), h);
+      each_token<L::kQuad>([&](auto t, auto jj, auto i) {
+        const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
+        float bt[4];
+        four(&shared[0][(m * kTok + t()) * N + 4 * s], bt);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          prev[t()][n] = h[n];
+          a[t()][n] = __builtin_amdgcn_exp2f(dt * A2[n]);
+          h[n] = __builtin_fmaf(a[t()][n], h[n], ut * bt[n]);
+        }
+      });
+      // back
+      float du[L::kRegs], turn[L::kRegs], read[L::kRegs];
+      each_token<L::kQuad>([&](auto back, auto, auto) {
+        constexpr int t = kTok - 1 - back(), i = t / L::kQuad, jj = t % L::kQuad;
+        const float dt = from_lane<L::kQuad, jj>(delta[i]), ut = from_lane<L::kQuad, jj>(u[i]), qt = from_lane<L::kQuad, jj>(q[i]);
+        float bt[4], ct[4], vb[4], vc[4], r = 0.0f, su = 0.0f, st = 0.0f;
+        four(&shared[0][(m * kTok + t) * N + 4 * s], bt);
+        four(&shared[1][(m * kTok + t) * N + 4 * s], ct);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          float now;                                  // the state after token t
+          if constexpr (t == kTok - 1) {
+            now = h[n];
+          } else {
+            now = prev[t + 1][n];
+          }
+          G[n] = __builtin_fmaf(qt, ct[n], G[n]);
+          r = __builtin_fmaf(ct[n], now, r);
+          su = __builtin_fmaf(G[n], bt[n], su);
+          vb[n] = cell.on ? G[n] * ut : 0.0f;
+          vc[n] = cell.on ? qt * now : 0.0f;
+          G[n] *= a[t][n];
+          const float mt = G[n] * prev[t][n];
+          st = __builtin_fmaf(A[n], mt, st);
+          dA[n] = __builtin_fmaf(mt, dt, dA[n]);
+        }
+        const float wb = channels_sum<N>(vb), wc = channels_sum<N>(vc);
+        if (lane % 16 < L::kPer) {
+          float* at_bc = &bc[wave][m * kTok + t][0][4 * s + row_state(lane)];
+          __hip_atomic_fetch_add(at_bc, wb, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+          __hip_atomic_fetch_add(at_bc + N, wc, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+        r = lanes_sum<L::kPer>(r);
+        su = lanes_sum<L::kPer>(su);
+        st = lanes_sum<L::kPer>(st);
+        const bool first_of_four = jj == L::kQuad - 1;
+        read[i] = first_of_four || j == jj ? r : read[i];
+        du[i] = first_of_four || j == jj ? su : du[i];
+        turn[i] = first_of_four || j == jj ? st : turn[i];
+      });
+      const int all = min(d.T - t0, kTok);
+      const auto rdx = rows_at(out.dx, d.D, token, all), rddt = rows_at(out.ddt, d.D, token, all);
+#pragma unroll
+      for (int i = 0; i < L::kRegs; ++i) {
+        const int o = out_at == kNowhere ? kNowhere : out_at + i * L::kQuad * d.D * 4;
+        const float dd = kept((turn[i] + du[i] * x[i]) * (SOFTPLUS ? sigmoid_f32(raw[i]) : 1.0f), t0 + L::kQuad * i + j < len);
+        dskip = __builtin_fmaf(q[i], x[i], dskip);
+        dbias += dd;
+        store_one<float>(rdx, o, __builtin_fmaf(du[i], delta[i], skip * q[i]));
+        store_one<float>(rddt, o, dd);
+      }
+      if (out.dz) {
+        const auto rdz = rows_at(out.dz, d.D, token, all);
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i)
+          store_one<float>(rdz, out_at == kNowhere ? kNowhere : out_at + i * L::kQuad * d.D * 4,
+                           dy[i] * __builtin_fmaf(skip, x[i], read[i]) * act_slope_f32<kActSilu>(z[i]));
+      }
+    }
+    dskip = lanes_sum<L::kQuad>(dskip);
+    dbias = lanes_sum<L::kQuad>(dbias);
+    if (cell.on) {
+      float* row = out.params + chunk * d.D * (N + 2);
+      *reinterpret_cast<float4*>(row + int64_t(cell.c) * N + 4 * s) = make_float4(dA[0], dA[1], dA[2], dA[3]);
+      if (s == 0) {
+        row[int64_t(d.D) * N + cell.c] = dskip;
+        row[int64_t(d.D) * (N + 1) + cell.c] = dbias;
+      }
+    }
+  }
+  __syncthreads();
+  float* rows = out.bc + int64_t(set) * d.B * d.T * d.G * 2 * N;
+  for (int i = threadIdx.x; i < kTokens * 2 * N; i += 64 * kBwdWaves) {
+    const int t = first + i / (2 * N);
+    if (t >= d.T) break;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBwdWaves; ++w) v += (&bc[w][0][0][0])[i];
+    rows[((b * d.T + t) * d.G + g) * 2 * N + i % (2 * N)] = v;
+  }
+}
+
+// dB, dC of every token and group from the sets' rows.
+__global__ __launch_bounds__(256) void scan_bc_kernel(const float* __restrict__ parts, int sets, int N, int64_t n, float* __restrict__ dB,
                                                       float* __restrict__ dC) {
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
     const int64_t tg = i / (2 * N);
     const int k = int(i % (2 * N));
     float s = 0.0f;
-    for (int j = 0; j < tiles; ++j) s += parts[(tg * tiles + j) * 2 * N + k];
+    for (int j = 0; j < sets; ++j) s += parts[j * n + i];
     if (k < N) {
       dB[tg * N + k] = s;
     } else {
@@ -561,28 +852,12 @@ __global__ __launch_bounds__(256) void scan_bc_kernel(const float* __restrict__ 
   }
 }
 
-// dA, dD and ddt_bias from the sequences' rows.
-__global__ __launch_bounds__(256) void scan_params_kernel(const float* __restrict__ parts, int rows, int D, int N, float* __restrict__ dA,
-                                                          float* __restrict__ dD, float* __restrict__ ddt_bias) {
-  const int64_t n = int64_t(D) * (N + 2);
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-    double s = 0.0;
-    for (int r = 0; r < rows; ++r) s += parts[r * n + i];
-    if (i < int64_t(D) * N) {
-      dA[i] = float(s);
-    } else if (i < int64_t(D) * (N + 1)) {
-      if (dD) dD[i - int64_t(D) * N] = float(s);
-    } else if (ddt_bias) {
-      ddt_bias[i - int64_t(D) * (N + 1)] = float(s);
-    }
-  }
-}
-
+// Channels a wave: 256 / N.
 ScanDims dims_of(const ScanArgs& a) {
   ScanDims d{};
   d.B = a.B; d.T = a.T; d.D = a.D; d.G = a.G;
   d.Dg = a.D / a.G;
-  d.tiles = (d.Dg + kLanes - 1) / kLanes;
+  d.tiles = (d.Dg + 256 / a.N - 1) / (256 / a.N);
   d.x_row = a.x_row; d.dt_row = a.dt_row; d.z_row = a.z_row; d.b_row = a.b_row; d.c_row = a.c_row;
   return d;
 }
@@ -600,8 +875,7 @@ bool fours_wide(const ScanArgs& a) { return a.b_row % 4 == 0 && a.c_row % 4 == 0
 
 template <typename IO, int N, bool SP>
 hipError_t fwd_typed(const ScanArgs& a, hipStream_t st) {
-  ScanDims d = dims_of(a);
-  d.tiles = (d.Dg + Lanes<N>::kChannels - 1) / Lanes<N>::kChannels;
+  const ScanDims d = dims_of(a);
   const int64_t blocks = int64_t(a.B) * a.G * d.tiles;
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
   scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kFwdWaves), 0, st>>>(d, inputs_of<IO>(a), fours_wide(a),
@@ -618,35 +892,67 @@ hipError_t step_typed(const ScanArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-int64_t states_floats(const ScanArgs& a) { return int64_t(a.B) * a.T * a.D * a.N; }
-int64_t bc_floats(const ScanArgs& a) { return int64_t(a.B) * a.T * a.G * dims_of(a).tiles * 2 * a.N; }
-int64_t params_floats(const ScanArgs& a) { return int64_t(a.B) * a.D * (a.N + 2); }
-
-template <typename IO, typename DY, int N, bool SP>
-hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
+// The backward's workspace: the chunks' maps, partial sums of dB and dC, and the
+// chunks' rows of parameter gradients.
+struct BwdShape {
+  int tokens, count, sets;
+  int64_t sums, states, bc, params;   // floats of each part (sums padded to 16 bytes)
+};
+BwdShape bwd_shape(const ScanArgs& a) {
+  BwdShape s{};
+  s.tokens = a.N <= 16 ? 64 : 1024 / a.N;
+  s.count = (a.T + s.tokens - 1) / s.tokens;
+  const int64_t chunks = int64_t(a.B) * s.count;
   const ScanDims d = dims_of(a);
-  const int64_t waves = int64_t(a.B) * a.G * d.tiles;
-  float* states = a.workspace;
-  float* bc = states + states_floats(a);
-  float* par = bc + bc_floats(a);
+  const int64_t groups = (d.tiles + kBwdWaves - 1) / kBwdWaves;
+  // two workgroups a CU fill the card; more only add rows of partial sums
+  s.sets = int(std::min<int64_t>(std::max<int64_t>(groups, 1), std::max<int64_t>(1, (512 + chunks * a.G - 1) / std::max<int64_t>(1, chunks * a.G))));
+  s.sums = (chunks * a.D + 3) / 4 * 4;
+  s.states = chunks * a.D * a.N;
+  s.bc = int64_t(s.sets) * a.B * a.T * a.G * 2 * a.N;
+  s.params = (chunks * a.D * (a.N + 2) + 3) / 4 * 4;
+  return s;
+}
+
+template <typename IO, int N, bool SP>
+hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
+  static_assert(kChunkTokens<N> == (N <= 16 ? 64 : 1024 / N));
+  const ScanDims d = dims_of(a);
+  const BwdShape s = bwd_shape(a);
+  Chunks k{s.tokens, s.count, nullptr, a.workspace, a.workspace + s.states};
+  float* bc = k.R + s.states;
+  float* params = bc + s.bc;
+  k.sums = params + s.params;
+  const int64_t chunks = int64_t(a.B) * s.count, states = int64_t(a.B) * a.D * N;
+  const ScanIn<IO> in = inputs_of<IO>(a);
+  const Incoming up{a.dy, a.dy_bf16};
+  const int64_t waves = chunks * a.G * d.tiles, ends = (waves + kEndsWaves - 1) / kEndsWaves, blocks = chunks * a.G * s.sets;
+  if (ends > kMaxGrid || blocks > kMaxGrid || (states + 255) / 256 > kMaxGrid) return hipErrorInvalidValue;
   hipError_t e = hipSuccess;
-  if (waves > kMaxGrid) return hipErrorInvalidValue;
-  if (waves > 0) {
-    scan_states_kernel<IO, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), states);
-    scan_bwd_kernel<IO, DY, N, SP><<<dim3(unsigned(waves)), dim3(64), 0, st>>>(d, inputs_of<IO>(a), static_cast<const DY*>(a.dy), a.dS_T,
-                                                                              states, a.dx, a.ddt, a.dz, a.dS0, bc, par);
+  if (ends > 0) {
+    scan_ends_kernel<IO, N, SP, true><<<dim3(unsigned(ends)), dim3(64 * kEndsWaves), 0, st>>>(d, in, fours_wide(a), up, k, waves);
     e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess) return e;
+  if (states > 0) {
+    scan_carry_kernel<true><<<dim3(unsigned((states + 255) / 256)), dim3(256), 0, st>>>(a.D, N, states, k, a.A, a.S0, a.dS_T, a.dS0);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (blocks > 0) {
+    const ScanGrads out{a.dx, a.ddt, a.dz, bc, params};
+    scan_bwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kBwdWaves), 0, st>>>(d, in, fours_wide(a), up, k, out, s.sets);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const int64_t n = int64_t(a.B) * a.T * a.G * 2 * N;
   if (n > 0) {
-    scan_bc_kernel<<<dim3(unsigned(std::min<int64_t>((n + 255) / 256, 1 << 16))), dim3(256), 0, st>>>(bc, d.tiles, N, n, a.dB, a.dC);
+    scan_bc_kernel<<<dim3(unsigned(std::min<int64_t>((n + 255) / 256, 1 << 16))), dim3(256), 0, st>>>(bc, s.sets, N, n, a.dB, a.dC);
     e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess) return e;
-  scan_params_kernel<<<dim3(unsigned(std::min<int64_t>((int64_t(a.D) * (N + 2) + 255) / 256, 1 << 16))), dim3(256), 0, st>>>(
-      par, a.B, a.D, N, a.dA, a.dD, a.ddt_bias);
-  return hipGetLastError();
+  const int64_t DN = int64_t(a.D) * N;
+  return launch_sum_parts({params, chunks, DN + 2 * a.D, {a.dA, a.dD, a.ddt_bias}, {DN, DN + a.D}}, st);
 }
 
 // Calls go(N, softplus) with compile-time values.
@@ -679,13 +985,13 @@ hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st) {
 }
 
 size_t scan_bwd_workspace_bytes(const ScanArgs& a) {
-  return size_t(states_floats(a) + bc_floats(a) + params_floats(a)) * sizeof(float);
+  const BwdShape s = bwd_shape(a);
+  return size_t(2 * s.states + s.bc + s.params + s.sums) * sizeof(float);
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st) {
   return by_size(a, [&](auto n, auto sp) {
-    if (a.bf16) return a.dy_bf16 ? bwd_typed<bf16_t, bf16_t, n(), sp()>(a, st) : bwd_typed<bf16_t, float, n(), sp()>(a, st);
-    return a.dy_bf16 ? bwd_typed<float, bf16_t, n(), sp()>(a, st) : bwd_typed<float, float, n(), sp()>(a, st);
+    return a.bf16 ? bwd_typed<bf16_t, n(), sp()>(a, st) : bwd_typed<float, n(), sp()>(a, st);
   });
 }
 
