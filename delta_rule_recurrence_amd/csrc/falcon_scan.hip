@@ -57,6 +57,20 @@ __device__ __forceinline__ void store_state(float* p, const float (&s)[N]) {
 template <bool SOFTPLUS>
 __device__ __forceinline__ float step_of(float v) { return SOFTPLUS ? softplus_f32(v) : v; }
 
+// ---- chunks --------------------------------------------------------------------------
+// A span of tokens cut into chunks, worked on at once: scan_ends_kernel gives each
+// chunk's map S -> exp(A sum delta) S + E (and, for the gradients, the map
+// G -> exp(A sum delta) G + R from the chunk's end to its start, R = sum_t
+// exp(A sum_{s <= t} delta_s) q_t C_t); scan_carry_kernel runs through the chunks
+// and leaves, in their places, the state that enters each chunk and the gradient
+// that enters it from behind.
+struct Chunks {
+  int tokens, count;      // tokens of a chunk (a multiple of kTok), chunks of a sequence
+  float* sums;            // [B, count, D]     sum of delta
+  float* E;               // [B, count, D, N]  E, then the state before the chunk
+  float* R;               // [B, count, D, N]  R, then the gradient behind it (gradients only)
+};
+
 // ---- prompts ----------------------------------------------------------------------
 // A lane owns four states of one channel: N / 4 lanes a channel, 256 / N channels
 // a wave.  A workgroup's kFwdWaves waves take sixteen tokens in turn.  What does
@@ -152,7 +166,8 @@ __device__ __forceinline__ float4 widen_four(const uint32_t (&v)[kFourWords<E>])
     return make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
   }
 }
-constexpr int kNowhere = 0x7ffffff0;   // an offset behind every buffer
+// An offset behind every buffer, also with 2^30 added (offsets are unsigned).
+constexpr int kNowhere = 0x7ffffff0;
 
 // A lane's byte offsets into sixteen rows: its tokens' rows of the tensors a
 // channel wide, and its fours of B and C.
@@ -274,13 +289,14 @@ constexpr int kFwdWaves = 4;
 __device__ __forceinline__ bool wait_turn(const int* at, int turn, int limit) {
   for (int polls = 0; __hip_atomic_load(at, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < turn; ++polls) {
     if (polls >= limit) return false;
+    __builtin_amdgcn_s_sleep(1);
   }
   return true;
 }
 
 template <typename IO, int N, bool SOFTPLUS>
 __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void scan_fwd_kernel(
-    ScanDims d, ScanIn<IO> in, bool wide, IO* __restrict__ y, float* __restrict__ S_T, int limit) {
+    ScanDims d, ScanIn<IO> in, bool wide, Chunks k, IO* __restrict__ y, float* __restrict__ S_T, int limit) {
   using L = Lanes<N>;
   __shared__ float shared[kFwdWaves][2][kShared<N>];      // B, C of a wave's tokens
   __shared__ float4 passed[64];                         // the state on its way to the next wave
@@ -288,14 +304,21 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int64_t id = by_xcd(blockIdx.x, gridDim.x);
   const int tile = int(id % d.tiles), g = int(id / d.tiles % d.G);
-  const int64_t b = id / (int64_t(d.tiles) * d.G);
+  const int64_t bc = id / (int64_t(d.tiles) * d.G), b = bc / k.count;   // b count + chunk
   const int in_group = tile * L::kChannels + lane / L::kPer;
   const bool on = in_group < d.Dg;
   const int c = g * d.Dg + min(in_group, d.Dg - 1), s = lane % L::kPer, j = lane % L::kQuad;
-  const int len = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T));
+  const int whole = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T));
+  const int first = int(bc % k.count) * k.tokens, len = min(first + k.tokens, whole);   // this chunk: [first, len)
   const int64_t at = (b * d.D + c) * N + 4 * s;
   float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A2[4];
-  if (in.S0 && wave == 0) four(in.S0 + at, h);
+  if (wave == 0) {
+    if (k.E) {
+      four(k.E + (bc * d.D + c) * N + 4 * s, h);
+    } else if (in.S0) {
+      four(in.S0 + at, h);
+    }
+  }
   four(in.A + int64_t(c) * N + 4 * s, A2);
 #pragma unroll
   for (int n = 0; n < 4; ++n) A2[n] *= kLog2e;
@@ -303,14 +326,14 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   float* Bs = shared[wave][0];
   float* Cs = shared[wave][1];
   const Offsets<IO, N> offsets(d, g, c);
-  const int y_at = on && s < L::kQuad ? (j * d.D + c) * int(sizeof(IO)) : kNowhere;
+  const uint32_t y_at = on && s < L::kQuad ? (j * d.D + c) * int(sizeof(IO)) : kNowhere;
 
   Tokens<IO, N> next;
-  if (wave * kTok < len) load_tokens<IO, N>(d, in, b, wave * kTok, len, wide, offsets, next);
+  if (first + wave * kTok < len) load_tokens<IO, N>(d, in, b, first + wave * kTok, len, wide, offsets, next);
   if (threadIdx.x == 0) turns = 0;
   __syncthreads();
-  for (int turn = wave; turn * kTok < len; turn += kFwdWaves) {
-    const int t0 = turn * kTok;
+  for (int turn = wave; first + turn * kTok < len; turn += kFwdWaves) {
+    const int t0 = first + turn * kTok;
     float delta[L::kRegs], x[L::kRegs], gate[L::kRegs], u[L::kRegs];
     stage_shared<IO, N>(next, Bs, Cs);
 #pragma unroll
@@ -329,6 +352,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
 #pragma unroll
       for (int n = 0; n < 4; ++n) v[t()][n] = __builtin_amdgcn_exp2f(dt * A2[n]);
     });
+    // (kept from sinking below the wait)
+#pragma unroll
+    for (int t = 0; t < kTok; ++t)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) asm volatile("" : "+v"(v[t][n]));
     __builtin_amdgcn_wave_barrier();
     float rows[4][4];
     four_rows<N>(Bs + 4 * s, 0, rows);
@@ -364,13 +392,14 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
     const auto ry = rows_at(y, d.D, b * d.T + t0, min(len - t0, kTok));
 #pragma unroll
     for (int i = 0; i < L::kRegs; ++i)
-      store_one<IO>(ry, y_at == kNowhere ? kNowhere : y_at + i * L::kQuad * d.D * int(sizeof(IO)),
+      store_one<IO>(ry, y_at + uint32_t(i * L::kQuad) * d.D * sizeof(IO),
                     __builtin_fmaf(skip, x[i], read[i]) * gate[i]);
     __builtin_amdgcn_wave_barrier();
   }
-  // the wave that ran the last tokens (wave 0 where there are none) has the end
-  const int last = len > 0 ? (len - 1) / kTok % kFwdWaves : 0;
-  if (S_T && wave == last && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(h[0], h[1], h[2], h[3]);
+  // the end is with the wave that ran the last tokens (wave 0 of the first chunk
+  // where there are none)
+  const bool holds = whole > 0 ? len == whole && first < whole && wave == (whole - 1 - first) / kTok % kFwdWaves : first == 0 && wave == 0;
+  if (S_T && holds && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(h[0], h[1], h[2], h[3]);
 }
 
 // ---- one token --------------------------------------------------------------------
@@ -410,20 +439,6 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanDims d, ScanIn<IO> i
     }
   }
 }
-
-// ---- chunks --------------------------------------------------------------------------
-// A span of tokens cut into chunks, worked on at once: scan_ends_kernel gives each
-// chunk's map S -> exp(A sum delta) S + E (and, for the gradients, the map
-// G -> exp(A sum delta) G + R from the chunk's end to its start, R = sum_t
-// exp(A sum_{s <= t} delta_s) q_t C_t); scan_carry_kernel runs through the chunks
-// and leaves, in their places, the state that enters each chunk and the gradient
-// that enters it from behind.
-struct Chunks {
-  int tokens, count;      // tokens of a chunk (a multiple of kTok), chunks of a sequence
-  float* sums;            // [B, count, D]     sum of delta
-  float* E;               // [B, count, D, N]  E, then the state before the chunk
-  float* R;               // [B, count, D, N]  R, then the gradient behind it (gradients only)
-};
 
 // dy of either type: bits as loaded, shifted into place where it is bf16.
 struct Incoming {
@@ -873,13 +888,54 @@ constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
 // Fours of B and C lie on multiples of a four's size.
 bool fours_wide(const ScanArgs& a) { return a.b_row % 4 == 0 && a.c_row % 4 == 0; }
 
+// Chunks of the forward.  One where there are channels for more than kCutBelow
+// workgroups or fewer than kCutFrom tokens; else enough for kCutInto workgroups.
+// Cutting works out every decay twice and takes two launches more, so it pays only
+// where a long chain of turns would leave most of the card idle (D = 1536, N = 16,
+// us, one chunk against cut): B = 1: T = 256: 12 and 19, T = 1024: 34 and 29,
+// T = 4096: 119 and 74; B = 2: T = 1024: 34 and 43, T = 4096: 119 and 127.
+constexpr int64_t kCutBelow = 128, kCutInto = 1536;
+constexpr int kCutFrom = 768;
+struct FwdShape {
+  int tokens, count;
+  int64_t sums, states;   // floats of the workspace's parts (sums padded to 16 bytes)
+};
+FwdShape fwd_shape(const ScanArgs& a) {
+  const ScanDims d = dims_of(a);
+  const int64_t blocks = int64_t(a.B) * a.G * d.tiles;
+  FwdShape s{std::max(a.T, 1), 1, 0, 0};
+  if (blocks == 0 || blocks > kCutBelow || a.T < kCutFrom) return s;
+  constexpr int kRound = kFwdWaves * kTok;   // tokens of one turn of every wave
+  const int64_t want = std::min<int64_t>((kCutInto + blocks - 1) / blocks, a.T / kRound);
+  s.tokens = int(((a.T + want - 1) / want + kRound - 1) / kRound * kRound);
+  s.count = (a.T + s.tokens - 1) / s.tokens;
+  s.sums = (int64_t(a.B) * s.count * a.D + 3) / 4 * 4;
+  s.states = int64_t(a.B) * s.count * a.D * a.N;
+  return s;
+}
+
 template <typename IO, int N, bool SP>
 hipError_t fwd_typed(const ScanArgs& a, hipStream_t st) {
   const ScanDims d = dims_of(a);
-  const int64_t blocks = int64_t(a.B) * a.G * d.tiles;
+  const FwdShape s = fwd_shape(a);
+  const int64_t blocks = int64_t(a.B) * s.count * a.G * d.tiles;
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
-  scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kFwdWaves), 0, st>>>(d, inputs_of<IO>(a), fours_wide(a),
-                                                                                     static_cast<IO*>(a.y), a.S_T, a.spin_limit);
+  const ScanIn<IO> in = inputs_of<IO>(a);
+  Chunks k{s.tokens, s.count, nullptr, nullptr, nullptr};
+  if (s.count > 1) {
+    k.E = a.workspace;
+    k.sums = k.E + s.states;
+    const int64_t states = int64_t(a.B) * a.D * N;
+    scan_ends_kernel<IO, N, SP, false><<<dim3(unsigned((blocks + kEndsWaves - 1) / kEndsWaves)), dim3(64 * kEndsWaves), 0, st>>>(
+        d, in, fours_wide(a), Incoming{nullptr, false}, k, blocks);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    scan_carry_kernel<false><<<dim3(unsigned((states + 255) / 256)), dim3(256), 0, st>>>(a.D, N, states, k, a.A, a.S0, nullptr, nullptr);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  scan_fwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kFwdWaves), 0, st>>>(d, in, fours_wide(a), k, static_cast<IO*>(a.y), a.S_T,
+                                                                                     a.spin_limit);
   return hipGetLastError();
 }
 
@@ -969,7 +1025,10 @@ hipError_t by_size(const ScanArgs& a, Go go) {
 
 }  // namespace
 
-size_t scan_workspace_bytes(const ScanArgs&) { return 0; }
+size_t scan_workspace_bytes(const ScanArgs& a) {
+  const FwdShape s = fwd_shape(a);
+  return size_t(s.states + s.sums) * sizeof(float);
+}
 
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st) {
   if (a.T == 0) return launch_state_copy(a.S0, a.S_T, int64_t(a.B) * a.D * a.N, st);
