@@ -21,8 +21,8 @@ using falcon::ScanArgs;
 // room to spare, and every grid its 32 bits.
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 
-// Longest row of the scan's inputs: 16 rows of float32 stay within 32 bits of bytes.
-constexpr int64_t kMaxScanRow = int64_t(1) << 24;
+// Longest row of the scan's inputs: 64 rows of float32 stay within 2^30 bytes.
+constexpr int64_t kMaxScanRow = int64_t(1) << 22;
 
 // a b c (each >= 0), or -1 beyond kMaxElems.
 int64_t elems(int64_t a, int64_t b, int64_t c = 1) {

@@ -615,10 +615,12 @@ constexpr int kBwdWaves = 4;
 template <int N>
 constexpr int kChunkTokens = N <= 16 ? 64 : 1024 / N;   // so that LDS holds the sums of 2 N a token and wave
 
-// Sum of v[0..3] over the wave's channels, one of the four sums in each row of 16
-// lanes: row r gets v[kRowOf[r]], in every lane of the same state four.
+// Sums of vb[0..3] and vc[0..3] over the wave's channels.  The lanes of a row of 16
+// end with one of the four states each (row_state), a lane the sum of vb where bit
+// 3 is clear and that of vc where it is set; for N = 64, whose rows hold one
+// channel, vb's sum in `w` and vc's in `w2`.
 template <int N>
-__device__ __forceinline__ float channels_sum(const float (&v)[4]) {
+__device__ __forceinline__ void channels_sum(const float (&vb)[4], const float (&vc)[4], bool high, float& w, float& w2) {
   auto swap32 = [](float a, float b) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
@@ -627,17 +629,34 @@ __device__ __forceinline__ float channels_sum(const float (&v)[4]) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
   };
-  float w = swap16(swap32(v[0], v[1]), swap32(v[2], v[3]));
-  if constexpr (Lanes<N>::kPer <= 2) w = dpp_plus<0x4e>(w);    // quad_perm [2, 3, 0, 1]
-  if constexpr (Lanes<N>::kPer <= 4) w = dpp_plus<0x124>(w);   // row_ror 4
-  if constexpr (Lanes<N>::kPer <= 8) w = dpp_plus<0x128>(w);   // row_ror 8
-  return w;
+  w = swap16(swap32(vb[0], vb[1]), swap32(vb[2], vb[3]));
+  w2 = swap16(swap32(vc[0], vc[1]), swap32(vc[2], vc[3]));
+  if constexpr (Lanes<N>::kPer <= 2) {
+    w = dpp_plus<0x4e>(w);     // quad_perm [2, 3, 0, 1]
+    w2 = dpp_plus<0x4e>(w2);
+  }
+  if constexpr (Lanes<N>::kPer <= 4) {
+    w = dpp_plus<0x124>(w);    // row_ror 4
+    w2 = dpp_plus<0x124>(w2);
+  }
+  if constexpr (Lanes<N>::kPer <= 8) {
+    // each half keeps one of the two and hands over its part of the other
+    const float give = high ? w : w2, keep = high ? w2 : w;
+    w = keep + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, give), 0x128, 0xf, 0xf, true));   // row_ror 8
+  }
 }
 // The state of its four that a lane's row of 16 holds after channels_sum.
 __device__ __forceinline__ int row_state(int lane) {
   const int r = lane / 16;
   return (r & 1) * 2 + (r >> 1);
 }
+
+// One wave's sixteen tokens of every input the gradients need, as loaded.
+template <typename IO, int N>
+struct BwdTokens {
+  bits_t<IO> x[Lanes<N>::kRegs], dt[Lanes<N>::kRegs], z[Lanes<N>::kRegs];
+  uint32_t dy[Lanes<N>::kRegs];
+};
 
 struct ScanGrads {
   float* dx;
@@ -689,25 +708,60 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
     const int es = sizeof(IO);
     const int x_at = (j * int(d.x_row) + cell.c) * es, dt_at = (j * int(d.dt_row) + cell.c) * es, z_at = (j * int(d.z_row) + cell.c) * es;
     const int up_at = (j * d.D + cell.c) * (up.bf16 ? 2 : 4);
-    const int out_at = cell.on && s < L::kQuad ? (j * d.D + cell.c) * 4 : kNowhere;
+    const uint32_t out_at = cell.on && s < L::kQuad ? (j * d.D + cell.c) * 4 : kNowhere;
+    // where this lane adds to dB (bit 3 clear) or dC, if at all
+    const bool high = L::kPer <= 8 && lane & 8, adds = (lane & 7) < L::kPer;
+    float* at_bc = &bc[wave][0][high ? 1 : 0][4 * s + row_state(lane)];
+    BwdTokens<IO, N> next;
+    auto load = [&](int m) {
+      const int64_t token = b * d.T + first + m * kTok;
+      const int rows = min(len - (first + m * kTok), kTok);
+      const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows), ru = rows_at(up, d.D, token, rows);
+#pragma unroll
+      for (int i = 0; i < L::kRegs; ++i) {
+        next.x[i] = load_bits<IO>(rx, x_at + i * L::kQuad * int(d.x_row) * es);
+        next.dt[i] = load_bits<IO>(rdt, dt_at + i * L::kQuad * int(d.dt_row) * es);
+      }
+      if (up.bf16) {
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) next.dy[i] = load_bits<bf16_t>(ru, up_at + i * L::kQuad * d.D * 2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) next.dy[i] = load_bits<float>(ru, up_at + i * L::kQuad * d.D * 4);
+      }
+      if (in.z) {
+        const auto rz = rows_at(in.z, d.z_row, token, rows);
+#pragma unroll
+        for (int i = 0; i < L::kRegs; ++i) next.z[i] = load_bits<IO>(rz, z_at + i * L::kQuad * int(d.z_row) * es);
+      }
+    };
 
     // the state before each sixteen
-    for (int m = 0; m < kSub; ++m) {
-      before[wave][m][lane] = make_float4(h[0], h[1], h[2], h[3]);
-      if (m == kSub - 1) break;
-      const int t0 = first + m * kTok;
-      const auto rx = rows_at(in.x, d.x_row, b * d.T + t0, min(len - t0, kTok)), rdt = rows_at(in.dt, d.dt_row, b * d.T + t0, min(len - t0, kTok));
-      float delta[L::kRegs], u[L::kRegs];
-      bits_t<IO> xb[L::kRegs], db[L::kRegs];
+    bits_t<IO> xb[L::kRegs], db[L::kRegs];
+    auto load_steps = [&](int m) {
+      const int64_t token = b * d.T + first + m * kTok;
+      const int rows = min(len - (first + m * kTok), kTok);
+      const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows);
 #pragma unroll
       for (int i = 0; i < L::kRegs; ++i) {
         xb[i] = load_bits<IO>(rx, x_at + i * L::kQuad * int(d.x_row) * es);
         db[i] = load_bits<IO>(rdt, dt_at + i * L::kQuad * int(d.dt_row) * es);
       }
+    };
+    if (kSub > 1) load_steps(0);
+    for (int m = 0; m < kSub - 1; ++m) {
+      const int t0 = first + m * kTok;
+      before[wave][m][lane] = make_float4(h[0], h[1], h[2], h[3]);
+      float delta[L::kRegs], u[L::kRegs];
 #pragma unroll
       for (int i = 0; i < L::kRegs; ++i) {
         delta[i] = kept(step_of<SOFTPLUS>(widen(db[i]) + bias), t0 + L::kQuad * i + j < len);
         u[i] = delta[i] * widen(xb[i]);
+      }
+      if (m + 1 < kSub - 1) {
+        load_steps(m + 1);
+      } else {
+        load(kSub - 1);
       }
       each_token<L::kQuad>([&](auto t, auto jj, auto i) {
         const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
@@ -717,43 +771,23 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
         for (int n = 0; n < 4; ++n) h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * A2[n]), h[n], ut * bt[n]);
       });
     }
+    before[wave][kSub - 1][lane] = make_float4(h[0], h[1], h[2], h[3]);
+    if (kSub == 1) load(0);
 
     for (int m = kSub - 1; m >= 0; --m) {
       const int t0 = first + m * kTok;
       const int64_t token = b * d.T + t0;
-      const int rows = min(len - t0, kTok);
       float delta[L::kRegs], x[L::kRegs], u[L::kRegs], q[L::kRegs], dy[L::kRegs], z[L::kRegs], raw[L::kRegs];
-      {
-        const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows), ru = rows_at(up, d.D, token, rows);
-        bits_t<IO> xb[L::kRegs], db[L::kRegs], zb[L::kRegs];
-        uint32_t ub[L::kRegs];
 #pragma unroll
-        for (int i = 0; i < L::kRegs; ++i) {
-          xb[i] = load_bits<IO>(rx, x_at + i * L::kQuad * int(d.x_row) * es);
-          db[i] = load_bits<IO>(rdt, dt_at + i * L::kQuad * int(d.dt_row) * es);
-        }
-        if (up.bf16) {
-#pragma unroll
-          for (int i = 0; i < L::kRegs; ++i) ub[i] = load_bits<bf16_t>(ru, up_at + i * L::kQuad * d.D * 2);
-        } else {
-#pragma unroll
-          for (int i = 0; i < L::kRegs; ++i) ub[i] = load_bits<float>(ru, up_at + i * L::kQuad * d.D * 4);
-        }
-        if (in.z) {
-          const auto rz = rows_at(in.z, d.z_row, token, rows);
-#pragma unroll
-          for (int i = 0; i < L::kRegs; ++i) zb[i] = load_bits<IO>(rz, z_at + i * L::kQuad * int(d.z_row) * es);
-        }
-#pragma unroll
-        for (int i = 0; i < L::kRegs; ++i) {
-          x[i] = widen(xb[i]);
-          raw[i] = widen(db[i]) + bias;
-          delta[i] = kept(step_of<SOFTPLUS>(raw[i]), t0 + L::kQuad * i + j < len);
-          u[i] = delta[i] * x[i];
-          dy[i] = widen(up, ub[i]);
-          z[i] = in.z ? widen(zb[i]) : 0.0f;
-          q[i] = in.z ? dy[i] * act_f32<kActSilu>(z[i]) : dy[i];
-        }
+      for (int i = 0; i < L::kRegs; ++i) {
+        // lanes without a channel of their own add nothing: u and q zero
+        x[i] = widen(next.x[i]);
+        raw[i] = widen(next.dt[i]) + bias;
+        delta[i] = kept(step_of<SOFTPLUS>(raw[i]), t0 + L::kQuad * i + j < len);
+        u[i] = kept(delta[i] * x[i], cell.on);
+        dy[i] = kept(widen(up, next.dy[i]), cell.on);
+        z[i] = in.z ? widen(next.z[i]) : 0.0f;
+        q[i] = in.z ? dy[i] * act_f32<kActSilu>(z[i]) : dy[i];
       }
       // forward: the decays, and the state before every token
       float a[kTok][4], prev[kTok][4];
@@ -788,18 +822,23 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
           G[n] = __builtin_fmaf(qt, ct[n], G[n]);
           r = __builtin_fmaf(ct[n], now, r);
           su = __builtin_fmaf(G[n], bt[n], su);
-          vb[n] = cell.on ? G[n] * ut : 0.0f;
-          vc[n] = cell.on ? qt * now : 0.0f;
+          vb[n] = G[n] * ut;
+          vc[n] = qt * now;
           G[n] *= a[t][n];
           const float mt = G[n] * prev[t][n];
           st = __builtin_fmaf(A[n], mt, st);
           dA[n] = __builtin_fmaf(mt, dt, dA[n]);
         }
-        const float wb = channels_sum<N>(vb), wc = channels_sum<N>(vc);
-        if (lane % 16 < L::kPer) {
-          float* at_bc = &bc[wave][m * kTok + t][0][4 * s + row_state(lane)];
-          __hip_atomic_fetch_add(at_bc, wb, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-          __hip_atomic_fetch_add(at_bc + N, wc, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        float w, w2;
+        channels_sum<N>(vb, vc, high, w, w2);
+        if (adds) {
+          float* to = at_bc + (m * kTok + t) * 2 * N;
+          __hip_atomic_fetch_add(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+          if constexpr (L::kPer == 16) __hip_atomic_fetch_add(to + N, w2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+        // half the decays and states are done with: room for the next sixteen
+        if constexpr (t == kTok / 2) {
+          if (m > 0) load(m - 1);
         }
         r = lanes_sum<L::kPer>(r);
         su = lanes_sum<L::kPer>(su);
@@ -813,7 +852,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
       const auto rdx = rows_at(out.dx, d.D, token, all), rddt = rows_at(out.ddt, d.D, token, all);
 #pragma unroll
       for (int i = 0; i < L::kRegs; ++i) {
-        const int o = out_at == kNowhere ? kNowhere : out_at + i * L::kQuad * d.D * 4;
+        const uint32_t o = out_at + uint32_t(i * L::kQuad) * d.D * 4;
         const float dd = kept((turn[i] + du[i] * x[i]) * (SOFTPLUS ? sigmoid_f32(raw[i]) : 1.0f), t0 + L::kQuad * i + j < len);
         dskip = __builtin_fmaf(q[i], x[i], dskip);
         dbias += dd;
@@ -824,7 +863,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
         const auto rdz = rows_at(out.dz, d.D, token, all);
 #pragma unroll
         for (int i = 0; i < L::kRegs; ++i)
-          store_one<float>(rdz, out_at == kNowhere ? kNowhere : out_at + i * L::kQuad * d.D * 4,
+          store_one<float>(rdz, out_at + uint32_t(i * L::kQuad) * d.D * 4,
                            dy[i] * __builtin_fmaf(skip, x[i], read[i]) * act_slope_f32<kActSilu>(z[i]));
       }
     }

@@ -440,7 +440,7 @@ size_t falcon_norm_bwd_workspace_bytes(const falcon_norm_problem* p);
  * (products of vectors of N elementwise).  The read comes after the write.
  *
  *  x, dt, z   : [B, T, D] io dtype, rows of x_row, dt_row, z_row elements; z
- *               may be NULL (no gate).  Rows have at most 2^24 elements.
+ *               may be NULL (no gate).  Rows have at most 2^22 elements.
  *  A          : [D, N] float32, N in {8, 16, 32, 64}.
  *  Bm, Cm     : [B, T, G, N] io dtype, rows of b_row, c_row elements; G
  *               divides D.
