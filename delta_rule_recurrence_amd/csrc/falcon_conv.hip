@@ -17,13 +17,26 @@ namespace falcon {
 
 namespace {
 
+// The taps and biases of V channels; in wide accesses for V = 4, 8 (c a multiple of
+// V, so V W floats start on a multiple of 16 bytes).
 template <typename IO, int W, int V>
 __device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c, float (&w)[W][V], float (&b)[V]) {
+  float all[V * W];
+  if constexpr (V > 1) {
+    load_vec<float, V * W>(weight + int64_t(c) * W, all);
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+    for (int j = 0; j < W; ++j) all[j] = weight[int64_t(c) * W + j];
+  }
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][v] = weight[int64_t(c + v) * W + j];
-    b[v] = bias ? bias[c + v] : 0.0f;
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][v] = all[v * W + j];
+  if (bias) {
+    load_vec<float, V>(bias + c, b);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) b[v] = 0.0f;
   }
 }
 

@@ -21,16 +21,21 @@ namespace {
 
 constexpr int kPiece = 8;   // adjacent channels of one access
 
-// Where token (b, t), group g lies: rows at (b T + t) row + g d, heads at
+// Where token b T + t, group g lies: rows at token * row + g d, heads at
 // ((b G + g) T + t) d.
 struct Layout {
   bool heads;
   int64_t row;
 };
-__device__ __forceinline__ int64_t group_at(Layout l, int64_t token, int g, int T, int G, int d) {
+// n / T for n < 2^31 as a product and a shift, worked out on the host.
+struct Divisor {
+  uint32_t magic, shift;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t n, Divisor by) { return (__umulhi(n, by.magic) + n) >> by.shift; }
+__device__ __forceinline__ int64_t group_at(Layout l, uint32_t token, int g, int T, Divisor by_T, int G, int d) {
   if (!l.heads) return token * l.row + int64_t(g) * d;
-  const int64_t b = token / T, t = token - b * T;
-  return ((b * G + g) * T + t) * d;
+  const uint32_t b = quotient(token, by_T), t = token - b * uint32_t(T);
+  return ((int64_t(b) * G + g) * T + t) * d;
 }
 
 // A lane's pieces of one group: piece k is channels (k LANES + l) 8 .. + 7.
@@ -88,7 +93,7 @@ __device__ __forceinline__ float normalise(float (&x)[NC][kPiece], int l, int d,
   for (int k = 0; k < NC; ++k)
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) q = __builtin_fmaf(x[k][i], x[k][i], q);
-  const float r = 1.0f / sqrtf(lanes_sum<LANES>(q) * inv_d + eps);
+  const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(lanes_sum<LANES>(q), inv_d, eps));
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
@@ -97,15 +102,16 @@ __device__ __forceinline__ float normalise(float (&x)[NC][kPiece], int l, int d,
 }
 
 // The weights of this lane's channels of group g; channels behind d get zero.
-template <int LANES, int NC>
+template <int LANES, int NC, bool WIDE>
 __device__ __forceinline__ void load_params(const float* p, float missing, int g, int l, int d, float (&v)[NC][kPiece]) {
+  if (p) {
+    load_group<float, LANES, NC, WIDE>(p + int64_t(g) * d, l, d, v);
+  } else {
 #pragma unroll
-  for (int k = 0; k < NC; ++k)
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) {
-      const int e = (k * LANES + l) * kPiece + i;
-      v[k][i] = e < d ? (p ? p[int64_t(g) * d + e] : missing) : 0.0f;
-    }
+      for (int i = 0; i < kPiece; ++i) v[k][i] = (k * LANES + l) * kPiece + i < d ? missing : 0.0f;
+  }
 }
 
 // A workgroup: `cols` threads side by side (whole groups of LANES lanes) times
@@ -139,8 +145,8 @@ __device__ __forceinline__ void each_act(int act, F f) {
 
 template <typename IO, int LANES, int NC, bool WIDE>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(const IO* __restrict__ x, Layout lx, const float* __restrict__ weight,
-                                                       const float* __restrict__ bias, IO* __restrict__ y, Layout ly, int64_t tokens,
-                                                       int T, int G, int d, bool center, int act, float eps, float scale, int cols,
+                                                       const float* __restrict__ bias, IO* __restrict__ y, Layout ly, uint32_t tokens,
+                                                       int T, Divisor by_T, int G, int d, bool center, int act, float eps, float scale, int cols,
                                                        int rows, int64_t cblocks, int64_t tokens_each) {
   const int64_t tblock = blockIdx.x / cblocks;
   const int col = int(blockIdx.x % cblocks) * cols + int(threadIdx.x) % cols;
@@ -150,27 +156,32 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const IO* __restrict__ x,
   const int g = min(col / LANES, G - 1);
   const float inv_d = 1.0f / float(d);
   float w[NC][kPiece], bs[NC][kPiece];
-  load_params<LANES, NC>(weight, 1.0f, g, l, d, w);
-  load_params<LANES, NC>(bias, 0.0f, g, l, d, bs);
-  const int64_t first = tblock * tokens_each * rows;
-  for (int64_t k = 0; k < tokens_each; ++k) {
-    const int64_t want = first + k * rows + mine;
-    const int64_t token = min(want, tokens - 1);
+  load_params<LANES, NC, WIDE>(weight, 1.0f, g, l, d, w);
+  load_params<LANES, NC, WIDE>(bias, 0.0f, g, l, d, bs);
+  uint32_t want = uint32_t(tblock * tokens_each * rows) + mine;
+  float next[NC][kPiece];
+  load_group<IO, LANES, NC, WIDE>(x + group_at(lx, min(want, tokens - 1), g, T, by_T, G, d), l, d, next);
+  for (int64_t k = 0; k < tokens_each; ++k, want += rows) {
     float v[NC][kPiece];
-    load_group<IO, LANES, NC, WIDE>(x + group_at(lx, token, g, T, G, d), l, d, v);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) v[c][i] = next[c][i];
+    if (k + 1 < tokens_each)
+      load_group<IO, LANES, NC, WIDE>(x + group_at(lx, min(want + rows, tokens - 1), g, T, by_T, G, d), l, d, next);
     normalise<LANES, NC>(v, l, d, inv_d, center, eps);
     each_act<NC>(act, [&](int c, int i, auto kind) {
       v[c][i] = act_f32<kind()>(__builtin_fmaf(v[c][i], w[c][i], bs[c][i])) * scale;
     });
-    if (on && want < tokens) store_group<IO, LANES, NC, WIDE>(y + group_at(ly, token, g, T, G, d), l, d, v);
+    if (on && want < tokens) store_group<IO, LANES, NC, WIDE>(y + group_at(ly, want, g, T, by_T, G, d), l, d, v);
   }
 }
 
 template <typename IO, int LANES, int NC, bool WIDE>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x, Layout lx, const float* __restrict__ weight,
                                                        const float* __restrict__ bias, const void* __restrict__ dy, bool dy_bf16, Layout ly,
-                                                       float* __restrict__ dx, Layout ldx, float* __restrict__ parts, int64_t tokens,
-                                                       int T, int G, int d, bool center, int act, float eps, float scale, int cols,
+                                                       float* __restrict__ dx, Layout ldx, float* __restrict__ parts, uint32_t tokens,
+                                                       int T, Divisor by_T, int G, int d, bool center, int act, float eps, float scale, int cols,
                                                        int rows, int64_t cblocks, int64_t tokens_each) {
   __shared__ float sums[256 * kPiece];
   const int64_t tblock = blockIdx.x / cblocks;
@@ -181,20 +192,19 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
   const int g = min(col / LANES, G - 1);
   const float inv_d = 1.0f / float(d);
   float w[NC][kPiece], bs[NC][kPiece], dw[NC][kPiece], db[NC][kPiece];
-  load_params<LANES, NC>(weight, 1.0f, g, l, d, w);
-  load_params<LANES, NC>(bias, 0.0f, g, l, d, bs);
+  load_params<LANES, NC, WIDE>(weight, 1.0f, g, l, d, w);
+  load_params<LANES, NC, WIDE>(bias, 0.0f, g, l, d, bs);
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) dw[c][i] = db[c][i] = 0.0f;
-  const int64_t first = tblock * tokens_each * rows;
-  for (int64_t k = 0; k < tokens_each; ++k) {
-    const int64_t want = first + k * rows + mine;
-    const int64_t token = min(want, tokens - 1);
+  uint32_t want = uint32_t(tblock * tokens_each * rows) + mine;
+  for (int64_t k = 0; k < tokens_each; ++k, want += rows) {
+    const uint32_t token = min(want, tokens - 1);
     const bool live = on && want < tokens;
     float v[NC][kPiece], dh[NC][kPiece];
-    load_group<IO, LANES, NC, WIDE>(x + group_at(lx, token, g, T, G, d), l, d, v);
-    const int64_t at_y = group_at(ly, token, g, T, G, d);
+    load_group<IO, LANES, NC, WIDE>(x + group_at(lx, token, g, T, by_T, G, d), l, d, v);
+    const int64_t at_y = group_at(ly, token, g, T, by_T, G, d);
     if (dy_bf16) {
       load_group<bf16_t, LANES, NC, WIDE>(static_cast<const bf16_t*>(dy) + at_y, l, d, dh);
     } else {
@@ -217,7 +227,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) v[c][i] = r * (dh[c][i] - m1 - v[c][i] * m2);
-    if (live) store_group<float, LANES, NC, WIDE>(dx + group_at(ldx, token, g, T, G, d), l, d, v);
+    if (live) store_group<float, LANES, NC, WIDE>(dx + group_at(ldx, token, g, T, by_T, G, d), l, d, v);
   }
   if (!parts) return;
   // the workgroup's sums over its rows of tokens, in a fixed order: one row of
@@ -268,14 +278,21 @@ NormShape norm_shape(const NormArgs& a, bool bwd) {
   return s;
 }
 
+Divisor divisor(uint32_t by) {
+  uint32_t shift = 0;
+  while ((uint64_t(1) << shift) < by) ++shift;
+  const uint64_t magic = ((uint64_t(1) << 32) * ((uint64_t(1) << shift) - by)) / by + 1;
+  return {uint32_t(magic), shift};
+}
+
 Layout x_layout(const NormArgs& a) { return {a.x_heads, a.x_row}; }
 Layout dense(const NormArgs& a, bool heads) { return {heads, int64_t(a.G) * a.d}; }
 
 template <typename IO, int LANES, int NC, bool WIDE>
 hipError_t norm_fwd_typed(const NormArgs& a, const NormShape& s, hipStream_t st) {
   norm_fwd_kernel<IO, LANES, NC, WIDE><<<dim3(unsigned(s.tblocks * s.cblocks)), dim3(s.threads), 0, st>>>(
-      static_cast<const IO*>(a.x), x_layout(a), a.weight, a.bias, static_cast<IO*>(a.y), dense(a, a.y_heads), int64_t(a.B) * a.T,
-      a.T, a.G, a.d, a.center, a.act, a.eps, a.scale, s.cols, s.rows, s.cblocks, s.tokens_each);
+      static_cast<const IO*>(a.x), x_layout(a), a.weight, a.bias, static_cast<IO*>(a.y), dense(a, a.y_heads), uint32_t(int64_t(a.B) * a.T),
+      a.T, divisor(a.T), a.G, a.d, a.center, a.act, a.eps, a.scale, s.cols, s.rows, s.cblocks, s.tokens_each);
   return hipGetLastError();
 }
 
@@ -283,7 +300,7 @@ template <typename IO, int LANES, int NC, bool WIDE>
 hipError_t norm_bwd_typed(const NormArgs& a, const NormShape& s, hipStream_t st) {
   norm_bwd_kernel<IO, LANES, NC, WIDE><<<dim3(unsigned(s.tblocks * s.cblocks)), dim3(s.threads), 0, st>>>(
       static_cast<const IO*>(a.x), x_layout(a), a.weight, a.bias, a.dy, a.dy_bf16, dense(a, a.y_heads), a.dx, dense(a, a.x_heads),
-      a.dweight || a.dbias ? a.workspace : nullptr, int64_t(a.B) * a.T, a.T, a.G, a.d, a.center, a.act, a.eps, a.scale, s.cols, s.rows,
+      a.dweight || a.dbias ? a.workspace : nullptr, uint32_t(int64_t(a.B) * a.T), a.T, divisor(a.T), a.G, a.d, a.center, a.act, a.eps, a.scale, s.cols, s.rows,
       s.cblocks, s.tokens_each);
   return hipGetLastError();
 }
