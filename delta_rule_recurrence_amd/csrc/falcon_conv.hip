@@ -150,6 +150,9 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const IO* __restrict__ x
 // in channels times 256 / lanes runs; their sums for the taps and the bias meet
 // in LDS in a fixed order and leave as one row of partial sums.
 constexpr int kBwdThreads = 256;
+// Tokens loaded at once, a step ahead of their work, and tokens of a run (at 8 x 2048
+// x 2304, W = 4, us: 2 ahead 100, 4 ahead 107, 1 ahead 118, runs of 64 101).
+constexpr int kBwdAhead = 2, kBwdRun = 32;
 
 template <typename IO, typename DY, int W, int V, int ACT>
 __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restrict__ x, int64_t x_row, const float* __restrict__ weight,
@@ -185,64 +188,86 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
     for (int j = 0; j < W; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) dp[j][v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[j][v] = 0.0f;
     if (t0 < len) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) load_row<IO, W, V>(x, x_row, state, b, T, C, c, t0 + j, win[j]);
     }
-    for (int t = t0; t < t1 + W - 1; ++t) {
-      if (t < len) {
-        float g[V];
-        load_vec<IO, V>(x + (b * T + t) * x_row + c, win[W - 1]);
-        load_vec<DY, V>(dy + (b * T + t) * C + c, g);
+    // kBwdAhead tokens' rows, loaded while the ones before are worked on
+    float x_next[kBwdAhead][V], dy_next[kBwdAhead][V];
+    auto load = [&](int tb) {
+      if (tb >= len) return;
+#pragma unroll
+      for (int k = 0; k < kBwdAhead; ++k) {
+        const int64_t token = b * T + min(tb + k, len - 1);
+        load_vec<IO, V>(x + token * x_row + c, x_next[k]);
+        load_vec<DY, V>(dy + token * C + c, dy_next[k]);
+      }
+    };
+    load(t0);
+    for (int tb = t0; tb < t1 + W - 1; tb += kBwdAhead) {
+      float xs[kBwdAhead][V], gs[kBwdAhead][V];
+#pragma unroll
+      for (int k = 0; k < kBwdAhead; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+          const bool live = tb + k < len;
+          xs[k][v] = live ? x_next[k][v] : 0.0f;
+          gs[k][v] = live ? dy_next[k][v] : 0.0f;
+        }
+      if (tb + kBwdAhead < t1 + W - 1) load(tb + kBwdAhead);
+#pragma unroll
+      for (int k = 0; k < kBwdAhead; ++k) {
+        const int t = tb + k;
+        const bool own = t < t1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          win[W - 1][v] = xs[k][v];
           float p = bs[v];
 #pragma unroll
           for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][v], win[j][v], p);
-          dp[W - 1][v] = g[v] * act_slope_f32<ACT>(p);
+          dp[W - 1][v] = t < len ? gs[k][v] * act_slope_f32<ACT>(p) : 0.0f;
+          const float mine_dp = own ? dp[W - 1][v] : 0.0f;
+          db[v] += mine_dp;
+#pragma unroll
+          for (int j = 0; j < W; ++j) dw[j][v] = __builtin_fmaf(mine_dp, win[j][v], dw[j][v]);
         }
-        if (t < t1) {
+        const int s = t - (W - 1);
+        // the first run's rows before the first token are the state's; a later
+        // run's belong to the run before it
+        if (t < t1 + W - 1) {
+          if (s >= t0 || (t0 == 0 && s < 0 && dstate)) {
+            float out[V];
+            const int i = s - (len - (W - 1));
+            const bool last = dstate_out && i >= 0 && i < W - 1;
+            if (last) {
+              load_vec<float, V>(dstate_out + (b * (W - 1) + i) * C + c, out);
+            } else {
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            db[v] += dp[W - 1][v];
+              for (int v = 0; v < V; ++v) out[v] = 0.0f;
+            }
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][v] = __builtin_fmaf(dp[W - 1][v], win[j][v], dw[j][v]);
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+              for (int j = 0; j < W; ++j) out[v] = __builtin_fmaf(w[W - 1 - j][v], dp[j][v], out[v]);
+            if (s >= 0) {
+              store_vec<float, V>(dx + (b * T + s) * C + c, out);
+            } else {
+              store_vec<float, V>(dstate + (b * (W - 1) + t) * C + c, out);
+            }
           }
         }
-      } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) dp[W - 1][v] = 0.0f;
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            win[j][v] = win[j + 1][v];
+            dp[j][v] = dp[j + 1][v];
+          }
       }
-      const int s = t - (W - 1);
-      // the first run's rows before the first token are the state's; a later
-      // run's belong to the run before it
-      if (s >= t0 || (t0 == 0 && dstate)) {
-        float out[V];
-        const int i = s - (len - (W - 1));
-        const bool last = dstate_out && i >= 0 && i < W - 1;
-        if (last) {
-          load_vec<float, V>(dstate_out + (b * (W - 1) + i) * C + c, out);
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v) out[v] = 0.0f;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int j = 0; j < W; ++j) out[v] = __builtin_fmaf(w[W - 1 - j][v], dp[j][v], out[v]);
-        if (s >= 0) {
-          store_vec<float, V>(dx + (b * T + s) * C + c, out);
-        } else {
-          store_vec<float, V>(dstate + (b * (W - 1) + t) * C + c, out);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          win[j][v] = win[j + 1][v];
-          dp[j][v] = dp[j + 1][v];
-        }
     }
   }
   // the workgroup's sums, run by run
@@ -287,7 +312,7 @@ ConvBwdShape conv_bwd_shape(const ConvArgs& a) {
   s.lanes = 1;
   while (s.lanes < 64 && s.lanes < s.nvec) s.lanes *= 2;
   s.cblocks = (s.nvec + s.lanes - 1) / s.lanes;
-  s.run = 32;
+  s.run = kBwdRun;
   s.nrun = std::max(1, (a.T + s.run - 1) / s.run);
   const int runs = kBwdThreads / s.lanes;
   s.rblocks = (int64_t(a.B) * s.nrun + runs - 1) / runs;
@@ -300,7 +325,7 @@ hipError_t conv_fwd_typed(const ConvArgs& a, hipStream_t st) {
   // a run long enough that its W - 1 rows read again cost little, short enough
   // that the runs fill the card
   int run = 32;
-  while (run > 1 && int64_t(a.B) * ((a.T + run - 1) / run) * nvec < 256 * 8 * 64) run /= 2;
+  while (run > 1 && int64_t(a.B) * ((a.T + run - 1) / run) * nvec < 256 * 16 * 64) run /= 2;
   while (int64_t(a.B) * ((a.T + run - 1) / run) * nvec > kMaxGrid * 256) run *= 2;   // within the grid's 32 bits
   const int nrun = std::max(1, (a.T + run - 1) / run);
   const int64_t blocks = (int64_t(a.B) * nrun * nvec + 255) / 256;

@@ -38,14 +38,18 @@ __device__ __forceinline__ int64_t group_at(Layout l, uint32_t token, int g, int
   return ((int64_t(b) * G + g) * T + t) * d;
 }
 
-// A lane's pieces of one group: piece k is channels (k LANES + l) 8 .. + 7.
-// WIDE: whole pieces in wide accesses; else element by element up to d.
+// Channel i of a lane's piece k.  WIDE: pieces of 8 adjacent channels, one wide
+// access each; else neighbours go to neighbouring lanes, element by element.
+template <int LANES, bool WIDE>
+__device__ __forceinline__ int channel(int k, int i, int l) {
+  return WIDE ? (k * LANES + l) * kPiece + i : (k * kPiece + i) * LANES + l;
+}
 template <typename E, int LANES, int NC, bool WIDE>
 __device__ __forceinline__ void load_group(const E* p, int l, int d, float (&v)[NC][kPiece]) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    const int e = (k * LANES + l) * kPiece;
     if constexpr (WIDE) {
+      const int e = channel<LANES, WIDE>(k, 0, l);
       if (e < d) {
         load_vec<E, kPiece>(p + e, v[k]);
       } else {
@@ -54,7 +58,10 @@ __device__ __forceinline__ void load_group(const E* p, int l, int d, float (&v)[
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[k][i] = e + i < d ? io<E>::load(p, e + i) : 0.0f;
+      for (int i = 0; i < kPiece; ++i) {
+        const int e = channel<LANES, WIDE>(k, i, l);
+        v[k][i] = e < d ? io<E>::load(p, e) : 0.0f;
+      }
     }
   }
 }
@@ -62,19 +69,21 @@ template <typename E, int LANES, int NC, bool WIDE>
 __device__ __forceinline__ void store_group(E* p, int l, int d, const float (&v)[NC][kPiece]) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    const int e = (k * LANES + l) * kPiece;
     if constexpr (WIDE) {
+      const int e = channel<LANES, WIDE>(k, 0, l);
       if (e < d) store_vec<E, kPiece>(p + e, v[k]);
     } else {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (e + i < d) io<E>::store(p, e + i, v[k][i]);
+      for (int i = 0; i < kPiece; ++i) {
+        const int e = channel<LANES, WIDE>(k, i, l);
+        if (e < d) io<E>::store(p, e, v[k][i]);
+      }
     }
   }
 }
 
 // xhat in place of x; returns r.  Channels behind d hold zero before and after.
-template <int LANES, int NC>
+template <int LANES, int NC, bool WIDE>
 __device__ __forceinline__ float normalise(float (&x)[NC][kPiece], int l, int d, float inv_d, bool center, float eps) {
   if (center) {
     float s = 0.0f;
@@ -86,7 +95,7 @@ __device__ __forceinline__ float normalise(float (&x)[NC][kPiece], int l, int d,
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) x[k][i] = (k * LANES + l) * kPiece + i < d ? x[k][i] - mu : 0.0f;
+      for (int i = 0; i < kPiece; ++i) x[k][i] = channel<LANES, WIDE>(k, i, l) < d ? x[k][i] - mu : 0.0f;
   }
   float q = 0.0f;
 #pragma unroll
@@ -110,7 +119,7 @@ __device__ __forceinline__ void load_params(const float* p, float missing, int g
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[k][i] = (k * LANES + l) * kPiece + i < d ? missing : 0.0f;
+      for (int i = 0; i < kPiece; ++i) v[k][i] = channel<LANES, WIDE>(k, i, l) < d ? missing : 0.0f;
   }
 }
 
@@ -169,7 +178,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const IO* __restrict__ x,
       for (int i = 0; i < kPiece; ++i) v[c][i] = next[c][i];
     if (k + 1 < tokens_each)
       load_group<IO, LANES, NC, WIDE>(x + group_at(lx, min(want + rows, tokens - 1), g, T, by_T, G, d), l, d, next);
-    normalise<LANES, NC>(v, l, d, inv_d, center, eps);
+    normalise<LANES, NC, WIDE>(v, l, d, inv_d, center, eps);
     each_act<NC>(act, [&](int c, int i, auto kind) {
       v[c][i] = act_f32<kind()>(__builtin_fmaf(v[c][i], w[c][i], bs[c][i])) * scale;
     });
@@ -199,18 +208,31 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) dw[c][i] = db[c][i] = 0.0f;
   uint32_t want = uint32_t(tblock * tokens_each * rows) + mine;
+  float x_next[NC][kPiece], dy_next[NC][kPiece];
+  auto load = [&](uint32_t token) {
+    load_group<IO, LANES, NC, WIDE>(x + group_at(lx, token, g, T, by_T, G, d), l, d, x_next);
+    const int64_t at_y = group_at(ly, token, g, T, by_T, G, d);
+    if (dy_bf16) {
+      load_group<bf16_t, LANES, NC, WIDE>(static_cast<const bf16_t*>(dy) + at_y, l, d, dy_next);
+    } else {
+      load_group<float, LANES, NC, WIDE>(static_cast<const float*>(dy) + at_y, l, d, dy_next);
+    }
+  };
+  load(min(want, tokens - 1));
   for (int64_t k = 0; k < tokens_each; ++k, want += rows) {
     const uint32_t token = min(want, tokens - 1);
     const bool live = on && want < tokens;
     float v[NC][kPiece], dh[NC][kPiece];
-    load_group<IO, LANES, NC, WIDE>(x + group_at(lx, token, g, T, by_T, G, d), l, d, v);
-    const int64_t at_y = group_at(ly, token, g, T, by_T, G, d);
-    if (dy_bf16) {
-      load_group<bf16_t, LANES, NC, WIDE>(static_cast<const bf16_t*>(dy) + at_y, l, d, dh);
-    } else {
-      load_group<float, LANES, NC, WIDE>(static_cast<const float*>(dy) + at_y, l, d, dh);
-    }
-    const float r = normalise<LANES, NC>(v, l, d, inv_d, center, eps);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) {
+        v[c][i] = x_next[c][i];
+        dh[c][i] = dy_next[c][i];
+      }
+    // (large groups have no registers to spare: they load as they go)
+    if (NC <= 2 && k + 1 < tokens_each) load(min(want + rows, tokens - 1));
+    const float r = normalise<LANES, NC, WIDE>(v, l, d, inv_d, center, eps);
     float s1 = 0.0f, s2 = 0.0f;
     each_act<NC>(act, [&](int c, int i, auto kind) {
       const float p = __builtin_fmaf(v[c][i], w[c][i], bs[c][i]);
@@ -228,6 +250,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) v[c][i] = r * (dh[c][i] - m1 - v[c][i] * m2);
     if (live) store_group<float, LANES, NC, WIDE>(dx + group_at(ldx, token, g, T, by_T, G, d), l, d, v);
+    if (NC > 2 && k + 1 < tokens_each) load(min(want + rows, tokens - 1));
   }
   if (!parts) return;
   // the workgroup's sums over its rows of tokens, in a fixed order: one row of
@@ -240,12 +263,12 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) sums[threadIdx.x * kPiece + i] = which ? db[c][i] : dw[c][i];
       __syncthreads();
-      const int e = (c * LANES + l) * kPiece;
       if (on && mine == 0) {
-        for (int i = 0; i < kPiece && e + i < d; ++i) {
+        for (int i = 0; i < kPiece; ++i) {
+          const int e = channel<LANES, WIDE>(c, i, l);
           float s = 0.0f;
           for (int r = 0; r < rows; ++r) s += sums[(r * cols + int(threadIdx.x)) * kPiece + i];
-          row[which * C + int64_t(g) * d + e + i] = s;
+          if (e < d) row[which * C + int64_t(g) * d + e] = s;
         }
       }
     }
@@ -270,8 +293,12 @@ NormShape norm_shape(const NormArgs& a, bool bwd) {
   s.rows = std::max(1, 256 / s.cols);
   s.threads = (s.rows * s.cols + 63) / 64 * 64;
   const int64_t tokens = int64_t(a.B) * a.T;
-  // tokens a thread walks over: enough workgroups to fill the card first
-  const int64_t most = bwd ? 1024 : 4096;
+  // Tokens a thread walks over: workgroups in whole rounds of the 256 CUs.  Forward
+  // eight a CU.  The gradients' workgroups each leave a row of partial sums: two a
+  // CU (8 x 2048 tokens of one group of 1024: 39 us; 54 at 2.5 a CU, 49 at four), or
+  // four where they have fewer than four waves (12 groups of 64, three waves: 31 us;
+  // 35 at two).
+  const int64_t most = bwd ? (s.threads > 192 ? 512 : 1024) : 2048;
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((tokens + s.rows - 1) / s.rows, std::max<int64_t>(1, most / s.cblocks)));
   s.tokens_each = (tokens + blocks * s.rows - 1) / (blocks * s.rows);
   s.tblocks = s.tokens_each > 0 ? (tokens + s.tokens_each * s.rows - 1) / (s.tokens_each * s.rows) : 0;

@@ -380,9 +380,31 @@ _LAYOUTS = ("rows", "heads")
 _F32 = (torch.float32,)
 
 
+def _is(t, shape, dtype, device):
+    """Whether t is a contiguous tensor of this shape, type and device."""
+    return (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device
+            and t.is_contiguous())
+
+
+def _need(t, name, shape, dtype, device, *, optional=False):
+    """``_expect`` for one type, quick where all is well."""
+    if not (_is(t, shape, dtype, device) or (optional and t is None)):
+        _expect(t, name, shape, (dtype,), device, optional=optional)
+
+
 def _row_step(t, name, shape, dtype, device, tail=1):
     """Checks a rows tensor ([..., width], the last ``tail`` axes dense) and
     returns the elements from one row to the next."""
+    if _is(t, shape, dtype, device):
+        return shape[-1] if tail == 1 else shape[-1] * shape[-2]
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device:
+        # columns of a contiguous projection, the usual case
+        stride, width = t.stride(), shape[-1]
+        if stride[-1] == 1 and (tail == 1 or (stride[-2] == width and shape[-1] > 1)):
+            width = width if tail == 1 else width * shape[-2]
+            row = stride[-tail - 1]
+            if row >= width and min(shape) > 1 and (len(shape) == tail + 1 or stride[0] == row * shape[1]):
+                return row
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if tuple(t.shape) != tuple(shape):
@@ -391,11 +413,7 @@ def _row_step(t, name, shape, dtype, device, tail=1):
         raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    width = 1
-    for size in shape[len(shape) - tail:]:
-        width *= size
-    if t.is_contiguous():
-        return width
+    width = _count(shape[-tail:])
     stride = t.stride()
     lead = len(shape) - tail
     dense = 1
@@ -426,36 +444,51 @@ def _activation(name, allowed):
     return ACTIVATIONS[name]
 
 
-class _on_stream:
-    """The device and stream of one call: allocations and the launch use them."""
+class _On:
+    """Makes a device and, if given, a stream current for one call."""
 
     def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("expected a device tensor")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream: on {stream.device}, the inputs are on {device}")
-        self._device = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-        self._stream = torch.cuda.stream(stream) if stream is not None else None
+        self._within = [torch.cuda.device(device)] + ([torch.cuda.stream(stream)] if stream is not None else [])
         self._of = device
 
     def __enter__(self):
-        if self._device is not None:
-            self._device.__enter__()
-        if self._stream is not None:
-            self._stream.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self._of).cuda_stream)
+        for w in self._within:
+            w.__enter__()
+        return torch.cuda.current_stream(self._of).cuda_stream
 
     def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+        for w in reversed(self._within):
+            w.__exit__(*exc)
         return False
+
+
+class _Here:
+    """The stream that is current already."""
+
+    def __init__(self, stream):
+        self._stream = stream
+
+    def __enter__(self):
+        return self._stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _on_stream(device, stream):
+    """The device and stream of one call: allocations and the launch use them."""
+    if device.type != "cuda":
+        raise ValueError("expected a device tensor")
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(torch.cuda.current_stream().cuda_stream)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, the inputs are on {device}")
+    return _On(device, stream)
 
 
 def _ref(t):
     """Address of a checked tensor, or NULL."""
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _workspace(given, need, device):
@@ -479,8 +512,8 @@ def _grads(given, shapes, device):
     unknown = set(g) - set(shapes)
     if unknown:
         raise ValueError(f"grads: unknown names {sorted(unknown)}")
-    for name, shape in shapes.items():
-        _expect(g.get(name), f"grads[{name!r}]", shape, _F32, device, optional=True)
+    for name, t in g.items():
+        _expect(t, f"grads[{name!r}]", shapes[name], _F32, device, optional=True)
     return g
 
 
@@ -498,8 +531,8 @@ def _conv_setup(x, weight, bias, activation, dims):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight: expected a [C, W] tensor")
     io, dev, C, W = _io_dtype(x, "x"), x.device, x.shape[-1], weight.shape[1]
-    _expect(weight, "weight", (C, W), _F32, dev)
-    _expect(bias, "bias", (C,), _F32, dev, optional=True)
+    _need(weight, "weight", (C, W), torch.float32, dev)
+    _need(bias, "bias", (C,), torch.float32, dev, optional=True)
     row = _row_step(x, "x", x.shape, io, dev)
     T = x.shape[1] if dims == 3 else 1
     return io, dev, W, FalconConvProblem(x.shape[0], T, C, W, DTYPES[io], act, row)
@@ -519,10 +552,10 @@ def falcon_conv_fwd(x, weight, bias=None, *, activation="silu", state=None, leng
     """
     io, dev, W, p = _conv_setup(x, weight, bias, activation, 3)
     B, T, C = x.shape
-    _expect(state, "state", (B, W - 1, C), (io,), dev, optional=True)
-    _expect(lengths, "lengths", (B,), (torch.int32,), dev, optional=True)
-    _expect(y, "y", (B, T, C), (io,), dev, optional=True)
-    _expect(state_out, "state_out", (B, W - 1, C), (io,), dev, optional=True)
+    _need(state, "state", (B, W - 1, C), io, dev, optional=True)
+    _need(lengths, "lengths", (B,), torch.int32, dev, optional=True)
+    _need(y, "y", (B, T, C), io, dev, optional=True)
+    _need(state_out, "state_out", (B, W - 1, C), io, dev, optional=True)
     with _on_stream(dev, stream) as st:
         if y is None:
             y = _new((B, T, C), io, dev, lengths)
@@ -539,9 +572,9 @@ def falcon_conv_step(x, weight, state, bias=None, *, activation="silu", is_first
     sequences whose earlier rows count as zero."""
     io, dev, W, p = _conv_setup(x, weight, bias, activation, 2)
     B, C = x.shape
-    _expect(state, "state", (B, W - 1, C), (io,), dev)
+    _need(state, "state", (B, W - 1, C), io, dev)
     _expect(is_first, "is_first", (B,), (torch.uint8, torch.bool), dev, optional=True)
-    _expect(y, "y", (B, C), (io,), dev, optional=True)
+    _need(y, "y", (B, C), io, dev, optional=True)
     with _on_stream(dev, stream) as st:
         if y is None:
             y = torch.empty((B, C), dtype=io, device=dev)
@@ -561,9 +594,9 @@ def falcon_conv_bwd(x, weight, dy, bias=None, *, activation="silu", state=None, 
     a bias) and dstate (None without a state, unless ``grads`` holds one)."""
     io, dev, W, p = _conv_setup(x, weight, bias, activation, 3)
     B, T, C = x.shape
-    _expect(state, "state", (B, W - 1, C), (io,), dev, optional=True)
-    _expect(lengths, "lengths", (B,), (torch.int32,), dev, optional=True)
-    _expect(dstate_out, "dstate_out", (B, W - 1, C), _F32, dev, optional=True)
+    _need(state, "state", (B, W - 1, C), io, dev, optional=True)
+    _need(lengths, "lengths", (B,), torch.int32, dev, optional=True)
+    _need(dstate_out, "dstate_out", (B, W - 1, C), torch.float32, dev, optional=True)
     dy_dtype = _dy_dtype(dy, (B, T, C), dev)
     shapes = {"dx": (B, T, C), "dweight": (C, W), "dbias": (C,), "dstate": (B, W - 1, C)}
     g = _grads(grads, shapes, dev)
@@ -597,10 +630,10 @@ def _norm_setup(x, groups, weight, bias, center, activation, eps, scale, x_layou
     B, T = x.shape[0], x.shape[2] if heads else x.shape[1]
     d = x.shape[3] if heads else x.shape[2] // G
     if heads:
-        _expect(x, "x", (B, G, T, d), (io,), dev)
+        _need(x, "x", (B, G, T, d), io, dev)
     row = G * d if heads else _row_step(x, "x", x.shape, io, dev)
-    _expect(weight, "weight", (G * d,), _F32, dev, optional=True)
-    _expect(bias, "bias", (G * d,), _F32, dev, optional=True)
+    _need(weight, "weight", (G * d,), torch.float32, dev, optional=True)
+    _need(bias, "bias", (G * d,), torch.float32, dev, optional=True)
     rows, by_head = (B, T, G * d), (B, G, T, d)
     p = FalconNormProblem(B, T, G, d, DTYPES[io], act, int(bool(center)), int(heads), int(y_layout == "heads"),
                           eps, scale, row)
@@ -618,7 +651,7 @@ def falcon_norm_fwd(x, groups, weight=None, bias=None, *, center=False, activati
     (elu + 1, a positive feature map); ``weight`` and ``bias`` are ``[G d]``.
     """
     io, dev, p, y_shape = _norm_setup(x, groups, weight, bias, center, activation, eps, scale, x_layout, y_layout)
-    _expect(y, "y", y_shape, (io,), dev, optional=True)
+    _need(y, "y", y_shape, io, dev, optional=True)
     with _on_stream(dev, stream) as st:
         if y is None:
             y = torch.empty(y_shape, dtype=io, device=dev)
@@ -662,9 +695,9 @@ def _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, dims):
     if not isinstance(B, torch.Tensor) or B.dim() != dims + 1:
         raise ValueError("B: expected a [B, T, G, N] tensor" if dims == 3 else "B: expected a [B, G, N] tensor")
     io, dev, width, N, G = _io_dtype(x, "x"), x.device, x.shape[-1], A.shape[1], B.shape[-2]
-    _expect(A, "A", (width, N), _F32, dev)
-    _expect(D, "D", (width,), _F32, dev, optional=True)
-    _expect(dt_bias, "dt_bias", (width,), _F32, dev, optional=True)
+    _need(A, "A", (width, N), torch.float32, dev)
+    _need(D, "D", (width,), torch.float32, dev, optional=True)
+    _need(dt_bias, "dt_bias", (width,), torch.float32, dev, optional=True)
     shared = tuple(x.shape[:-1]) + (G, N)
     rows = [_row_step(x, "x", x.shape, io, dev), _row_step(dt, "dt", x.shape, io, dev),
             _row_step(z, "z", x.shape, io, dev) if z is not None else width,
@@ -692,10 +725,10 @@ def falcon_scan_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, z=No
     io, dev, p = _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, 3)
     nb, T, width = x.shape
     state = (nb, width, p.N)
-    _expect(S0, "S0", state, _F32, dev, optional=True)
-    _expect(lengths, "lengths", (nb,), (torch.int32,), dev, optional=True)
-    _expect(y, "y", (nb, T, width), (io,), dev, optional=True)
-    _expect(S_T, "S_T", state, _F32, dev, optional=True)
+    _need(S0, "S0", state, torch.float32, dev, optional=True)
+    _need(lengths, "lengths", (nb,), torch.int32, dev, optional=True)
+    _need(y, "y", (nb, T, width), io, dev, optional=True)
+    _need(S_T, "S_T", state, torch.float32, dev, optional=True)
     need = falcon_scan_workspace_bytes(p)
     _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
     with _on_stream(dev, stream) as st:
@@ -717,9 +750,9 @@ def falcon_scan_step(x, dt, A, B, C, S, *, D=None, dt_bias=None, softplus=True, 
     (``[B]`` bytes) marks sequences whose state so far counts as zero."""
     io, dev, p = _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, 2)
     nb, width = x.shape
-    _expect(S, "S", (nb, width, p.N), _F32, dev)
+    _need(S, "S", (nb, width, p.N), torch.float32, dev)
     _expect(is_first, "is_first", (nb,), (torch.uint8, torch.bool), dev, optional=True)
-    _expect(y, "y", (nb, width), (io,), dev, optional=True)
+    _need(y, "y", (nb, width), io, dev, optional=True)
     with _on_stream(dev, stream) as st:
         if y is None:
             y = torch.empty((nb, width), dtype=io, device=dev)
@@ -742,9 +775,9 @@ def falcon_scan_bwd(x, dt, A, B, C, dy, *, D=None, dt_bias=None, softplus=True, 
     io, dev, p = _scan_setup(x, dt, A, B, C, D, dt_bias, softplus, z, 3)
     nb, T, width = x.shape
     state, shared = (nb, width, p.N), (nb, T, p.G, p.N)
-    _expect(S0, "S0", state, _F32, dev, optional=True)
-    _expect(lengths, "lengths", (nb,), (torch.int32,), dev, optional=True)
-    _expect(dS_T, "dS_T", state, _F32, dev, optional=True)
+    _need(S0, "S0", state, torch.float32, dev, optional=True)
+    _need(lengths, "lengths", (nb,), torch.int32, dev, optional=True)
+    _need(dS_T, "dS_T", state, torch.float32, dev, optional=True)
     dy_dtype = _dy_dtype(dy, (nb, T, width), dev)
     shapes = {"dx": (nb, T, width), "ddt": (nb, T, width), "dz": (nb, T, width), "dA": (width, p.N), "dB": shared,
               "dC": shared, "dD": (width,), "ddt_bias": (width,), "dS0": state}
