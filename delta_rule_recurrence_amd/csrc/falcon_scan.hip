@@ -283,15 +283,20 @@ __device__ __forceinline__ int64_t by_xcd(int64_t block, int64_t blocks) {
 
 constexpr int kFwdWaves = 4;
 
-// A turn of a wave: token block `turn` may start once *at has reached it.  False
-// if that did not happen within `limit` polls (then the caller poisons its
-// results; see falcon_set_wait_limit).
-__device__ __forceinline__ bool wait_turn(const int* at, int turn, int limit) {
-  for (int polls = 0; __hip_atomic_load(at, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < turn; ++polls) {
+// Turns.  *done counts the token blocks whose steps are through; a wave waits for it
+// to reach its own block's number.  A wave that gives up, after `limit` polls, or
+// finds that one did, poisons its states and stores kGaveUp instead of its count:
+// no count past a poisoned block ever appears, so whatever a late wave may still
+// store, every later block is poisoned too (see falcon_set_wait_limit).
+constexpr int kGaveUp = 1 << 30;
+// Whether the state after block turn - 1 is there.
+__device__ __forceinline__ bool wait_turn(const int* done, int turn, int limit) {
+  int now = 0;
+  for (int polls = 0; (now = __hip_atomic_load(done, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP)) < turn; ++polls) {
     if (polls >= limit) return false;
     __builtin_amdgcn_s_sleep(1);
   }
-  return true;
+  return now < kGaveUp;
 }
 
 template <typename IO, int N, bool SOFTPLUS>
@@ -361,8 +366,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
     float rows[4][4];
     four_rows<N>(Bs + 4 * s, 0, rows);
     // the steps, each decay giving way to its state
+    bool came = true;
     if (turn > 0) {
-      const bool came = wait_turn(&turns, turn, limit);
+      came = wait_turn(&turns, turn, limit);
       four(reinterpret_cast<const float*>(&passed[lane]), h);
       if (!came) h[0] = h[1] = h[2] = h[3] = __builtin_nanf("");
     }
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
       }
     });
     passed[lane] = make_float4(h[0], h[1], h[2], h[3]);
-    if (lane == 0) __hip_atomic_store(&turns, turn + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+    if (lane == 0) __hip_atomic_store(&turns, came ? turn + 1 : kGaveUp, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
     __builtin_amdgcn_s_setprio(0);
     // the reads
     float read[L::kRegs];

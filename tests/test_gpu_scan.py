@@ -221,3 +221,28 @@ def test_gradients_are_the_same_every_time():
     for _ in range(3):
         again = fb.falcon_scan_bwd(*main, dy, **a)
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_a_wait_that_gives_up_poisons_what_follows():
+    """With a limit of no polls some waves go on without the state they wait for:
+    the call ends all the same, and what is not NaN is right: a channel's outputs
+    up to the first poisoned block of 16 tokens, and its final state only if no
+    block was."""
+    case = (3, 400, 100, 16, 1, "f32", True, True, True, True, True, None, False)
+    d, softplus, _, _ = inputs(case)
+    main, a = device_args(d, softplus, None, False)
+    y, S = fb.falcon_scan_fwd(*main, **a)
+    previous = fb.falcon_set_wait_limit(0)
+    try:
+        for _ in range(3):
+            y0, S0 = fb.falcon_scan_fwd(*main, **a)
+            torch.cuda.synchronize()
+            lost = y0.isnan()
+            assert torch.equal(y0[~lost], y[~lost])
+            # once lost, lost to the end
+            assert torch.equal(lost, lost.cumsum(1) > 0)
+            assert torch.equal(S0.isnan().all(-1), lost[:, -1]) and torch.equal(S0[~lost[:, -1]], S[~lost[:, -1]])
+    finally:
+        fb.falcon_set_wait_limit(previous)
+    y1, S1 = fb.falcon_scan_fwd(*main, **a)
+    assert torch.equal(y1, y) and torch.equal(S1, S)
