@@ -20,6 +20,8 @@ using falcon::ScanArgs;
 // Largest element count of one tensor; every index then fits an int64_t with
 // room to spare, and every grid its 32 bits.
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+// Most tokens of one call: token indices and what is added to them fit an int.
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
 
 // Longest row of the scan's inputs: 64 rows of float32 stay within 2^30 bytes.
 constexpr int64_t kMaxScanRow = int64_t(1) << 22;
@@ -67,7 +69,7 @@ falcon_status check_conv(const falcon_conv_problem* p, bool step, ConvArgs* a) {
   if (!p) return FALCON_ERR_NULL;
   const int T = step ? 1 : p->T;
   if (p->B < 0 || T < 0 || p->C < 0 || p->W < 2 || p->W > 4) return FALCON_ERR_SHAPE;
-  if (elems(p->B, int64_t(T) + 4, int64_t(p->C) + 8) < 0 || int64_t(p->B) * T >= (int64_t(1) << 31)) return FALCON_ERR_SHAPE;
+  if (elems(p->B, int64_t(T) + 4, int64_t(p->C) + 8) < 0 || int64_t(p->B) * T > kMaxTokens) return FALCON_ERR_SHAPE;
   if (!rows_ok(int64_t(p->B) * T, p->x_row, p->C)) return FALCON_ERR_SHAPE;
   if (step && int64_t(p->B) * p->C > (int64_t(1) << 31)) return FALCON_ERR_SHAPE;
   if (!dtype_ok(p->io_dtype)) return FALCON_ERR_DTYPE;
@@ -85,7 +87,7 @@ falcon_status check_norm(const falcon_norm_problem* p, NormArgs* a) {
   if (!p) return FALCON_ERR_NULL;
   if (p->B < 0 || p->T < 0 || p->G < 0 || p->d < 1 || p->d > 4096) return FALCON_ERR_SHAPE;
   const int64_t C = int64_t(p->G) * p->d;
-  if (C > (int64_t(1) << 30) || elems(p->B, p->T, C) < 0 || int64_t(p->B) * p->T >= (int64_t(1) << 31)) return FALCON_ERR_SHAPE;
+  if (C > (int64_t(1) << 30) || elems(p->B, p->T, C) < 0 || int64_t(p->B) * p->T > kMaxTokens) return FALCON_ERR_SHAPE;
   if (!p->x_heads && !rows_ok(int64_t(p->B) * p->T, p->x_row, C)) return FALCON_ERR_SHAPE;
   if (!dtype_ok(p->io_dtype)) return FALCON_ERR_DTYPE;
   if (p->activation < FALCON_ACT_NONE || p->activation > FALCON_ACT_ELU1) return FALCON_ERR_VALUE;
@@ -110,7 +112,7 @@ falcon_status check_scan(const falcon_scan_problem* p, bool step, bool gate, Sca
   if (p->N != 8 && p->N != 16 && p->N != 32 && p->N != 64) return FALCON_ERR_SHAPE;
   if (p->D % p->G != 0) return FALCON_ERR_SHAPE;
   const int64_t rows = int64_t(p->B) * T, GN = int64_t(p->G) * p->N;
-  if (rows >= (int64_t(1) << 31) || elems(p->B, int64_t(T) + 1, int64_t(p->D) * p->N) < 0) return FALCON_ERR_SHAPE;
+  if (rows > kMaxTokens || elems(p->B, int64_t(T) + 1, int64_t(p->D) * p->N) < 0) return FALCON_ERR_SHAPE;
   const int64_t steps[] = {p->x_row, p->dt_row, gate ? p->z_row : p->D, p->b_row, p->c_row};
   for (int i = 0; i < 5; ++i)
     if (!rows_ok(rows, steps[i], i < 3 ? p->D : GN) || steps[i] > kMaxScanRow) return FALCON_ERR_SHAPE;

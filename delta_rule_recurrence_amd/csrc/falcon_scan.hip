@@ -559,8 +559,12 @@ __global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, 
   }
 }
 
-// One thread a state.  Loads run kAhead chunks in front.
+// One thread a state.  Loads run kAhead chunks in front.  From nothing a chunk leaves
+// its own part alone: where states grow (delta A > 0) the map's factor may overflow.
 constexpr int kAhead = 8;
+__device__ __forceinline__ float carried(float factor, float from, float own) {
+  return from == 0.0f ? own : __builtin_fmaf(factor, from, own);
+}
 template <bool GRAD>
 __global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t states, Chunks k, const float* __restrict__ A,
                                                          const float* __restrict__ S0, const float* __restrict__ dS_T,
@@ -584,7 +588,7 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t s
     for (int i = 0; i < kAhead; ++i)
       if (k0 + i < k.count) {
         k.E[(first + k0 + i) * DN + dn] = H;
-        H = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * sum[i]), H, E[i]);
+        H = carried(__builtin_amdgcn_exp2f(A2 * sum[i]), H, E[i]);
       }
   }
   if constexpr (GRAD) {
@@ -601,7 +605,7 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t s
       for (int i = 0; i < kAhead; ++i)
         if (k0 - i >= 0) {
           k.R[(first + k0 - i) * DN + dn] = G;
-          G = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * sum[i]), G, R[i]);
+          G = carried(__builtin_amdgcn_exp2f(A2 * sum[i]), G, R[i]);
         }
     }
     if (dS0) dS0[id] = G;

@@ -317,6 +317,7 @@ size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
  *    falcon_dtype of its own (falcon_bwd_chunked gives float32 ones).
  *  - Sums over tokens (parameter gradients) are made in a fixed order: results
  *    are the same from call to call.
+ *  - A call has at most 2^30 tokens (B T) and 2^40 elements of one tensor.
  */
 
 typedef enum {
@@ -392,8 +393,8 @@ size_t falcon_conv_bwd_workspace_bytes(const falcon_conv_problem* p);
  *     xhat = (x - mu) / sqrt( mean((x - mu)^2) + eps ),   mu = mean(x) if center, else 0
  *     y    = scale f( weight xhat + bias )
  *
- * With center = 0 this is the root-mean-square norm (the paper's QK-RMSNorm),
- * with f = FALCON_ACT_ELU1 a positive feature map phi.
+ * (a group of zeros needs eps > 0 to stay finite).  With center = 0 this is the
+ * root-mean-square norm (the paper's QK-RMSNorm), with f = FALCON_ACT_ELU1 a positive feature map phi.
  *
  *  x          : rows [B, T, C] of x_row elements, or heads [B, G, T, d]
  *               (x_heads; contiguous, x_row is ignored), io dtype.
@@ -451,7 +452,10 @@ size_t falcon_norm_bwd_workspace_bytes(const falcon_norm_problem* p);
  *               may alias S0 exactly.
  *  workspace  : at least falcon_scan_workspace_bytes(p) bytes (may be NULL
  *               when that is 0), 16-byte aligned, overlapping nothing else.
- * Arithmetic is float32 throughout.
+ * Arithmetic is float32 throughout.  The scan is meant for states that decay
+ * (delta A <= 0); where they grow past float32 the results are not finite.  A
+ * wait between waves that gives up (falcon_set_wait_limit) leaves NaN in the
+ * outputs of its channels from some token on and in their final state.
  */
 typedef struct {
   int32_t B, T, D, N, G;

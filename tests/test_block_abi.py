@@ -116,7 +116,7 @@ def test_problems(call, name):
     step = name.endswith("step")
     bad = [(dict(B=-1), SHAPE), (dict(io_dtype=2), DTYPE), (dict(io_dtype=-1), DTYPE)]
     if not step:
-        bad += [(dict(T=-1), SHAPE), (dict(B=1 << 30, T=1 << 30), SHAPE)]
+        bad += [(dict(T=-1), SHAPE), (dict(B=1 << 30, T=1 << 30), SHAPE), (dict(B=2, T=(1 << 29) + 1), SHAPE)]
     if make is not scan:
         bad += [(dict(activation=5), VALUE), (dict(activation=-1), VALUE)]
     if make is conv:
@@ -125,6 +125,7 @@ def test_problems(call, name):
         bad += [(dict(d=0), SHAPE), (dict(d=4097), SHAPE), (dict(G=-1), SHAPE), (dict(x_row=255), SHAPE), (dict(eps=-1.0), VALUE),
                 (dict(eps=float("nan")), VALUE), (dict(scale=float("inf")), VALUE)]
     if make is scan:
+        bad += [(dict(x_row=(1 << 22) + 1), SHAPE)]
         bad += [(dict(N=12), SHAPE), (dict(N=128), SHAPE), (dict(G=0), SHAPE), (dict(G=3), SHAPE), (dict(D=-2), SHAPE)]
         bad += [({k: v}, SHAPE) for k, v in (("x_row", 63), ("dt_row", 8), ("z_row", 63), ("b_row", 31), ("c_row", 31))]
     for kw, want in bad:
@@ -142,6 +143,19 @@ def test_workspaces(call, lib):
         assert c(workspace=c.args["dx"]) == ALIAS and c(workspace=c.args["x"]) == ALIAS
     for fn, p in (("conv_bwd", conv(W=9)), ("norm_bwd", norm(d=0)), ("scan_bwd", scan(N=7)), ("scan", scan(N=7))):
         assert getattr(lib, f"falcon_{fn}_workspace_bytes")(ctypes.byref(p)) == NONE
+
+
+def test_scans_of_long_prompts_need_a_workspace(call, lib):
+    """Few channels and many tokens are cut into chunks, whose states it holds."""
+    p = scan(B=1, T=5000)
+    need = lib.falcon_scan_workspace_bytes(ctypes.byref(p))
+    assert need > 0
+    c = call["scan_fwd"]
+    assert c(p=p, workspace=None, bytes=0) == WORKSPACE
+    assert c(p=p, bytes=need - 1) == WORKSPACE
+    assert c(p=p, bytes=need, workspace=fake(40, misalign=4)) == ALIGN
+    for over in ("x", "S0", "y", "S_T", "lengths"):
+        assert c(p=p, bytes=need, workspace=c.args[over]) == ALIAS, over
 
 
 @pytest.mark.parametrize("name", REQUIRED)
