@@ -69,6 +69,10 @@ struct Chunks {
   float* sums;            // [B, count, D]     sum of delta
   float* E;               // [B, count, D, N]  E, then the state before the chunk
   float* R;               // [B, count, D, N]  R, then the gradient behind it (gradients only)
+  // the maps up to each of the chunk's later sixteens (gradients only)
+  int subs;               // tokens / kTok - 1
+  float* sub_sums;        // [B, count, subs, D]
+  float* sub_E;           // [B, count, subs, D, N]
 };
 
 // ---- prompts ----------------------------------------------------------------------
@@ -512,21 +516,38 @@ __global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, 
       }
     }
   };
+  // the map of the chunk's tokens before t0 (stores by offset: no branch around the
+  // lane moves)
+  const auto sub_E = rows_at(k.sub_E, int64_t(d.D) * N, bc * k.subs, GRAD ? k.subs : 0);
+  const auto sub_sums = rows_at(k.sub_sums, d.D, bc * k.subs, GRAD ? k.subs : 0);
+  const uint32_t E_at = cell.on ? (cell.c * N + 4 * cell.s) * 4 : kNowhere, sum_at = cell.on && cell.s == 0 ? cell.c * 4 : kNowhere;
+  auto sub_map = [&](int t0) {
+    const uint32_t row = (t0 - first) / kTok - 1;
+    const auto bits = [](float v) { return __float_as_uint(v); };
+    typedef uint32_t four_words __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(four_words{bits(E[0]), bits(E[1]), bits(E[2]), bits(E[3])}, sub_E, E_at + row * d.D * N * 4, 0, 0);
+    store_one<float>(sub_sums, sum_at + row * d.D * 4, lanes_sum<L::kQuad>(sum));
+  };
   if (first < end) load(first);
-  for (int t0 = first; t0 < end; t0 += kTok) {
+  int t0 = first;
+  for (; t0 < end; t0 += kTok) {
     float delta[L::kRegs], u[L::kRegs], q[L::kRegs];
     stage_shared<IO, N>(next, Bs, Cs);
 #pragma unroll
     for (int i = 0; i < L::kRegs; ++i) {
       delta[i] = kept(step_of<SOFTPLUS>(widen(next.dt[i]) + bias), t0 + L::kQuad * i + cell.j < end);
       u[i] = delta[i] * widen(next.x[i]);
-      sum += delta[i];
       if constexpr (GRAD) {
         q[i] = widen(up, up_next[i]);
         if (in.z) q[i] *= act_f32<kActSilu>(widen(next.z[i]));
       }
     }
     if (t0 + kTok < end) load(t0 + kTok);
+    if constexpr (GRAD) {
+      if (t0 > first) sub_map(t0);
+    }
+#pragma unroll
+    for (int i = 0; i < L::kRegs; ++i) sum += delta[i];
     __builtin_amdgcn_wave_barrier();
     each_token<L::kQuad>([&](auto t, auto jj, auto i) {
       const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
@@ -549,6 +570,10 @@ __global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, 
       }
     });
     __builtin_amdgcn_wave_barrier();
+  }
+  if constexpr (GRAD) {
+    // sixteens that the sequence does not reach
+    for (t0 = max(t0, first + kTok); t0 < first + k.tokens; t0 += kTok) sub_map(t0);
   }
   sum = lanes_sum<L::kQuad>(sum);
   if (cell.on) {
@@ -614,9 +639,9 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t s
 
 // ---- gradients ----------------------------------------------------------------------
 // A workgroup takes one chunk of one group and, four waves side by side, its
-// channels, 4 x 256 / N at a time.  A wave first runs forward over the chunk for
-// the state before each sixteen tokens, then takes the sixteens from the last to
-// the first: forward again (decays and states in registers), then back with G.
+// channels, 4 x 256 / N at a time.  A wave takes the chunk's sixteens from the last
+// to the first: forward from the state before them (from scan_ends_kernel's maps;
+// decays and states stay in registers), then back with G.
 // What sums over channels (dB, dC) is summed over the wave's lanes by lane swaps
 // and over its channel tiles in LDS, over the waves at the end, in this order;
 // workgroups of other channels leave rows of partial sums.  What sums over tokens
@@ -746,43 +771,18 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
       }
     };
 
+    load(kSub - 1);
     // the state before each sixteen
-    bits_t<IO> xb[L::kRegs], db[L::kRegs];
-    auto load_steps = [&](int m) {
-      const int64_t token = b * d.T + first + m * kTok;
-      const int rows = min(len - (first + m * kTok), kTok);
-      const auto rx = rows_at(in.x, d.x_row, token, rows), rdt = rows_at(in.dt, d.dt_row, token, rows);
+    before[wave][0][lane] = make_float4(h[0], h[1], h[2], h[3]);
 #pragma unroll
-      for (int i = 0; i < L::kRegs; ++i) {
-        xb[i] = load_bits<IO>(rx, x_at + i * L::kQuad * int(d.x_row) * es);
-        db[i] = load_bits<IO>(rdt, dt_at + i * L::kQuad * int(d.dt_row) * es);
-      }
-    };
-    if (kSub > 1) load_steps(0);
-    for (int m = 0; m < kSub - 1; ++m) {
-      const int t0 = first + m * kTok;
-      before[wave][m][lane] = make_float4(h[0], h[1], h[2], h[3]);
-      float delta[L::kRegs], u[L::kRegs];
-#pragma unroll
-      for (int i = 0; i < L::kRegs; ++i) {
-        delta[i] = kept(step_of<SOFTPLUS>(widen(db[i]) + bias), t0 + L::kQuad * i + j < len);
-        u[i] = delta[i] * widen(xb[i]);
-      }
-      if (m + 1 < kSub - 1) {
-        load_steps(m + 1);
-      } else {
-        load(kSub - 1);
-      }
-      each_token<L::kQuad>([&](auto t, auto jj, auto i) {
-        const float dt = from_lane<L::kQuad, jj()>(delta[i()]), ut = from_lane<L::kQuad, jj()>(u[i()]);
-        float bt[4];
-        four(&shared[0][(m * kTok + t()) * N + 4 * s], bt);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * A2[n]), h[n], ut * bt[n]);
-      });
+    for (int m = 1; m < kSub; ++m) {
+      const int64_t row = (chunk * k.subs + m - 1) * d.D + cell.c;
+      const float sum = k.sub_sums[row];
+      float E[4];
+      four(k.sub_E + row * N + 4 * s, E);
+      before[wave][m][lane] = make_float4(carried(__builtin_amdgcn_exp2f(sum * A2[0]), h[0], E[0]), carried(__builtin_amdgcn_exp2f(sum * A2[1]), h[1], E[1]),
+                                          carried(__builtin_amdgcn_exp2f(sum * A2[2]), h[2], E[2]), carried(__builtin_amdgcn_exp2f(sum * A2[3]), h[3], E[3]));
     }
-    before[wave][kSub - 1][lane] = make_float4(h[0], h[1], h[2], h[3]);
-    if (kSub == 1) load(0);
 
     for (int m = kSub - 1; m >= 0; --m) {
       const int t0 = first + m * kTok;
@@ -970,7 +970,9 @@ hipError_t fwd_typed(const ScanArgs& a, hipStream_t st) {
   const int64_t blocks = int64_t(a.B) * s.count * a.G * d.tiles;
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
   const ScanIn<IO> in = inputs_of<IO>(a);
-  Chunks k{s.tokens, s.count, nullptr, nullptr, nullptr};
+  Chunks k{};
+  k.tokens = s.tokens;
+  k.count = s.count;
   if (s.count > 1) {
     k.E = a.workspace;
     k.sums = k.E + s.states;
@@ -1001,7 +1003,7 @@ hipError_t step_typed(const ScanArgs& a, hipStream_t st) {
 // chunks' rows of parameter gradients.
 struct BwdShape {
   int tokens, count, sets;
-  int64_t sums, states, bc, params;   // floats of each part (sums padded to 16 bytes)
+  int64_t sums, states, subs, bc, params;   // floats of each part (sums padded to 16 bytes)
 };
 BwdShape bwd_shape(const ScanArgs& a) {
   BwdShape s{};
@@ -1012,7 +1014,8 @@ BwdShape bwd_shape(const ScanArgs& a) {
   const int64_t groups = (d.tiles + kBwdWaves - 1) / kBwdWaves;
   // two workgroups a CU fill the card; more only add rows of partial sums
   s.sets = int(std::min<int64_t>(std::max<int64_t>(groups, 1), std::max<int64_t>(1, (512 + chunks * a.G - 1) / std::max<int64_t>(1, chunks * a.G))));
-  s.sums = (chunks * a.D + 3) / 4 * 4;
+  s.subs = s.tokens / kTok - 1;
+  s.sums = (chunks * a.D * (1 + s.subs) + 3) / 4 * 4;
   s.states = chunks * a.D * a.N;
   s.bc = int64_t(s.sets) * a.B * a.T * a.G * 2 * a.N;
   s.params = (chunks * a.D * (a.N + 2) + 3) / 4 * 4;
@@ -1024,11 +1027,18 @@ hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
   static_assert(kChunkTokens<N> == (N <= 16 ? 64 : 1024 / N));
   const ScanDims d = dims_of(a);
   const BwdShape s = bwd_shape(a);
-  Chunks k{s.tokens, s.count, nullptr, a.workspace, a.workspace + s.states};
-  float* bc = k.R + s.states;
+  Chunks k{};
+  k.tokens = s.tokens;
+  k.count = s.count;
+  k.subs = int(s.subs);
+  k.E = a.workspace;
+  k.R = k.E + s.states;
+  k.sub_E = k.R + s.states;
+  float* bc = k.sub_E + s.states * s.subs;
   float* params = bc + s.bc;
   k.sums = params + s.params;
   const int64_t chunks = int64_t(a.B) * s.count, states = int64_t(a.B) * a.D * N;
+  k.sub_sums = k.sums + chunks * a.D;
   const ScanIn<IO> in = inputs_of<IO>(a);
   const Incoming up{a.dy, a.dy_bf16};
   const int64_t waves = chunks * a.G * d.tiles, ends = (waves + kEndsWaves - 1) / kEndsWaves, blocks = chunks * a.G * s.sets;
@@ -1094,7 +1104,7 @@ hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st) {
 
 size_t scan_bwd_workspace_bytes(const ScanArgs& a) {
   const BwdShape s = bwd_shape(a);
-  return size_t(2 * s.states + s.bc + s.params + s.sums) * sizeof(float);
+  return size_t((2 + s.subs) * s.states + s.bc + s.params + s.sums) * sizeof(float);
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st) {

@@ -444,6 +444,12 @@ def _activation(name, allowed):
     return ACTIVATIONS[name]
 
 
+# The current stream's handle without the Stream object around it (2.7 us of a
+# small call's 12), where torch has the call.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """Makes a device and, if given, a stream current for one call."""
 
@@ -480,7 +486,7 @@ def _on_stream(device, stream):
     if device.type != "cuda":
         raise ValueError("expected a device tensor")
     if stream is None and device.index == torch.cuda.current_device():
-        return _Here(torch.cuda.current_stream().cuda_stream)
+        return _Here(_current_stream(device.index))
     if stream is not None and stream.device != device:
         raise ValueError(f"stream: on {stream.device}, the inputs are on {device}")
     return _On(device, stream)
