@@ -477,21 +477,31 @@ struct Cell {
 
 constexpr int kEndsWaves = 4;
 
-// One wave a chunk and 256 / N channels.
+// A map after another.  From nothing it leaves its own part alone: where states grow
+// (delta A > 0) its factor may overflow.
+__device__ __forceinline__ float carried(float factor, float from, float own) {
+  return from == 0.0f ? own : __builtin_fmaf(factor, from, own);
+}
+
+// For the gradients one wave a chunk and 256 / N channels, four neighbouring tiles of
+// channels a workgroup.  For the forward, whose chunks are few and long, a
+// workgroup's four waves take a quarter of one chunk each and join their maps (one
+// wave a chunk left the card half empty: 63 us of 1 x 16384 x 768's 125).
 template <typename IO, int N, bool SOFTPLUS, bool GRAD>
 __global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, ScanIn<IO> in, bool wide, Incoming up, Chunks k,
                                                                     int64_t waves) {
   using L = Lanes<N>;
   __shared__ float shared[kEndsWaves][2][kShared<N>];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t id = by_xcd(blockIdx.x, gridDim.x) * kEndsWaves + wave;
+  const int64_t id = GRAD ? by_xcd(blockIdx.x, gridDim.x) * kEndsWaves + wave : by_xcd(blockIdx.x, gridDim.x);
   if (id >= waves) return;
   const int tile = int(id % d.tiles), g = int(id / d.tiles % d.G);
   const int64_t bc = id / (int64_t(d.tiles) * d.G);     // b count + chunk
   const int64_t b = bc / k.count;
-  const int first = int(bc % k.count) * k.tokens;
+  const int part = GRAD ? k.tokens : k.tokens / kEndsWaves;
+  const int first = int(bc % k.count) * k.tokens + (GRAD ? 0 : wave * part);
   const Cell<N> cell(d, g, tile);
-  const int len = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T)), end = min(first + k.tokens, len);
+  const int len = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T)), end = min(first + part, len);
   float A2[4], E[4] = {0.0f, 0.0f, 0.0f, 0.0f}, R[4] = {0.0f, 0.0f, 0.0f, 0.0f}, P[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sum = 0.0f;
   four(in.A + int64_t(cell.c) * N + 4 * cell.s, A2);
 #pragma unroll
@@ -576,6 +586,24 @@ __global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, 
     for (t0 = max(t0, first + kTok); t0 < first + k.tokens; t0 += kTok) sub_map(t0);
   }
   sum = lanes_sum<L::kQuad>(sum);
+  if constexpr (!GRAD) {
+    __shared__ float4 E_of[kEndsWaves][64];
+    __shared__ float sum_of[kEndsWaves][64];
+    const int lane = threadIdx.x % 64;
+    E_of[wave][lane] = make_float4(E[0], E[1], E[2], E[3]);
+    sum_of[wave][lane] = sum;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 1; w < kEndsWaves; ++w) {
+      float own[4];
+      four(reinterpret_cast<const float*>(&E_of[w][lane]), own);
+      const float s = sum_of[w][lane];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) E[n] = carried(__builtin_amdgcn_exp2f(s * A2[n]), E[n], own[n]);
+      sum += s;
+    }
+  }
   if (cell.on) {
     const int64_t at = (bc * d.D + cell.c) * N + 4 * cell.s;
     *reinterpret_cast<float4*>(k.E + at) = make_float4(E[0], E[1], E[2], E[3]);
@@ -584,12 +612,8 @@ __global__ __launch_bounds__(64 * kEndsWaves) void scan_ends_kernel(ScanDims d, 
   }
 }
 
-// One thread a state.  Loads run kAhead chunks in front.  From nothing a chunk leaves
-// its own part alone: where states grow (delta A > 0) the map's factor may overflow.
+// One thread a state.  Loads run kAhead chunks in front.
 constexpr int kAhead = 8;
-__device__ __forceinline__ float carried(float factor, float from, float own) {
-  return from == 0.0f ? own : __builtin_fmaf(factor, from, own);
-}
 template <bool GRAD>
 __global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t states, Chunks k, const float* __restrict__ A,
                                                          const float* __restrict__ S0, const float* __restrict__ dS_T,
@@ -941,9 +965,11 @@ bool fours_wide(const ScanArgs& a) { return a.b_row % 4 == 0 && a.c_row % 4 == 0
 // workgroups or fewer than kCutFrom tokens; else enough for kCutInto workgroups.
 // Cutting works out every decay twice and takes two launches more, so it pays only
 // where a long chain of turns would leave most of the card idle (D = 1536, N = 16,
-// us, one chunk against cut): B = 1: T = 256: 12 and 19, T = 1024: 34 and 29,
-// T = 4096: 119 and 74; B = 2: T = 1024: 34 and 43, T = 4096: 119 and 127.
-constexpr int64_t kCutBelow = 128, kCutInto = 1536;
+// us, one chunk against cut): B = 1: T = 256: 12 and 19, T = 1024: 34 and 25,
+// T = 4096: 119 and 60; B = 2: T = 1024: 34 and 37, T = 4096: 120 and 110.  768
+// workgroups are one round of three a CU; 1024 (1 x 16384 x 768: 126 us against
+// 107) and 2560 (112) are not.
+constexpr int64_t kCutBelow = 128, kCutInto = 768;
 constexpr int kCutFrom = 768;
 struct FwdShape {
   int tokens, count;
@@ -977,8 +1003,8 @@ hipError_t fwd_typed(const ScanArgs& a, hipStream_t st) {
     k.E = a.workspace;
     k.sums = k.E + s.states;
     const int64_t states = int64_t(a.B) * a.D * N;
-    scan_ends_kernel<IO, N, SP, false><<<dim3(unsigned((blocks + kEndsWaves - 1) / kEndsWaves)), dim3(64 * kEndsWaves), 0, st>>>(
-        d, in, fours_wide(a), Incoming{nullptr, false}, k, blocks);
+    scan_ends_kernel<IO, N, SP, false><<<dim3(unsigned(blocks)), dim3(64 * kEndsWaves), 0, st>>>(d, in, fours_wide(a),
+                                                                                                          Incoming{nullptr, false}, k, blocks);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     scan_carry_kernel<false><<<dim3(unsigned((states + 255) / 256)), dim3(256), 0, st>>>(a.D, N, states, k, a.A, a.S0, nullptr, nullptr);
