@@ -103,9 +103,34 @@ __device__ __forceinline__ float from_lane(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false));
 }
 
-// Sixteen (or fewer) rows of one tensor as a buffer: an access behind its rows
-// reads zero or is dropped, so no address is clamped, and a lane's offsets are
-// the same 32-bit numbers at every step.  Rows have at most 2^24 elements.
+template <int CTRL>
+__device__ __forceinline__ float dpp_of(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// v[t] of every lane summed over a channel's lanes, for the group's Q tokens t: the
+// lane of token j gets the sum of v[j].  Each step halves what a lane carries.
+template <int N>
+__device__ __forceinline__ float own_sum(const float (&v)[Lanes<N>::kQuad], int j) {
+  const bool odd = j & 1, far = j & 2;
+  float s = (odd ? v[1] : v[0]) + dpp_of<0xb1>(odd ? v[0] : v[1]);        // quad_perm [1, 0, 3, 2]
+  if constexpr (Lanes<N>::kQuad == 4) {
+    const float s2 = (odd ? v[3] : v[2]) + dpp_of<0xb1>(odd ? v[2] : v[3]);
+    s = (far ? s2 : s) + dpp_of<0x4e>(far ? s : s2);                      // quad_perm [2, 3, 0, 1]
+  }
+  // the other quads' lanes of the same token: the mirror inside 8 lanes with the
+  // quads' order put right again, or rotations of the row of 16
+  if constexpr (Lanes<N>::kPer == 8) s += dpp_of<0x1b>(dpp_of<0x141>(s));  // row_half_mirror, quad_perm [3, 2, 1, 0]
+  if constexpr (Lanes<N>::kPer == 16) {
+    s = dpp_plus<0x124>(s);                                               // row_ror 4
+    s = dpp_plus<0x128>(s);                                               // row_ror 8
+  }
+  return s;
+}
+
+// Some rows of one tensor as a buffer: an access behind them reads zero or is
+// dropped, so no address is clamped, and a lane's offsets are the same 32-bit
+// numbers at every step.  The rows together have less than 2^30 bytes (sixteen of
+// at most 2^22 elements, or a chunk's few rows of states).
 template <typename E>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const E* p, int64_t row, int64_t token, int rows) {
   const int bytes = __builtin_amdgcn_readfirstlane(max(rows, 0)) * int(row) * int(sizeof(E));
@@ -389,15 +414,14 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
     if (lane == 0) __hip_atomic_store(&turns, came ? turn + 1 : kGaveUp, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
     __builtin_amdgcn_s_setprio(0);
     // the reads
-    float read[L::kRegs];
+    float read[L::kRegs], group[L::kQuad];
     four_rows<N>(Cs + 4 * s, 0, rows);
     each_row<N>(Cs + 4 * s, rows, [&](auto t, const float (&ct)[4]) {
       constexpr int jj = t() % L::kQuad;
-      float r = ct[0] * v[t()][0];
+      group[jj] = ct[0] * v[t()][0];
 #pragma unroll
-      for (int n = 1; n < 4; ++n) r = __builtin_fmaf(ct[n], v[t()][n], r);
-      r = lanes_sum<L::kPer>(r);
-      read[t() / L::kQuad] = jj == 0 || j == jj ? r : read[t() / L::kQuad];
+      for (int n = 1; n < 4; ++n) group[jj] = __builtin_fmaf(ct[n], v[t()][n], group[jj]);
+      if constexpr (jj == L::kQuad - 1) read[t() / L::kQuad] = own_sum<N>(group, j);
     });
     const auto ry = rows_at(y, d.D, b * d.T + t0, min(len - t0, kTok));
 #pragma unroll
@@ -838,7 +862,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
         }
       });
       // back
-      float du[L::kRegs], turn[L::kRegs], read[L::kRegs];
+      float du[L::kRegs], turn[L::kRegs], read[L::kRegs], sums[4], sums2[4];
       each_token<L::kQuad>([&](auto back, auto, auto) {
         constexpr int t = kTok - 1 - back(), i = t / L::kQuad, jj = t % L::kQuad;
         const float dt = from_lane<L::kQuad, jj>(delta[i]), ut = from_lane<L::kQuad, jj>(u[i]), qt = from_lane<L::kQuad, jj>(q[i]);
@@ -863,12 +887,24 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
           st = __builtin_fmaf(A[n], mt, st);
           dA[n] = __builtin_fmaf(mt, dt, dA[n]);
         }
-        float w, w2;
-        channels_sum<N>(vb, vc, high, w, w2);
-        if (adds) {
-          float* to = at_bc + (m * kTok + t) * 2 * N;
-          __hip_atomic_fetch_add(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-          if constexpr (L::kPer == 16) __hip_atomic_fetch_add(to + N, w2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        channels_sum<N>(vb, vc, high, sums[t % 4], sums2[t % 4]);
+        if constexpr (t % 4 == 0) {
+          if (adds) {
+            // read, add and write, four tokens at a time: an LDS atomic here took 80
+            // cycles each, and 303 us of the whole in place of 260
+            float* to = at_bc + (m * kTok + t) * 2 * N;
+            float old[4], old2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              old[k] = to[k * 2 * N];
+              if constexpr (L::kPer == 16) old2[k] = to[k * 2 * N + N];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              to[k * 2 * N] = old[k] + sums[k];
+              if constexpr (L::kPer == 16) to[k * 2 * N + N] = old2[k] + sums2[k];
+            }
+          }
         }
         // half the decays and states are done with: room for the next sixteen
         if constexpr (t == kTok / 2) {
