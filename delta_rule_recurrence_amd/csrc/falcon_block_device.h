@@ -136,6 +136,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// Workgroups b, b + 8, b + 16, ... run on one XCD: this order lets neighbours, which
+// share cache lines or rows, follow one another there.
+__device__ __forceinline__ int64_t by_xcd(int64_t block, int64_t blocks) {
+  const int64_t each = blocks / 8, more = blocks % 8, x = block % 8;
+  return x * each + min(x, more) + block / 8;
+}
+
 // Tokens of sequence b, between 0 and T.
 __device__ __forceinline__ int tokens_of(const int32_t* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;

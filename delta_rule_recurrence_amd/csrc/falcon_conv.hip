@@ -6,7 +6,10 @@
 // Every form is bound by its bytes (a few flops an element).  A thread owns V
 // adjacent channels (16 bytes, or one where rows are not multiples of that)
 // and a run of tokens; the last W rows slide through its registers, so each
-// row is read once, and W - 1 again at the start of a run.
+// row is read once, and W - 1 again at the start of a run.  Measured (W = 4, bf16):
+// prompts of 8 x 2048 x 2304 30 us, 5.0 TB/s of the 5.4 that a copy of that size
+// reaches; their gradients 97 us and 5 for the sums of the taps (3.9 TB/s: reads of
+// two types and float32 writes); one token of 512 x 4608 10.5 us (3.6 TB/s).
 
 #include <algorithm>
 
@@ -64,7 +67,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const IO* __restrict__ x,
                                                        const int32_t* __restrict__ lengths, IO* __restrict__ y,
                                                        IO* __restrict__ state_out, int B, int T, int C, int nvec, int run,
                                                        int nrun) {
-  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t id = by_xcd(blockIdx.x, gridDim.x) * 256 + threadIdx.x;
   if (id >= int64_t(B) * nrun * nvec) return;
   const int c = int(id % nvec) * V;
   const int64_t br = id / nvec;
@@ -162,8 +165,8 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
                                                                float* __restrict__ dstate, float* __restrict__ parts, int B, int T,
                                                                int C, int nvec, int lanes, int run, int nrun, int64_t cblocks) {
   extern __shared__ float sums[];   // [runs of the workgroup][W + 1][lanes * V]
-  const int64_t rblock = blockIdx.x / cblocks;
-  const int cblock = int(blockIdx.x % cblocks);
+  const int64_t block = by_xcd(blockIdx.x, gridDim.x), rblock = block / cblocks;
+  const int cblock = int(block % cblocks);
   const int runs = kBwdThreads / lanes;
   const int lane = threadIdx.x % lanes, mine = threadIdx.x / lanes;
   const int vec = cblock * lanes + lane;

@@ -26,6 +26,11 @@ CASES = [
     (5, 17, 12, 64, 4, "f32", False, True, True, True, False, [17, 3, 16, 9, 1], True),
     (2, 257, 136, 8, 1, "bf16", True, True, True, True, True, [255, 257], False),
     (1, 520, 24, 16, 1, "f32", True, True, True, True, True, None, False),
+    # few channels and many tokens: cut into chunks
+    (1, 1000, 20, 16, 1, "f32", True, True, True, True, True, None, False),
+    (2, 901, 40, 8, 2, "bf16", True, True, True, True, True, [900, 130], True),
+    (3, 770, 12, 64, 1, "f32", False, False, True, True, False, [0, 770, 65], False),
+    (1, 768, 33, 32, 3, "f32", True, True, False, True, True, None, True),
 ]
 
 
@@ -131,8 +136,9 @@ def test_rows_behind_the_ends_stay_and_are_not_read():
         close(g[name], ref[name], 80 + 120, name)
 
 
-def test_state_may_be_updated_in_place():
-    case = (2, 150, 100, 16, 1, "bf16", True, True, True, True, True, None, False)
+@pytest.mark.parametrize("T", [150, 900])
+def test_state_may_be_updated_in_place(T):
+    case = (2, T, 100, 16, 1, "bf16", True, True, True, True, True, None, False)
     d, softplus, _, _ = inputs(case)
     main, a = device_args(d, softplus, None, False)
     y, S = fb.falcon_scan_fwd(*main, **a)
@@ -228,6 +234,7 @@ def test_a_wait_that_gives_up_poisons_what_follows():
     the call ends all the same, and what is not NaN is right: a channel's outputs
     up to the first poisoned block of 16 tokens, and its final state only if no
     block was."""
+    # channels enough that the prompt is not cut: one chain of 25 blocks each
     case = (3, 400, 100, 16, 1, "f32", True, True, True, True, True, None, False)
     d, softplus, _, _ = inputs(case)
     main, a = device_args(d, softplus, None, False)
