@@ -324,19 +324,28 @@ ConvBwdShape conv_bwd_shape(const ConvArgs& a) {
 
 template <typename IO, int W, int V, int ACT>
 hipError_t conv_fwd_typed(const ConvArgs& a, hipStream_t st) {
-  const int nvec = (a.C + V - 1) / V;
+  const int64_t nvec = (int64_t(a.C) + V - 1) / V;
+  const auto runs_of = [&](int64_t run) { return std::max<int64_t>(1, (a.T + run - 1) / run); };
   // a run long enough that its W - 1 rows read again cost little, short enough
-  // that the runs fill the card
-  int run = 32;
-  while (run > 1 && int64_t(a.B) * ((a.T + run - 1) / run) * nvec < 256 * 16 * 64) run /= 2;
-  while (int64_t(a.B) * ((a.T + run - 1) / run) * nvec > kMaxGrid * 256) run *= 2;   // within the grid's 32 bits
-  const int nrun = std::max(1, (a.T + run - 1) / run);
-  const int64_t blocks = (int64_t(a.B) * nrun * nvec + 255) / 256;
-  if (blocks > kMaxGrid) return hipErrorInvalidValue;
-  conv_fwd_kernel<IO, W, V, ACT><<<dim3(unsigned(blocks)), dim3(256), 0, st>>>(
-      static_cast<const IO*>(a.x), a.x_row, a.weight, a.bias, static_cast<const IO*>(a.state), a.lengths, static_cast<IO*>(a.y),
-      static_cast<IO*>(a.state_out), a.B, a.T, a.C, nvec, run, nrun);
-  return hipGetLastError();
+  // that the runs fill the card, and, where that can be, a grid holds them all
+  int64_t run = 32;
+  while (run > 1 && a.B * runs_of(run) * nvec < 256 * 16 * 64) run /= 2;
+  while (run < a.T && a.B * runs_of(run) * nvec > kMaxGrid * 256) run *= 2;
+  const int64_t nrun = runs_of(run);
+  // as many sequences at once as a grid holds: one at least, since nvec < 2^31
+  const int64_t each = std::min<int64_t>(a.B, kMaxGrid * 256 / (nrun * nvec));
+  for (int64_t b = 0; b < a.B; b += each) {
+    const int64_t n = std::min(each, a.B - b), rows = b * a.T, kept = b * (W - 1) * a.C;
+    const IO* state = static_cast<const IO*>(a.state);
+    IO* state_out = static_cast<IO*>(a.state_out);
+    conv_fwd_kernel<IO, W, V, ACT><<<dim3(unsigned((n * nrun * nvec + 255) / 256)), dim3(256), 0, st>>>(
+        static_cast<const IO*>(a.x) + rows * a.x_row, a.x_row, a.weight, a.bias, state ? state + kept : nullptr,
+        a.lengths ? a.lengths + b : nullptr, static_cast<IO*>(a.y) + rows * a.C, state_out ? state_out + kept : nullptr, int(n), a.T,
+        a.C, int(nvec), int(run), int(nrun));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename IO, int W, int V, int ACT>

@@ -317,7 +317,10 @@ size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
  *    falcon_dtype of its own (falcon_bwd_chunked gives float32 ones).
  *  - Sums over tokens (parameter gradients) are made in a fixed order: results
  *    are the same from call to call.
- *  - A call has at most 2^30 tokens (B T) and 2^40 elements of one tensor.
+ *  - A call has at most 2^30 tokens (B T) and 2^40 elements of one tensor, a
+ *    single-token call 2^31 elements of x (the scan's 2^27).  Scans and
+ *    gradients that would take more than 2^24 - 1 workgroups return
+ *    FALCON_ERR_HIP, with nothing launched.
  */
 
 typedef enum {
