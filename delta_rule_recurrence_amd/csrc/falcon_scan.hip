@@ -308,20 +308,76 @@ __device__ __forceinline__ void each_token(F f) {
 
 constexpr int kFwdWaves = 4;
 
+// Where a lane stands in the channels of a wave, tile `tile` of group g.
+template <int N>
+struct Cell {
+  int c, s, j;        // channel, four of its states, token of the quad
+  bool on;
+  __device__ __forceinline__ Cell(const ScanDims& d, int g, int tile, int lane = threadIdx.x % 64) {
+    using L = Lanes<N>;
+    const int in_group = tile * L::kChannels + lane / L::kPer;
+    on = in_group < d.Dg;
+    c = g * d.Dg + min(in_group, d.Dg - 1);
+    s = lane % L::kPer;
+    j = lane % L::kQuad;
+  }
+};
+// The lane, worked out anew: what follows from it is not kept in registers till here.
+__device__ __forceinline__ int lane_again() {
+  int lane = threadIdx.x % 64;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // Turns.  *done counts the token blocks whose steps are through; a wave waits for it
-// to reach its own block's number.  A wave that gives up, after `limit` polls, or
-// finds that one did, poisons its states and stores kGaveUp instead of its count:
-// no count past a poisoned block ever appears, so whatever a late wave may still
-// store, every later block is poisoned too (see falcon_set_wait_limit).
-constexpr int kGaveUp = 1 << 30;
-// Whether the state after block turn - 1 is there.
-__device__ __forceinline__ bool wait_turn(const int* done, int turn, int limit) {
-  int now = 0;
-  for (int polls = 0; (now = __hip_atomic_load(done, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP)) < turn; ++polls) {
-    if (polls >= limit) return false;
+// to reach its own block's number, up to `limit` polls (falcon_set_wait_limit).  A
+// wave that gives up goes on, as the waves behind it do, with a state that is none,
+// and marks the workgroup's tokens as lost: run_alone then makes them good.
+__device__ __forceinline__ void wait_turn(const int* done, int turn, int limit, int* lost) {
+  for (int polls = 0; __hip_atomic_load(done, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < turn; ++polls) {
+    if (polls >= limit) {
+      *lost = 1;
+      break;
+    }
     __builtin_amdgcn_s_sleep(1);
   }
-  return now < kGaveUp;
+}
+
+// Lost tokens, [first, len) of sequence b for a wave's channels: a wave by itself runs
+// them one after another from the state `before` them, with the operations, orders and
+// roundings of the turns, so the results are the same bit for bit.  Leaves the state.
+template <typename IO, int N, bool SOFTPLUS>
+__device__ __forceinline__ void run_alone(const ScanDims& d, const ScanIn<IO>& in, int64_t b, int g, int tile, int first, int len,
+                                          const float* before, IO* y, float (&h)[4]) {
+  using L = Lanes<N>;
+  const Cell<N> cell(d, g, tile, lane_again());
+  const int c = cell.c, s = cell.s;
+  float A2[4];
+  h[0] = h[1] = h[2] = h[3] = 0.0f;
+  if (before) four(before + int64_t(c) * N + 4 * s, h);
+  four(in.A + int64_t(c) * N + 4 * s, A2);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) A2[n] *= kLog2e;
+  const float skip = in.Dskip ? in.Dskip[c] : 0.0f, bias = in.dt_bias ? in.dt_bias[c] : 0.0f;
+  for (int t = first; t < len; ++t) {
+    const int64_t token = b * d.T + t;
+    const float x = io<IO>::load(in.x, token * d.x_row + c);
+    const float delta = step_of<SOFTPLUS>(io<IO>::load(in.dt, token * d.dt_row + c) + bias), u = delta * x;
+    const float gate = in.z ? act_f32<kActSilu>(io<IO>::load(in.z, token * d.z_row + c)) : 1.0f;
+    const IO* pb = in.Bm + token * d.b_row + int64_t(g) * N + 4 * s;
+    const IO* pc = in.Cm + token * d.c_row + int64_t(g) * N + 4 * s;
+    float read = 0.0f, group[L::kQuad];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), h[n], u * io<IO>::load(pb, n));
+      const float ct = io<IO>::load(pc, n);
+      read = n == 0 ? ct * h[n] : __builtin_fmaf(ct, h[n], read);
+    }
+#pragma unroll
+    for (int q = 0; q < L::kQuad; ++q) group[q] = read;
+    read = own_sum<N>(group, cell.j);
+    if (cell.on && s == 0) io<IO>::store(y, token * d.D + c, __builtin_fmaf(skip, x, read) * gate);
+  }
 }
 
 template <typename IO, int N, bool SOFTPLUS>
@@ -330,23 +386,21 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   using L = Lanes<N>;
   __shared__ float shared[kFwdWaves][2][kShared<N>];      // B, C of a wave's tokens
   __shared__ float4 passed[64];                         // the state on its way to the next wave
-  __shared__ int turns;                                 // token blocks whose steps are done
+  __shared__ int turns, lost;                           // token blocks whose steps are done; whether a wait gave up
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int64_t id = by_xcd(blockIdx.x, gridDim.x);
   const int tile = int(id % d.tiles), g = int(id / d.tiles % d.G);
   const int64_t bc = id / (int64_t(d.tiles) * d.G), b = bc / k.count;   // b count + chunk
-  const int in_group = tile * L::kChannels + lane / L::kPer;
-  const bool on = in_group < d.Dg;
-  const int c = g * d.Dg + min(in_group, d.Dg - 1), s = lane % L::kPer, j = lane % L::kQuad;
+  const Cell<N> here(d, g, tile);
+  const int c = here.c, s = here.s, j = here.j;
   const int whole = __builtin_amdgcn_readfirstlane(tokens_of(in.lengths, int(b), d.T));
   const int first = int(bc % k.count) * k.tokens, len = min(first + k.tokens, whole);   // this chunk: [first, len)
-  const int64_t at = (b * d.D + c) * N + 4 * s;
   float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A2[4];
   if (wave == 0) {
     if (k.E) {
       four(k.E + (bc * d.D + c) * N + 4 * s, h);
     } else if (in.S0) {
-      four(in.S0 + at, h);
+      four(in.S0 + (b * d.D + c) * N + 4 * s, h);
     }
   }
   four(in.A + int64_t(c) * N + 4 * s, A2);
@@ -356,11 +410,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   float* Bs = shared[wave][0];
   float* Cs = shared[wave][1];
   const Offsets<IO, N> offsets(d, g, c);
-  const uint32_t y_at = on && s < L::kQuad ? (j * d.D + c) * int(sizeof(IO)) : kNowhere;
+  const uint32_t y_at = here.on && s < L::kQuad ? (j * d.D + c) * int(sizeof(IO)) : kNowhere;
 
   Tokens<IO, N> next;
   if (first + wave * kTok < len) load_tokens<IO, N>(d, in, b, first + wave * kTok, len, wide, offsets, next);
-  if (threadIdx.x == 0) turns = 0;
+  if (threadIdx.x == 0) turns = lost = 0;
   __syncthreads();
   for (int turn = wave; first + turn * kTok < len; turn += kFwdWaves) {
     const int t0 = first + turn * kTok;
@@ -391,11 +445,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
     float rows[4][4];
     four_rows<N>(Bs + 4 * s, 0, rows);
     // the steps, each decay giving way to its state
-    bool came = true;
     if (turn > 0) {
-      came = wait_turn(&turns, turn, limit);
+      wait_turn(&turns, turn, limit, &lost);
       four(reinterpret_cast<const float*>(&passed[lane]), h);
-      if (!came) h[0] = h[1] = h[2] = h[3] = __builtin_nanf("");
     }
     __builtin_amdgcn_s_setprio(2);
     each_row<N>(Bs + 4 * s, rows, [&](auto t, const float (&bt)[4]) {
@@ -407,7 +459,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
       }
     });
     passed[lane] = make_float4(h[0], h[1], h[2], h[3]);
-    if (lane == 0) __hip_atomic_store(&turns, came ? turn + 1 : kGaveUp, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+    if (lane == 0) __hip_atomic_store(&turns, turn + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
     __builtin_amdgcn_s_setprio(0);
     // the reads
     float read[L::kRegs], group[L::kQuad];
@@ -428,8 +480,19 @@ __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void sc
   }
   // the end is with the wave that ran the last tokens (wave 0 of the first chunk
   // where there are none)
-  const bool holds = whole > 0 ? len == whole && first < whole && wave == (whole - 1 - first) / kTok % kFwdWaves : first == 0 && wave == 0;
-  if (S_T && holds && on) *reinterpret_cast<float4*>(S_T + at) = make_float4(h[0], h[1], h[2], h[3]);
+  bool holds = whole > 0 ? len == whole && first < whole && wave == (whole - 1 - first) / kTok % kFwdWaves : first == 0 && wave == 0;
+  __syncthreads();
+  if (__builtin_amdgcn_readfirstlane(lost)) {
+    // the first wave runs the chunk again, behind the others' stores of y
+    __threadfence();
+    __syncthreads();
+    if (wave > 0) return;
+    holds = len == whole;
+    run_alone<IO, N, SOFTPLUS>(d, in, b, g, tile, first, len, k.E ? k.E + bc * d.D * N : in.S0 ? in.S0 + b * d.D * N : nullptr, y, h);
+  }
+  const Cell<N> cell(d, g, tile, lane_again());
+  if (S_T && holds && cell.on)
+    *reinterpret_cast<float4*>(S_T + (b * d.D + cell.c) * N + 4 * cell.s) = make_float4(h[0], h[1], h[2], h[3]);
 }
 
 // ---- one token --------------------------------------------------------------------
@@ -481,21 +544,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const Incoming& in, in
   return in.bf16 ? rows_at(static_cast<const bf16_t*>(in.dy), row, token, rows) : rows_at(static_cast<const float*>(in.dy), row, token, rows);
 }
 __device__ __forceinline__ float widen(const Incoming& in, uint32_t bits) { return __uint_as_float(in.bf16 ? bits << 16 : bits); }
-
-// Where a wave of scan_ends_kernel or scan_bwd_kernel stands in its channels.
-template <int N>
-struct Cell {
-  int c, s, j;        // channel, four of its states, token of the quad
-  bool on;
-  __device__ __forceinline__ Cell(const ScanDims& d, int g, int tile) {
-    using L = Lanes<N>;
-    const int lane = threadIdx.x % 64, in_group = tile * L::kChannels + lane / L::kPer;
-    on = in_group < d.Dg;
-    c = g * d.Dg + min(in_group, d.Dg - 1);
-    s = lane % L::kPer;
-    j = lane % L::kQuad;
-  }
-};
 
 constexpr int kEndsWaves = 4;
 

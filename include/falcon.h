@@ -117,6 +117,8 @@ const char* falcon_status_string(int32_t status);
  * 4194304, about 0.1-0.2 s).  A call in which a wait gave up does not hang:
  * it finishes and reports the failure in its results, every output element
  * and every final-state element of the affected sequences being NaN.
+ * falcon_scan_fwd works the tokens concerned out again where nothing waits
+ * instead: its results are the same whether or not a wait gave up.
  * Meant for tests of that path and for debugging; calls made while it
  * changes read either value.  polls = 0 makes every such wait give up at
  * once.  Returns the previous limit, or -1 (nothing changed) for polls < 0.
@@ -457,8 +459,8 @@ size_t falcon_norm_bwd_workspace_bytes(const falcon_norm_problem* p);
  *               when that is 0), 16-byte aligned, overlapping nothing else.
  * Arithmetic is float32 throughout.  The scan is meant for states that decay
  * (delta A <= 0); where they grow past float32 the results are not finite.  A
- * wait between waves that gives up (falcon_set_wait_limit) leaves NaN in the
- * outputs of its channels from some token on and in their final state.
+ * wait between waves that gives up (falcon_set_wait_limit) costs time only: one
+ * wave then runs its channels' tokens by itself, to the same bits.
  */
 typedef struct {
   int32_t B, T, D, N, G;
