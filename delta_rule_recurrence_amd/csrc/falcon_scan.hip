@@ -937,6 +937,14 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
           st = __builtin_fmaf(A[n], mt, st);
           dA[n] = __builtin_fmaf(mt, dt, dA[n]);
         }
+        if (t0 + t >= len) {
+          // Behind the sequence's end every factor is zero, but zero times a state or a
+          // gradient that is not finite is not: these tokens, the first that come by,
+          // leave nothing.  (The empty asm keeps this a branch: four selects a token
+          // took 6 us of 260, the branch 2.)
+          asm volatile("");
+          dA[0] = dA[1] = dA[2] = dA[3] = 0.0f;
+        }
         channels_sum<N>(vb, vc, high, sums[t % 4], sums2[t % 4]);
         if constexpr (t % 4 == 0) {
           if (adds) {
@@ -973,10 +981,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
 #pragma unroll
       for (int i = 0; i < L::kRegs; ++i) {
         const uint32_t o = out_at + uint32_t(i * L::kQuad) * d.D * 4;
-        const float dd = kept((turn[i] + du[i] * x[i]) * (SOFTPLUS ? sigmoid_f32(raw[i]) : 1.0f), t0 + L::kQuad * i + j < len);
+        const bool live = t0 + L::kQuad * i + j < len;    // (zeros behind the end, whatever the state: not products with zero)
+        const float dd = kept((turn[i] + du[i] * x[i]) * (SOFTPLUS ? sigmoid_f32(raw[i]) : 1.0f), live);
         dskip = __builtin_fmaf(q[i], x[i], dskip);
         dbias += dd;
-        store_one<float>(rdx, o, __builtin_fmaf(du[i], delta[i], skip * q[i]));
+        store_one<float>(rdx, o, kept(__builtin_fmaf(du[i], delta[i], skip * q[i]), live));
         store_one<float>(rddt, o, dd);
       }
       if (out.dz) {
@@ -984,7 +993,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
 #pragma unroll
         for (int i = 0; i < L::kRegs; ++i)
           store_one<float>(rdz, out_at + uint32_t(i * L::kQuad) * d.D * 4,
-                           dy[i] * __builtin_fmaf(skip, x[i], read[i]) * act_slope_f32<kActSilu>(z[i]));
+                           kept(dy[i] * __builtin_fmaf(skip, x[i], read[i]) * act_slope_f32<kActSilu>(z[i]), t0 + L::kQuad * i + j < len));
       }
     }
     dskip = lanes_sum<L::kQuad>(dskip);
@@ -1006,6 +1015,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBwdWaves; ++w) v += (&bc[w][0][0][0])[i];
+    if (t >= len) v = 0.0f;   // (as above: not what a state that is not finite left)
     rows[((b * d.T + t) * d.G + g) * 2 * N + i % (2 * N)] = v;
   }
 }
