@@ -12,6 +12,7 @@
 // two types and float32 writes); one token of 512 x 4608 10.5 us (3.6 TB/s).
 
 #include <algorithm>
+#include <type_traits>
 
 #include "falcon_block_device.h"
 #include "falcon_launch.h"
@@ -210,14 +211,37 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
         load_vec<DY, V>(dy + token * C + c, dy_next[k]);
       }
     };
-    load(t0);
-    for (int tb = t0; tb < t1 + W - 1; tb += kBwdAhead) {
+    // dx of row s = t - (W - 1), or of that row of the state; the first run's rows
+    // before the first token are the state's, a later run's belong to the run before it.
+    // Taps of tokens that there are, s + j for j = 0 .. W - 1, and no others: zero in
+    // their place would be NaN times a tap that is not finite.
+    auto back = [&](int t, auto all_there) __attribute__((always_inline)) {
+      const int s = t - (W - 1);
+      float out[V];
+      const int i = s - (len - (W - 1));
+      if (!all_there() && dstate_out && i >= 0 && i < W - 1) {
+        load_vec<float, V>(dstate_out + (b * (W - 1) + i) * C + c, out);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        if (all_there() || (s + j >= 0 && s + j < len))
+#pragma unroll
+          for (int v = 0; v < V; ++v) out[v] = __builtin_fmaf(w[W - 1 - j][v], dp[j][v], out[v]);
+      float* to = s >= 0 ? dx + (b * T + s) * C + c : dstate + (b * (W - 1) + t) * C + c;
+      store_vec<float, V>(to, out);
+    };
+    // kBwdAhead tokens from tb.  INSIDE: all of them this run's and before the
+    // sequence's end; else sums take those that are, again without products with zero.
+    auto tokens = [&](int tb, auto inside) __attribute__((always_inline)) {
       float xs[kBwdAhead][V], gs[kBwdAhead][V];
 #pragma unroll
       for (int k = 0; k < kBwdAhead; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const bool live = tb + k < len;
+          const bool live = inside() || tb + k < len;
           xs[k][v] = live ? x_next[k][v] : 0.0f;
           gs[k][v] = live ? dy_next[k][v] : 0.0f;
         }
@@ -225,43 +249,31 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
 #pragma unroll
       for (int k = 0; k < kBwdAhead; ++k) {
         const int t = tb + k;
-        const bool own = t < t1;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           win[W - 1][v] = xs[k][v];
           float p = bs[v];
 #pragma unroll
           for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][v], win[j][v], p);
-          dp[W - 1][v] = t < len ? gs[k][v] * act_slope_f32<ACT>(p) : 0.0f;
-          const float mine_dp = own ? dp[W - 1][v] : 0.0f;
-          db[v] += mine_dp;
+          dp[W - 1][v] = inside() || t < len ? gs[k][v] * act_slope_f32<ACT>(p) : 0.0f;
+        }
+        if (inside() || t < min(t1, len)) {
 #pragma unroll
-          for (int j = 0; j < W; ++j) dw[j][v] = __builtin_fmaf(mine_dp, win[j][v], dw[j][v]);
+          for (int v = 0; v < V; ++v) {
+            db[v] += dp[W - 1][v];
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][v] = __builtin_fmaf(dp[W - 1][v], win[j][v], dw[j][v]);
+          }
         }
         const int s = t - (W - 1);
-        // the first run's rows before the first token are the state's; a later
-        // run's belong to the run before it
-        if (t < t1 + W - 1) {
-          if (s >= t0 || (t0 == 0 && s < 0 && dstate)) {
-            float out[V];
-            const int i = s - (len - (W - 1));
-            const bool last = dstate_out && i >= 0 && i < W - 1;
-            if (last) {
-              load_vec<float, V>(dstate_out + (b * (W - 1) + i) * C + c, out);
-            } else {
-#pragma unroll
-              for (int v = 0; v < V; ++v) out[v] = 0.0f;
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-              for (int j = 0; j < W; ++j) out[v] = __builtin_fmaf(w[W - 1 - j][v], dp[j][v], out[v]);
-            if (s >= 0) {
-              store_vec<float, V>(dx + (b * T + s) * C + c, out);
-            } else {
-              store_vec<float, V>(dstate + (b * (W - 1) + t) * C + c, out);
-            }
+        if (inside()) {
+          if (s >= t0) {
+            back(t, std::true_type{});
+          } else if (t0 == 0 && dstate) {
+            back(t, std::false_type{});
           }
+        } else if (t < t1 + W - 1 && (s >= t0 || (t0 == 0 && dstate))) {
+          back(t, std::false_type{});
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -271,7 +283,11 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
             dp[j][v] = dp[j + 1][v];
           }
       }
-    }
+    };
+    load(t0);
+    int tb = t0;
+    for (; tb + kBwdAhead <= min(t1, len); tb += kBwdAhead) tokens(tb, std::true_type{});
+    for (; tb < t1 + W - 1; tb += kBwdAhead) tokens(tb, std::false_type{});
   }
   // the workgroup's sums, run by run
   const int width = lanes * V;
