@@ -110,12 +110,12 @@ hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st);
 size_t scan_bwd_workspace_bytes(const ScanArgs& a);
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st);
 
-// Columns of `parts` rows of n partial sums, summed in a fixed order: column i goes
-// to out[0][i] below ends[0], to out[1][i - ends[0]] below ends[1], else to
+// Columns of `parts` rows of n partial sums, `row` floats from one to the next, summed
+// in a fixed order: column i goes to out[0][i] below ends[0], to out[1][i - ends[0]] below ends[1], else to
 // out[2][i - ends[1]]; a null output is skipped.
 struct PartSums {
   const float* in;
-  int64_t parts, n;
+  int64_t parts, n, row;
   float* out[3];
   int64_t ends[2];
 };

@@ -346,7 +346,7 @@ falcon_status falcon_scan_bwd(const falcon_scan_problem* p, const void* x, const
     if (!all_aligned({dB, dC})) return FALCON_ERR_ALIGN;
     if (nb > 0 && overlap({dB, nb * 4}, {dC, nb * 4})) return FALCON_ERR_ALIAS;
     (void)hipGetLastError();
-    hipError_t e = nb > 0 ? falcon::launch_sum_parts({nullptr, 0, 2 * nb, {dB, dC, nullptr}, {nb, 2 * nb}}, stream) : hipSuccess;
+    hipError_t e = nb > 0 ? falcon::launch_sum_parts({nullptr, 0, 2 * nb, 2 * nb, {dB, dC, nullptr}, {nb, 2 * nb}}, stream) : hipSuccess;
     return finish(e);
   }
   if (!A || !dA || (n > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dB || !dC || (z && !dz))))

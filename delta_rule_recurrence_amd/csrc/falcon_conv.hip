@@ -445,7 +445,7 @@ hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t st) {
   }
   if (e != hipSuccess) return e;
   const int64_t taps = int64_t(a.C) * a.W;
-  return launch_sum_parts({a.workspace, s.rblocks, taps + a.C, {a.dweight, a.dbias, nullptr}, {taps, taps + a.C}}, st);
+  return launch_sum_parts({a.workspace, s.rblocks, taps + a.C, taps + a.C, {a.dweight, a.dbias, nullptr}, {taps, taps + a.C}}, st);
 }
 
 }  // namespace falcon

@@ -384,7 +384,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st) {
   }
   if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
   const int64_t C = int64_t(a.G) * a.d;
-  return launch_sum_parts({a.workspace, s.tblocks, 2 * C, {a.dweight, a.dbias, nullptr}, {C, 2 * C}}, st);
+  return launch_sum_parts({a.workspace, s.tblocks, 2 * C, 2 * C, {a.dweight, a.dbias, nullptr}, {C, 2 * C}}, st);
 }
 
 }  // namespace falcon

@@ -796,8 +796,11 @@ struct ScanGrads {
   float* ddt;
   float* dz;
   float* bc;       // dB and dC, or rows of partial sums: [sets][B T][G][2][N]
-  float* params;   // [B count][D (N + 2)]: dA, dD, ddt_bias of a chunk
+  float* params;   // [B count] rows of params_row floats: dA, dD, ddt_bias of a chunk
 };
+
+// D (N + 2) floats, and as many more as put every row on a multiple of 16 bytes.
+__host__ __device__ __forceinline__ int64_t params_row(int D, int N) { return (int64_t(D) * (N + 2) + 3) / 4 * 4; }
 
 template <typename IO, int N, bool SOFTPLUS>
 __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d, ScanIn<IO> in, bool wide, Incoming up, Chunks k,
@@ -999,7 +1002,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d,
     dskip = lanes_sum<L::kQuad>(dskip);
     dbias = lanes_sum<L::kQuad>(dbias);
     if (cell.on) {
-      float* row = out.params + chunk * d.D * (N + 2);
+      float* row = out.params + chunk * params_row(d.D, N);
       *reinterpret_cast<float4*>(row + int64_t(cell.c) * N + 4 * s) = make_float4(dA[0], dA[1], dA[2], dA[3]);
       if (s == 0) {
         row[int64_t(d.D) * N + cell.c] = dskip;
@@ -1140,7 +1143,7 @@ BwdShape bwd_shape(const ScanArgs& a) {
   s.sums = (chunks * a.D * (1 + s.subs) + 3) / 4 * 4;
   s.states = chunks * a.D * a.N;
   s.bc = int64_t(s.sets) * a.B * a.T * a.G * 2 * a.N;
-  s.params = (chunks * a.D * (a.N + 2) + 3) / 4 * 4;
+  s.params = chunks * params_row(a.D, a.N);
   return s;
 }
 
@@ -1189,7 +1192,7 @@ hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   const int64_t DN = int64_t(a.D) * N;
-  return launch_sum_parts({params, chunks, DN + 2 * a.D, {a.dA, a.dD, a.ddt_bias}, {DN, DN + a.D}}, st);
+  return launch_sum_parts({params, chunks, DN + 2 * a.D, params_row(a.D, N), {a.dA, a.dD, a.ddt_bias}, {DN, DN + a.D}}, st);
 }
 
 // Calls go(N, softplus) with compile-time values.

@@ -25,11 +25,11 @@ __global__ __launch_bounds__(64 * kSlices) void sum_parts_kernel(PartSums s) {
       for (; p + (kInFlight - 1) * kSlices < s.parts; p += kInFlight * kSlices) {
         float x[kInFlight];
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) x[k] = s.in[(p + k * kSlices) * s.n + i];
+        for (int k = 0; k < kInFlight; ++k) x[k] = s.in[(p + k * kSlices) * s.row + i];
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) v += x[k];
       }
-      for (; p < s.parts; p += kSlices) v += s.in[p * s.n + i];
+      for (; p < s.parts; p += kSlices) v += s.in[p * s.row + i];
     }
     sums[slice][lane] = v;
     __syncthreads();
