@@ -189,6 +189,13 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const IO* __restrict__ x,
   }
 }
 
+// A thread's sums of the parameters' gradients go on for kSumTokens tokens, then they
+// are added to what it holds in LDS: a float32 sum of n tokens that all have one sign
+// is off by up to 64 + n / 64 roundings, not n.  (In registers that would cost a
+// wave a SIMD; a row of partial sums every 64 tokens took 12 % longer at 8 x 16384
+// tokens of 12 x 128.)
+constexpr int kSumTokens = 64;
+
 template <typename IO, int LANES, int NC, bool WIDE>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x, Layout lx, const float* __restrict__ weight,
                                                        const float* __restrict__ bias, const void* __restrict__ dy, bool dy_bf16, Layout ly,
@@ -196,6 +203,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
                                                        int T, Divisor by_T, int G, int d, bool center, int act, float eps, float scale, int cols,
                                                        int rows, int64_t cblocks, int64_t tokens_each) {
   __shared__ float sums[256 * kPiece];
+  extern __shared__ float folded[];          // [2][NC kPiece][threads], where tokens_each > kSumTokens
+  const bool folds = parts && tokens_each > kSumTokens;
   const int64_t tblock = blockIdx.x / cblocks;
   const int col = int(blockIdx.x % cblocks) * cols + int(threadIdx.x) % cols;
   const int mine = int(threadIdx.x) / cols;
@@ -210,6 +219,17 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) dw[c][i] = db[c][i] = 0.0f;
+  // each(f): f(this thread's place, its sum) for all of its sums
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) {
+        f(folded[(c * kPiece + i) * blockDim.x + threadIdx.x], dw[c][i]);
+        f(folded[((NC + c) * kPiece + i) * blockDim.x + threadIdx.x], db[c][i]);
+      }
+  };
+  if (folds) each([](float& held, float&) { held = 0.0f; });
   uint32_t want = uint32_t(tblock * tokens_each * rows) + mine;
   float x_next[NC][kPiece], dy_next[NC][kPiece];
   auto load = [&](uint32_t token) {
@@ -254,8 +274,15 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
       for (int i = 0; i < kPiece; ++i) v[c][i] = r * (dh[c][i] - m1 - v[c][i] * m2);
     if (live) store_group<float, LANES, NC, WIDE>(dx + group_at(ldx, token, g, T, by_T, G, d), l, d, v);
     if (NC > 2 && k + 1 < tokens_each) load(min(want + rows, tokens - 1));
+    if (folds && k % kSumTokens == kSumTokens - 1) {
+      each([](float& held, float& sum) {
+        held += sum;
+        sum = 0.0f;
+      });
+    }
   }
   if (!parts) return;
+  if (folds) each([](float& held, float& sum) { sum += held; });
   // the workgroup's sums over its rows of tokens, in a fixed order: one row of
   // partial sums, [C] of the weights and [C] of the biases
   const int64_t C = int64_t(G) * d;
@@ -269,9 +296,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const IO* __restrict__ x,
       if (on && mine == 0) {
         for (int i = 0; i < kPiece; ++i) {
           const int e = channel<LANES, WIDE>(c, i, l);
-          float s = 0.0f;
+          double s = 0.0;
           for (int r = 0; r < rows; ++r) s += sums[(r * cols + int(threadIdx.x)) * kPiece + i];
-          if (e < d) row[which * C + int64_t(g) * d + e] = s;
+          if (e < d) row[which * C + int64_t(g) * d + e] = float(s);
         }
       }
     }
@@ -328,7 +355,13 @@ hipError_t norm_fwd_typed(const NormArgs& a, const NormShape& s, hipStream_t st)
 
 template <typename IO, int LANES, int NC, bool WIDE>
 hipError_t norm_bwd_typed(const NormArgs& a, const NormShape& s, hipStream_t st) {
-  norm_bwd_kernel<IO, LANES, NC, WIDE><<<dim3(unsigned(s.tblocks * s.cblocks)), dim3(s.threads), 0, st>>>(
+  auto* const kernel = norm_bwd_kernel<IO, LANES, NC, WIDE>;
+  const size_t lds = (a.dweight || a.dbias) && s.tokens_each > kSumTokens ? size_t(2) * NC * kPiece * s.threads * sizeof(float) : 0;
+  if (lds > 32 * 1024) {   // with the 8 KiB of its own past what a launch may take unasked
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<dim3(unsigned(s.tblocks * s.cblocks)), dim3(s.threads), lds, st>>>(
       static_cast<const IO*>(a.x), x_layout(a), a.weight, a.bias, a.dy, a.dy_bf16, dense(a, a.y_heads), a.dx, dense(a, a.x_heads),
       a.dweight || a.dbias ? a.workspace : nullptr, uint32_t(int64_t(a.B) * a.T), a.T, divisor(a.T), a.G, a.d, a.center, a.act, a.eps, a.scale, s.cols, s.rows,
       s.cblocks, s.tokens_each);
