@@ -7,11 +7,12 @@
 namespace falcon {
 
 // ---- V consecutive elements as floats ----------------------------------------
-// V * sizeof(IO) is 16 bytes or a multiple (VEC: one or more wide accesses, the
-// address a multiple of 16, or of the access if that is smaller), or the
-// elements go one by one.
+// V is one, or a multiple of four: wide accesses of 16 bytes (8 for four bf16), the
+// address a multiple of that.
 template <typename IO, int V>
 __device__ __forceinline__ void load_vec(const IO* p, float (&out)[V]) {
+  static_assert(V == 1 || V % 4 == 0);
+  static_assert(sizeof(IO) == 4 || V == 1 || V == 4 || V % 8 == 0);
   if constexpr (V == 1) {
     out[0] = io<IO>::load(p, 0);
   } else if constexpr (sizeof(IO) == 2) {
@@ -26,18 +27,14 @@ __device__ __forceinline__ void load_vec(const IO* p, float (&out)[V]) {
           out[8 * k + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
       }
-    } else if constexpr (V == 4) {
+    } else {
       const uint2 a = *reinterpret_cast<const uint2*>(p);
       out[0] = __uint_as_float(a.x << 16);
       out[1] = __uint_as_float(a.x & 0xffff0000u);
       out[2] = __uint_as_float(a.y << 16);
       out[3] = __uint_as_float(a.y & 0xffff0000u);
-    } else {
-      const uint32_t a = *reinterpret_cast<const uint32_t*>(p);
-      out[0] = __uint_as_float(a << 16);
-      out[1] = __uint_as_float(a & 0xffff0000u);
     }
-  } else if constexpr (V % 4 == 0) {
+  } else {
 #pragma unroll
     for (int k = 0; k < V / 4; ++k) {
       const float4 a = reinterpret_cast<const float4*>(p)[k];
@@ -46,10 +43,6 @@ __device__ __forceinline__ void load_vec(const IO* p, float (&out)[V]) {
       out[4 * k + 2] = a.z;
       out[4 * k + 3] = a.w;
     }
-  } else {
-    const float2 a = *reinterpret_cast<const float2*>(p);
-    out[0] = a.x;
-    out[1] = a.y;
   }
 }
 
@@ -68,17 +61,13 @@ __device__ __forceinline__ void store_vec(IO* p, const float (&v)[V]) {
       for (int k = 0; k < V / 8; ++k)
         reinterpret_cast<uint4*>(p)[k] = make_uint4(bf16_pair(v[8 * k], v[8 * k + 1]), bf16_pair(v[8 * k + 2], v[8 * k + 3]),
                                                     bf16_pair(v[8 * k + 4], v[8 * k + 5]), bf16_pair(v[8 * k + 6], v[8 * k + 7]));
-    } else if constexpr (V == 4) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     } else {
-      *reinterpret_cast<uint32_t*>(p) = bf16_pair(v[0], v[1]);
+      *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     }
-  } else if constexpr (V % 4 == 0) {
+  } else {
 #pragma unroll
     for (int k = 0; k < V / 4; ++k)
       reinterpret_cast<float4*>(p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  } else {
-    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
   }
 }
 

@@ -23,7 +23,7 @@ namespace {
 
 // The taps and biases of V channels; in wide accesses for V = 4, 8 (c a multiple of
 // V, so V W floats start on a multiple of 16 bytes).
-template <typename IO, int W, int V>
+template <int W, int V>
 __device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c, float (&w)[W][V], float (&b)[V]) {
   float all[V * W];
   if constexpr (V > 1) {
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const IO* __restrict__ x,
   const int t1 = min(t0 + run, len);
   if (t0 >= t1) return;
   float w[W][V], bs[V], win[W][V];
-  load_taps<IO, W, V>(weight, bias, c, w, bs);
+  load_taps<W, V>(weight, bias, c, w, bs);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) load_row<IO, W, V>(x, x_row, state, b, T, C, c, t0 + j, win[j]);
   const IO* px = x + (b * T + t0) * x_row + c;
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const IO* __restrict__ x
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) load_vec<IO, V>(ps + int64_t(j) * C, win[j]);
   load_vec<IO, V>(x + b * x_row + c, win[W - 1]);
-  load_taps<IO, W, V>(weight, bias, c, w, bs);
+  load_taps<W, V>(weight, bias, c, w, bs);
   if (fresh) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(kBwdThreads) void conv_bwd_kernel(const IO* __restr
     const int len = tokens_of(lengths, int(b), T);
     const int t1 = min(t0 + run, T);          // rows of dx that are this run's: [t0, t1), and dstate's for the first
     float w[W][V], bs[V], win[W][V], dp[W][V];  // dp[j]: the slope of token t - (W - 1) + j
-    load_taps<IO, W, V>(weight, bias, c, w, bs);
+    load_taps<W, V>(weight, bias, c, w, bs);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
@@ -387,7 +387,7 @@ hipError_t conv_bwd_typed(const ConvArgs& a, const ConvBwdShape& s, hipStream_t 
   return hipGetLastError();
 }
 
-// Calls F::go<IO, W, V, ACT>.
+// The kernels by activation, taps, type and width of access.
 enum class Form { kFwd, kStep };
 template <Form F, typename IO, int W, int V>
 hipError_t by_act(const ConvArgs& a, hipStream_t st) {

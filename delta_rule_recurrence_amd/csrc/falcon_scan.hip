@@ -803,7 +803,7 @@ struct ScanGrads {
 __host__ __device__ __forceinline__ int64_t params_row(int D, int N) { return (int64_t(D) * (N + 2) + 3) / 4 * 4; }
 
 template <typename IO, int N, bool SOFTPLUS>
-__global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d, ScanIn<IO> in, bool wide, Incoming up, Chunks k,
+__global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(ScanDims d, ScanIn<IO> in, Incoming up, Chunks k,
                                                                     ScanGrads out, int sets) {
   using L = Lanes<N>;
   constexpr int kTokens = kChunkTokens<N>, kSub = kTokens / kTok;
@@ -1181,7 +1181,7 @@ hipError_t bwd_typed(const ScanArgs& a, hipStream_t st) {
   }
   if (blocks > 0) {
     const ScanGrads out{a.dx, a.ddt, a.dz, bc, params};
-    scan_bwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kBwdWaves), 0, st>>>(d, in, fours_wide(a), up, k, out, s.sets);
+    scan_bwd_kernel<IO, N, SP><<<dim3(unsigned(blocks)), dim3(64 * kBwdWaves), 0, st>>>(d, in, up, k, out, s.sets);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
