@@ -105,12 +105,29 @@ __device__ __forceinline__ float normalise(float (&x)[NC][kPiece], int l, int d,
   for (int k = 0; k < NC; ++k)
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) q = __builtin_fmaf(x[k][i], x[k][i], q);
-  const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(lanes_sum<LANES>(q), inv_d, eps));
+  const float m = __builtin_fmaf(lanes_sum<LANES>(q), inv_d, eps);
+  float r = __builtin_amdgcn_rsqf(m), scaled = 1.0f;
+  // Squares that leave float32's normal numbers (values past 2^60 or, with eps = 0,
+  // below 2^-63): the groups concerned once more, scaled by a power of two.  The whole
+  // wave goes along, for the moves between lanes.
+  if (__builtin_amdgcn_ballot_w64(!(m >= 0x1p-126f && m <= 0x1.fffffep127f))) {
+    if (m < 0x1p-126f) scaled = 0x1p75f;
+    if (m > 0x1.fffffep127f) scaled = 0x1p-75f;
+    q = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) {
+        x[k][i] *= scaled;
+        q = __builtin_fmaf(x[k][i], x[k][i], q);
+      }
+    r = __builtin_amdgcn_rsqf(__builtin_fmaf(lanes_sum<LANES>(q), inv_d, eps * scaled * scaled));
+  }
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) x[k][i] *= r;
-  return r;
+  return r * scaled;
 }
 
 // The weights of this lane's channels of group g; channels behind d get zero.

@@ -398,7 +398,8 @@ size_t falcon_conv_bwd_workspace_bytes(const falcon_conv_problem* p);
  *     xhat = (x - mu) / sqrt( mean((x - mu)^2) + eps ),   mu = mean(x) if center, else 0
  *     y    = scale f( weight xhat + bias )
  *
- * (a group of zeros needs eps > 0 to stay finite).  With center = 0 this is the
+ * (a group of zeros needs eps > 0 to stay finite; with center, a group's sum has
+ * to be a float32 number).  With center = 0 this is the
  * root-mean-square norm (the paper's QK-RMSNorm), with f = FALCON_ACT_ELU1 a positive feature map phi.
  *
  *  x          : rows [B, T, C] of x_row elements, or heads [B, G, T, d]
