@@ -7,9 +7,12 @@
 // adjacent channels (16 bytes, or one where rows are not multiples of that)
 // and a run of tokens; the last W rows slide through its registers, so each
 // row is read once, and W - 1 again at the start of a run.  Measured (W = 4, bf16):
-// prompts of 8 x 2048 x 2304 30 us, 5.0 TB/s of the 5.4 that a copy of that size
-// reaches; their gradients 97 us and 5 for the sums of the taps (3.9 TB/s: reads of
-// two types and float32 writes); one token of 512 x 4608 10.5 us (3.6 TB/s).
+// prompts of 8 x 2048 x 2304 29 us where the tensors are still in the last-level
+// cache (a copy of them 22), 42 where they are not (the copy 30), 3.6 TB/s: rows
+// read again miss L2 (89 MB read for 75).  Their gradients 92 us and 5 for the sums
+// of the taps (3.9 TB/s: reads of two types and float32 writes).  One token of
+// 512 x 4608 10 us (3.7 TB/s): a thread loads 160 bytes of taps and bias for 128 of
+// data, at addresses 128 bytes apart.
 
 #include <algorithm>
 #include <type_traits>
@@ -155,7 +158,8 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const IO* __restrict__ x
 // in LDS in a fixed order and leave as one row of partial sums.
 constexpr int kBwdThreads = 256;
 // Tokens loaded at once, a step ahead of their work, and tokens of a run (at 8 x 2048
-// x 2304, W = 4, us: 2 ahead 100, 4 ahead 107, 1 ahead 118, runs of 64 101).
+// x 2304, W = 4, us: 2 ahead 97, 4 ahead 101, 1 ahead 114; runs of 16 95, of 64 91,
+// but half the workgroups where there are few).
 constexpr int kBwdAhead = 2, kBwdRun = 32;
 
 template <typename IO, typename DY, int W, int V, int ACT>
@@ -342,8 +346,9 @@ template <typename IO, int W, int V, int ACT>
 hipError_t conv_fwd_typed(const ConvArgs& a, hipStream_t st) {
   const int64_t nvec = (int64_t(a.C) + V - 1) / V;
   const auto runs_of = [&](int64_t run) { return std::max<int64_t>(1, (a.T + run - 1) / run); };
-  // a run long enough that its W - 1 rows read again cost little, short enough
-  // that the runs fill the card, and, where that can be, a grid holds them all
+  // runs of 32 tokens, or fewer where those would not fill the card (16 at 8 x 2048 x
+  // 2304, bf16: three rows in sixteen are read twice), or more where a grid would
+  // not hold them
   int64_t run = 32;
   while (run > 1 && a.B * runs_of(run) * nvec < 256 * 16 * 64) run /= 2;
   while (run < a.T && a.B * runs_of(run) * nvec > kMaxGrid * 256) run *= 2;

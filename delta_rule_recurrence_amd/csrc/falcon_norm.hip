@@ -11,7 +11,9 @@
 // tokens, the next one's loads in flight.  Measured at 8 x 2048 tokens of 12 groups
 // of 64 (bf16, ELU + 1, rows to heads): 12 us, 4.3 TB/s; gradients 26 us and 5 for
 // the parameters' sums (4.9 TB/s).  The index of a token in its sequence comes from a
-// multiply (a 64-bit division by T a token and thread made the 12 us 29).
+// multiply (a 64-bit division by T a token and thread made the 12 us 29).  Groups of
+// more than 2048 channels keep the gradients' sums in memory, not in registers:
+// 2^18 tokens of 4096 take 12.4 ms, 2^19 of 2048 3.2.
 
 #include <algorithm>
 

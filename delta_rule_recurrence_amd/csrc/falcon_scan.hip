@@ -86,9 +86,9 @@ struct Chunks {
 // product u B and a multiply-add for the state and one for the read (4 each).
 // What a token and a channel need once is worked out by one lane of a quad for
 // every fourth token and handed round by quad permutes.  8 x 2048 x 1536, N = 16:
-// 111 us, of which the vector units are busy 90 %; two scans a wave from zero and
-// from the joined states (no waiting, every product twice) took 176, and decays that
-// the compiler had let sink below the wait 130.
+// 112 us, the vector units busy 81 % of the time (of 127 us under the profiler); two
+// scans a wave from zero and from the joined states (no waiting, every product twice)
+// took 176, and decays that the compiler had let sink below the wait 130.
 constexpr int kTok = 16;
 
 template <int N>
@@ -380,6 +380,7 @@ __device__ __forceinline__ void run_alone(const ScanDims& d, const ScanIn<IO>& i
   }
 }
 
+// (Three waves a SIMD keep 1 to 6 registers in memory with N = 32, none with 16.)
 template <typename IO, int N, bool SOFTPLUS>
 __global__ __launch_bounds__(64 * kFwdWaves, N == 16 || N == 32 ? 3 : 2) void scan_fwd_kernel(
     ScanDims d, ScanIn<IO> in, bool wide, Chunks k, IO* __restrict__ y, float* __restrict__ S_T, int limit) {
@@ -740,10 +741,11 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(int D, int N, int64_t s
 // and over its channel tiles in LDS, over the waves at the end, in this order;
 // workgroups of other channels leave rows of partial sums.  What sums over tokens
 // (dA, dD, ddt_bias) leaves as one row a chunk.  8 x 2048 x 768, N = 16: maps 68 us,
-// carry 14, this kernel 185, sums 10; bound by the vector units (about 100
+// carry 14, this kernel 188, sums 10; bound by the vector units (about 100
 // instructions a token and wave) at two waves a SIMD, which the 128 registers of
-// decays and states allow.  Eights instead of sixteens (fewer registers, more maps)
-// ran slower.
+// decays and states allow.  (With N = 8 they do not: 41 to 57 registers a lane are
+// kept in memory, and 8 x 2048 x 768 takes 256 us.)  Eights instead of sixteens
+// (fewer registers, more maps) ran slower at N = 16.
 constexpr int kBwdWaves = 4;
 template <int N>
 constexpr int kChunkTokens = N <= 16 ? 64 : 1024 / N;   // so that LDS holds the sums of 2 N a token and wave
@@ -1065,9 +1067,13 @@ bool fours_wide(const ScanArgs& a) { return a.b_row % 4 == 0 && a.c_row % 4 == 0
 // Cutting works out every decay twice and takes two launches more, so it pays only
 // where a long chain of turns would leave most of the card idle (D = 1536, N = 16,
 // us, one chunk against cut): B = 1: T = 256: 12 and 19, T = 1024: 34 and 25,
-// T = 4096: 119 and 60; B = 2: T = 1024: 34 and 37, T = 4096: 120 and 110.  768
-// workgroups are one round of three a CU; 1024 (1 x 16384 x 768: 126 us against
-// 107) and 2560 (112) are not.
+// T = 4096: 119 and 60; B = 2: T = 1024: 34 and 37, T = 4096: 120 and 110.  With
+// N = 8 (48 workgroups): T = 256: 13 and 19, T = 768: 29 and 23, T = 4096: 132 and
+// 48; with N = 64 (96 workgroups): T = 256: 12 and 19, T = 768: 27 and 29, T = 1024:
+// 35 and 30, T = 4096: 123 and 72.  768 workgroups are one round of three a CU for
+// N = 16 and 32; 1024 (1 x 16384 x 768: 126 us against 107) and 2560 (112) are not.
+// N = 8 and 64 run two a CU, and yet 512 workgroups are slower there, too (T = 4096:
+// 62 us against 48, and 91 against 72).
 constexpr int64_t kCutBelow = 128, kCutInto = 768;
 constexpr int kCutFrom = 768;
 struct FwdShape {
