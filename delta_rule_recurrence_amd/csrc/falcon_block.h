@@ -1,5 +1,5 @@
 // Host-side launch interface of the operators around the recurrence (short
-// convolution, group norm, selective scan).  Arguments reaching the launchers
+// convolution, group norm, selective scan, linear attention, residual update).  Arguments reaching the launchers
 // have been validated.
 #pragma once
 
@@ -109,6 +109,70 @@ hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st);
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st);
 size_t scan_bwd_workspace_bytes(const ScanArgs& a);
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st);
+
+// Elements from one sequence, head and token of a tensor to the next.
+struct HeadSteps {
+  int64_t b, h, t;
+};
+
+struct LinearArgs {
+  int B, H, T, dk, dv;
+  bool bf16;
+  float scale;
+  HeadSteps q_at, k_at, v_at, o_at;   // o_at: of o or dO; gradients lie as their inputs, dense
+  HeadSteps dqk_at, dv_at;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_decay;
+  const float* S0;         // may be null (zero)
+  const int32_t* lengths;  // may be null
+  void* o;
+  float* S_T;              // may be null; may be S0
+  float* workspace;
+  // single token
+  float* S;
+  const uint8_t* is_first;  // may be null
+  // backward
+  const void* dO;
+  const float* dS_T;       // may be null
+  float* dq;
+  float* dk_out;
+  float* dv_out;
+  float* dS0;              // may be null
+  float* dlog_decay;       // may be null
+};
+
+size_t linear_workspace_bytes(const LinearArgs& a);
+hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_step(const LinearArgs& a, hipStream_t st);
+size_t linear_bwd_workspace_bytes(const LinearArgs& a);
+hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st);
+
+// One launch over every tile of every head: see falcon_linear_kernel.h.
+struct LinearSweep {
+  const void* q;           // null without outputs
+  const void* k;
+  const void* v;
+  void* out;               // null: the tiles' sums into their slots
+  HeadSteps q_at, k_at, v_at, out_at;
+  const float* log_decay;
+  const int32_t* lengths;  // may be null
+  const float* start;      // the state before the first chunk where there are no slots; may be null (zero)
+  float* last;             // the state behind the last chunk, of one tile a head; may be null
+  float* slots;            // [heads][slots_each] states, tile t's at slot0 + t; may be null
+  int64_t slots_each;
+  int slot0;
+  int64_t heads;
+  int H, T, dv, tiles, chunks;   // chunks: of a tile
+  int sf, sc;              // a state's element (f, c) lies at f sf + c sc
+  float read, write;       // factors of what is read and of what is written
+  bool rev, bf16, out_bf16;
+};
+hipError_t launch_linear_sweep_16(const LinearSweep& s, hipStream_t st);
+hipError_t launch_linear_sweep_32(const LinearSweep& s, hipStream_t st);
+hipError_t launch_linear_sweep_64(const LinearSweep& s, hipStream_t st);
+hipError_t launch_linear_sweep_128(const LinearSweep& s, hipStream_t st);
 
 // Columns of `parts` rows of n partial sums, `row` floats from one to the next, summed
 // in a fixed order: column i goes to out[0][i] below ends[0], to out[1][i - ends[0]] below ends[1], else to

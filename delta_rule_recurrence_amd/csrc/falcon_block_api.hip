@@ -2,8 +2,6 @@
 // dispatch.  Nothing here allocates or synchronises.
 #include <math.h>
 
-#include <initializer_list>
-
 #include "falcon.h"
 #include "falcon_block.h"
 #include "falcon_check.h"
@@ -11,58 +9,23 @@
 namespace {
 
 using falcon::aligned16;
+using falcon::all_aligned;
+using falcon::any_overlap;
 using falcon::ConvArgs;
+using falcon::dtype_bytes;
+using falcon::dtype_ok;
+using falcon::elems;
+using falcon::finish;
+using falcon::kMaxTokens;
 using falcon::NormArgs;
 using falcon::overlap;
 using falcon::Range;
+using falcon::rows_bytes;
+using falcon::rows_ok;
 using falcon::ScanArgs;
-
-// Largest element count of one tensor; every index then fits an int64_t with
-// room to spare, and every grid its 32 bits.
-constexpr int64_t kMaxElems = int64_t(1) << 40;
-// Most tokens of one call: token indices and what is added to them fit an int.
-constexpr int64_t kMaxTokens = int64_t(1) << 30;
 
 // Longest row of the scan's inputs: 64 rows of float32 stay within 2^30 bytes.
 constexpr int64_t kMaxScanRow = int64_t(1) << 22;
-
-// a b c (each >= 0), or -1 beyond kMaxElems.
-int64_t elems(int64_t a, int64_t b, int64_t c = 1) {
-  const __int128 n = static_cast<__int128>(a) * b * c;
-  return n > kMaxElems ? -1 : static_cast<int64_t>(n);
-}
-
-bool all_aligned(std::initializer_list<const void*> ptrs) {
-  for (const void* q : ptrs)
-    if (q && !aligned16(q)) return false;
-  return true;
-}
-
-// True when any of `outs` overlaps another of them or one of `ins`.
-bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-  for (const Range* a = outs.begin(); a != outs.end(); ++a) {
-    for (const Range* b = a + 1; b != outs.end(); ++b)
-      if (overlap(*a, *b)) return true;
-    for (const Range& r : ins)
-      if (overlap(*a, r)) return true;
-  }
-  return false;
-}
-
-// Bytes from the first to the last element of `rows` rows.
-int64_t rows_bytes(int64_t rows, int64_t row, int64_t width, int64_t es) {
-  return rows > 0 && width > 0 ? ((rows - 1) * row + width) * es : 0;
-}
-
-// Whether `rows` rows of `width` elements, `row` apart, are valid.
-bool rows_ok(int64_t rows, int64_t row, int64_t width) {
-  return row >= width && row <= (int64_t(1) << 31) && elems(rows, row) >= 0;
-}
-
-bool dtype_ok(int32_t t) { return t == FALCON_F32 || t == FALCON_BF16; }
-int64_t dtype_bytes(int32_t t) { return t == FALCON_BF16 ? 2 : 4; }
-
-falcon_status finish(hipError_t e) { return e == hipSuccess ? FALCON_OK : FALCON_ERR_HIP; }
 
 // ---- convolution ---------------------------------------------------------------
 falcon_status check_conv(const falcon_conv_problem* p, bool step, ConvArgs* a) {

@@ -49,6 +49,13 @@ class FalconScanProblem(ctypes.Structure):
                 ("b_row", ctypes.c_int64), ("c_row", ctypes.c_int64)]
 
 
+class FalconLinearProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("T", ctypes.c_int32), ("dk", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("qk_heads", ctypes.c_int32),
+                ("v_heads", ctypes.c_int32), ("o_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "falcon_abi_version": (ctypes.c_int32, []),
@@ -82,6 +89,11 @@ _SIGNATURES = {
     "falcon_scan_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconScanProblem)]),
     "falcon_scan_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconScanProblem)] + [_P] * 11 + [ctypes.c_int32]
                         + [_P] * 11 + [ctypes.c_size_t, _P]),
+    "falcon_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconLinearProblem)]),
+    "falcon_linear_fwd": (ctypes.c_int32, [ctypes.POINTER(FalconLinearProblem)] + [_P] * 9 + [ctypes.c_size_t, _P]),
+    "falcon_linear_step": (ctypes.c_int32, [ctypes.POINTER(FalconLinearProblem)] + [_P] * 8),
+    "falcon_linear_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconLinearProblem)]),
+    "falcon_linear_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconLinearProblem)] + [_P] * 14 + [ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -368,7 +380,8 @@ def falcon_bwd_chunked(phi_k, phi_q, v, beta, lam, dO, *, S0=None, k_prev=None, 
     return g
 
 
-# ---- around the recurrence: short convolution, group norm, selective scan ------
+# ---- around the recurrence: short convolution, group norm, selective scan,
+#      linear attention ------------------------------------------------------------
 #
 # Channels-last "rows" inputs ([B, T, width], or [B, width] for single tokens)
 # may be some of the columns of a wider contiguous projection; everything else
@@ -802,4 +815,137 @@ def falcon_scan_bwd(x, dt, A, B, C, dy, *, D=None, dt_bias=None, softplus=True, 
             ctypes.byref(p), _ref(x), _ref(dt), _ref(A), _ref(B), _ref(C), _ref(D), _ref(dt_bias), _ref(z), _ref(S0),
             _ref(lengths), _ref(dy), dy_dtype, _ref(dS_T), _ref(g["dx"]), _ref(g["ddt"]), _ref(g["dz"]), _ref(g["dA"]),
             _ref(g["dB"]), _ref(g["dC"]), _ref(g["dD"]), _ref(g["ddt_bias"]), _ref(g["dS0"]), _ref(workspace), have, st))
+    return g
+
+
+def _by_head(t, name, layout, shape, io, dev):
+    """Checks a tensor of heads ([B, H, T, d], ``shape``) in either layout;
+    elements from one row to the next."""
+    B, H, T, d = shape
+    if layout == "heads":
+        _need(t, name, shape, io, dev)
+        return H * d
+    return _row_step(t, name, (B, T, H * d), io, dev)
+
+
+def _laid(layout, B, H, T, d):
+    return (B, H, T, d) if layout == "heads" else (B, T, H * d)
+
+
+def _linear_setup(q, k, v, log_decay, scale, qk_layout, v_layout, o_layout):
+    for name, layout in (("qk_layout", qk_layout), ("v_layout", v_layout), ("o_layout", o_layout)):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"{name}: expected \"rows\" or \"heads\", got {layout!r}")
+    if not isinstance(log_decay, torch.Tensor) or log_decay.dim() != 1 or log_decay.shape[0] < 1:
+        raise ValueError("log_decay: expected an [H] tensor")
+    H = log_decay.shape[0]
+    sizes = []
+    for name, t, layout in (("q", q, qk_layout), ("v", v, v_layout)):
+        heads = layout == "heads"
+        if not isinstance(t, torch.Tensor) or t.dim() != (4 if heads else 3):
+            raise ValueError(f"{name}: expected a [B, H, T, d] tensor" if heads else f"{name}: expected a [B, T, H d] tensor")
+        if t.shape[1] != H if heads else t.shape[2] % H != 0:
+            raise ValueError(f"{name}: {H} heads do not fit its shape {tuple(t.shape)}")
+        sizes.append((t.shape[0], H, *t.shape[2:]) if heads else (t.shape[0], H, t.shape[1], t.shape[2] // H))
+    B, H, T, dk = sizes[0]
+    dv = sizes[1][3]
+    io, dev = _io_dtype(q, "q"), q.device
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    rows = [_by_head(q, "q", qk_layout, (B, H, T, dk), io, dev), _by_head(k, "k", qk_layout, (B, H, T, dk), io, dev),
+            _by_head(v, "v", v_layout, (B, H, T, dv), io, dev)]
+    return io, dev, FalconLinearProblem(B, H, T, dk, dv, DTYPES[io], int(qk_layout == "heads"), int(v_layout == "heads"),
+                                        int(o_layout == "heads"), scale, *rows)
+
+
+def falcon_linear_workspace_bytes(problem: FalconLinearProblem) -> int:
+    return int(load_library().falcon_linear_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_linear_fwd(q, k, v, log_decay, *, scale=1.0, S0=None, lengths=None, qk_layout="heads", v_layout="heads",
+                      o_layout="heads", o=None, S_T=None, workspace=None, return_state=True, stream=None):
+    """Linear attention with a decay for each head (``log_decay [H]``, at most
+    zero); returns ``(o, S_T)``.
+
+    ``S_t = exp(log_decay) S_(t-1) + k_t v_t'`` and ``o_t = scale S_t' q_t``.
+    ``q`` and ``k``, ``v`` and ``o`` are each ``[B, H, T, d]`` ("heads") or
+    ``[B, T, H d]`` ("rows"), with d in 16, 32, 64, 128.  ``S0`` and ``S_T`` are
+    ``[B, H, dk, dv]`` float32; ``lengths`` (``[B]`` int32) marks padded
+    sequences: ``S_T`` is the state at the end, rows of ``o`` behind it stay as
+    they were, or zero when ``o`` is allocated here.
+    """
+    io, dev, p = _linear_setup(q, k, v, log_decay, scale, qk_layout, v_layout, o_layout)
+    state, out = (p.B, p.H, p.dk, p.dv), _laid(o_layout, p.B, p.H, p.T, p.dv)
+    _need(S0, "S0", state, torch.float32, dev, optional=True)
+    _need(lengths, "lengths", (p.B,), torch.int32, dev, optional=True)
+    _need(o, "o", out, io, dev, optional=True)
+    _need(S_T, "S_T", state, torch.float32, dev, optional=True)
+    need = falcon_linear_workspace_bytes(p)
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    with _on_stream(dev, stream) as st:
+        if o is None:
+            o = _new(out, io, dev, lengths)
+        if S_T is None and return_state:
+            S_T = torch.empty(state, dtype=torch.float32, device=dev)
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_linear_fwd(
+            ctypes.byref(p), _ref(q), _ref(k), _ref(v), _ref(log_decay), _ref(S0), _ref(lengths), _ref(o), _ref(S_T),
+            _ref(workspace), have, st))
+    return o, S_T
+
+
+def falcon_linear_step(q, k, v, log_decay, S, *, scale=1.0, is_first=None, o=None, stream=None):
+    """One token of every sequence (``q, k [B, H, dk]``, ``v [B, H, dv]``); moves
+    ``S [B, H, dk, dv]`` on in place and returns ``o [B, H, dv]``.  ``is_first``
+    (``[B]`` bytes) marks sequences whose state so far counts as zero."""
+    for name, t in (("q", q), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name}: expected a [B, H, d] tensor")
+    B, H, dk = q.shape
+    dv = v.shape[2]
+    io, dev = _io_dtype(q, "q"), q.device
+    rows = [_row_step(t, name, (B, H, d), io, dev, 2) for t, name, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv))]
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    _need(S, "S", (B, H, dk, dv), torch.float32, dev)
+    _expect(is_first, "is_first", (B,), (torch.uint8, torch.bool), dev, optional=True)
+    _need(o, "o", (B, H, dv), io, dev, optional=True)
+    p = FalconLinearProblem(B, H, 1, dk, dv, DTYPES[io], 0, 0, 0, scale, *rows)
+    with _on_stream(dev, stream) as st:
+        if o is None:
+            o = torch.empty((B, H, dv), dtype=io, device=dev)
+        _check(load_library().falcon_linear_step(ctypes.byref(p), _ref(q), _ref(k), _ref(v), _ref(log_decay), _ref(S),
+                                                 _ref(is_first), _ref(o), st))
+    return o
+
+
+def falcon_linear_bwd_workspace_bytes(problem: FalconLinearProblem) -> int:
+    return int(load_library().falcon_linear_bwd_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_linear_bwd(q, k, v, log_decay, dO, *, scale=1.0, S0=None, lengths=None, dS_T=None, learned_decay=False,
+                      qk_layout="heads", v_layout="heads", o_layout="heads", grads=None, workspace=None, stream=None):
+    """Gradients of ``<dO, o> + <dS_T, S_T>``: a dict of float32 tensors dq, dk
+    and dv (in the layouts of q, k and v; zero behind the sequences' ends), dS0
+    (None without an S0) and dlog_decay (None unless ``learned_decay``); either
+    of the last two may still be asked for through ``grads``.  ``dO`` has o's
+    layout and type."""
+    io, dev, p = _linear_setup(q, k, v, log_decay, scale, qk_layout, v_layout, o_layout)
+    state = (p.B, p.H, p.dk, p.dv)
+    _need(S0, "S0", state, torch.float32, dev, optional=True)
+    _need(lengths, "lengths", (p.B,), torch.int32, dev, optional=True)
+    _need(dO, "dO", _laid(o_layout, p.B, p.H, p.T, p.dv), io, dev)
+    _need(dS_T, "dS_T", state, torch.float32, dev, optional=True)
+    by_qk, by_v = _laid(qk_layout, p.B, p.H, p.T, p.dk), _laid(v_layout, p.B, p.H, p.T, p.dv)
+    shapes = {"dq": by_qk, "dk": by_qk, "dv": by_v, "dlog_decay": (p.H,), "dS0": state}
+    g = _grads(grads, shapes, dev)
+    missing = {"dlog_decay": not learned_decay, "dS0": S0 is None}
+    need = falcon_linear_bwd_workspace_bytes(p)
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    with _on_stream(dev, stream) as st:
+        for name, shape in shapes.items():
+            if g.get(name) is None:
+                g[name] = None if missing.get(name) else torch.empty(shape, dtype=torch.float32, device=dev)
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_linear_bwd(
+            ctypes.byref(p), _ref(q), _ref(k), _ref(v), _ref(log_decay), _ref(S0), _ref(lengths), _ref(dO), _ref(dS_T),
+            _ref(g["dq"]), _ref(g["dk"]), _ref(g["dv"]), _ref(g["dlog_decay"]), _ref(g["dS0"]), _ref(workspace), have, st))
     return g

@@ -300,7 +300,8 @@ size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
  *   falcon_norm_*  the group norm with an activation, a token's head at a time:
  *                  it makes phi(k) and phi(q) in the [B, H, T, dk] layout that
  *                  falcon_fwd_* read, and norms the [B, H, T, dv] outputs;
- *   falcon_scan_*  the selective state space scan.
+ *   falcon_scan_*  the selective state space scan;
+ *   falcon_linear_*  linear attention with a decay for each head.
  * Status codes, streams, the order of checks and launches and the absence of
  * allocation are those of the entry points above.  Also:
  *  - "Rows" tensors are channels last, [B, T, width].  Where a field *_row is
@@ -510,6 +511,77 @@ falcon_status falcon_scan_bwd(const falcon_scan_problem* p, const void* x, const
                               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 size_t falcon_scan_bwd_workspace_bytes(const falcon_scan_problem* p);
+
+/*
+ * falcon_linear_fwd -- linear attention with a decay for each head.  Head h of H
+ * has a state S of dk x dv numbers and forgets at one rate:
+ *
+ *     S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T
+ *     o_t = scale S_t^T q_t
+ *
+ * The read comes after the write.  It is the recurrences' plain relative: no shift,
+ * no step size, a decay that does not depend on the token.
+ *
+ *  q, k       : heads [B, H, T, dk] (qk_heads; contiguous, q_row and k_row are
+ *               ignored) or rows [B, T, H dk] of q_row and k_row elements, io dtype.
+ *  v          : heads [B, H, T, dv] (v_heads) or rows [B, T, H dv] of v_row.
+ *               Rows are a multiple of 16 bytes apart (FALCON_ERR_ALIGN).
+ *  log_decay  : [H] float32, at most 0; -infinity leaves each token to itself, 0
+ *               forgets nothing.  Not checked.
+ *  S0         : [B, H, dk, dv] float32, or NULL for zero.
+ *  o          : heads [B, H, T, dv] (o_heads) or rows [B, T, H dv], io dtype.
+ *  S_T        : [B, H, dk, dv] float32, the state at each sequence's end, or NULL;
+ *               may alias S0 exactly.
+ *  workspace  : at least falcon_linear_workspace_bytes(p) bytes (may be NULL when
+ *               that is 0), 16-byte aligned, overlapping nothing else.
+ * dk, dv in {16, 32, 64, 128}; at most 2^22 heads (B H).  The prompt is worked on in
+ * chunks of 64 tokens: float32 throughout with float32 inputs, and with bf16 inputs
+ * by bf16 products with float32 sums in which every float32 operand is a sum of two
+ * bf16 numbers (three for the state and for gradients), so results are those of
+ * float32 arithmetic, rounded once.  A token whose values are not finite reaches the
+ * outputs of its sequence from the start of its chunk on.
+ */
+typedef struct {
+  int32_t B, H, T, dk, dv;
+  int32_t io_dtype;
+  int32_t qk_heads, v_heads, o_heads;   /* 0: rows, 1: heads */
+  float scale;                          /* finite */
+  int64_t q_row, k_row, v_row;
+} falcon_linear_problem;
+
+falcon_status falcon_linear_fwd(const falcon_linear_problem* p, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* S0,
+                                const int32_t* lengths, void* o, float* S_T, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+size_t falcon_linear_workspace_bytes(const falcon_linear_problem* p);
+
+/*
+ * falcon_linear_step -- one token of every sequence: q and k are [B, H dk] with rows of
+ * q_row and k_row, v is [B, H dv] with rows of v_row, o [B, H dv]; p->T and the layouts
+ * are ignored, S ([B, H, dk, dv] float32) moves on IN PLACE.  is_first, [B] bytes or
+ * NULL: a nonzero entry marks a sequence whose state before this token counts as zero,
+ * whatever S holds.  Arithmetic is float32.
+ */
+falcon_status falcon_linear_step(const falcon_linear_problem* p, const void* q, const void* k,
+                                 const void* v, const float* log_decay, float* S,
+                                 const uint8_t* is_first, void* o, hipStream_t stream);
+
+/*
+ * falcon_linear_bwd -- gradients of <dO, o> + <dS_T, S_T>; the states are recomputed.
+ *  dO         : io dtype, in o's layout;  dS_T : [B, H, dk, dv] float32 or NULL.
+ *  dq, dk, dv : float32, contiguous, in the layouts of q and k, and of v.
+ *  dlog_decay : [H] float32, or NULL to skip.
+ *  dS0        : [B, H, dk, dv] float32, or NULL to skip.
+ *  workspace  : at least falcon_linear_bwd_workspace_bytes(p) bytes.
+ */
+falcon_status falcon_linear_bwd(const falcon_linear_problem* p, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* S0,
+                                const int32_t* lengths, const void* dO, const float* dS_T,
+                                float* dq, float* dk, float* dv, float* dlog_decay, float* dS0,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t falcon_linear_bwd_workspace_bytes(const falcon_linear_problem* p);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,256 @@
+"""Linear attention with a decay for each head against its oracle, on the GPU."""
+
+import numpy as np
+import pytest
+import torch
+
+from delta_rule_recurrence_amd import falcon as fb
+from oracle import linear_oracle as lo
+
+from block_utils import IO, close, columns, cuda, draws, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(B, H, T, dk, dv, io, seed, carry=True, decay=None):
+    n = draws(seed)
+    d = dict(q=n(B, H, T, dk, dtype=io), k=n(B, H, T, dk, dtype=io), v=n(B, H, T, dv, dtype=io), dO=n(B, H, T, dv, dtype=io),
+             S0=n(B, H, dk, dv) if carry else None, dS_T=n(B, H, dk, dv, scale=dk ** -0.5) if carry else None)
+    # decays from next to none to nearly all of a token
+    d["log_decay"] = -torch.exp(torch.linspace(-6.0, 1.0, H)) if decay is None else torch.full((H,), decay)
+    return d
+
+
+def depth(T, dk):
+    """Terms of one result: the tokens it sums and the products over a key."""
+    return T + dk
+
+
+def rows(t):
+    """[B, T, H d] of [B, H, T, d]."""
+    return t.transpose(1, 2).flatten(2).contiguous()
+
+
+def by(layout, t, wide=False):
+    if layout == "heads":
+        return t.cuda()
+    return columns(rows(t)) if wide else rows(t).cuda()
+
+
+def heads(t, layout, H):
+    """[B, H, T, d] of either layout."""
+    return t if layout == "heads" else t.unflatten(-1, (H, -1)).transpose(1, 2)
+
+
+def check_forward(d, *, scale=0.3, lengths=None, layouts=("heads",) * 3, wide=False, what="", **kw):
+    H, (T, dk) = d["q"].shape[1], d["q"].shape[2:]
+    ends = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+    q, k, v = by(layouts[0], d["q"], wide), by(layouts[0], d["k"], wide), by(layouts[1], d["v"], wide)
+    o, S_T = fb.falcon_linear_fwd(q, k, v, d["log_decay"].cuda(), scale=scale, S0=cuda(d["S0"]), lengths=cuda(ends),
+                                  qk_layout=layouts[0], v_layout=layouts[1], o_layout=layouts[2], **kw)
+    torch.cuda.synchronize()
+    want, S_want = lo.linear_forward(f64(d["q"]), f64(d["k"]), f64(d["v"]), f64(d["log_decay"]), scale=scale, S0=f64(d["S0"]),
+                                     lengths=lengths)
+    close(heads(o, layouts[2], H), want, depth(T, dk), f"{what} o")
+    close(S_T, S_want, depth(T, dk), f"{what} S_T")
+    return o, S_T
+
+
+def check_backward(d, *, scale=0.3, lengths=None, layouts=("heads",) * 3, wide=False, what="", learned=True, **kw):
+    H, (T, dk), dv = d["q"].shape[1], d["q"].shape[2:], d["v"].shape[-1]
+    ends = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+    q, k, v = by(layouts[0], d["q"], wide), by(layouts[0], d["k"], wide), by(layouts[1], d["v"], wide)
+    g = fb.falcon_linear_bwd(q, k, v, d["log_decay"].cuda(), by(layouts[2], d["dO"]), scale=scale, S0=cuda(d["S0"]),
+                             lengths=cuda(ends), dS_T=cuda(d["dS_T"]), learned_decay=learned, qk_layout=layouts[0],
+                             v_layout=layouts[1], o_layout=layouts[2], **kw)
+    torch.cuda.synchronize()
+    want = lo.linear_backward(f64(d["q"]), f64(d["k"]), f64(d["v"]), f64(d["log_decay"]), f64(d["dO"]), scale=scale,
+                              S0=f64(d["S0"]), lengths=lengths, dS_T=f64(d["dS_T"]))
+    for name, layout in (("dq", layouts[0]), ("dk", layouts[0]), ("dv", layouts[1])):
+        close(heads(g[name], layout, H), want[name], depth(T, max(dk, dv)), f"{what} {name}")
+    if d["S0"] is not None:
+        close(g["dS0"], want["dS0"], depth(T, dv), f"{what} dS0")
+    if learned:
+        # A head's gradient sums terms of both signs over all tokens and pairs, each a
+        # product of float32 results weighted by up to a tile's tokens; its error is
+        # measured against the terms' size, sum over tokens of (distance to the tile's
+        # end) |k . dk| + |q . dq|, of which float32 keeps UNIT a term and operation.
+        L = min(T, 4096)
+        size = (np.abs((f64(d["q"]) * want["dq"]).sum(-1)) + np.abs((f64(d["k"]) * want["dk"]).sum(-1))).sum((0, 2)) * L
+        err = np.abs(f64(g["dlog_decay"]) - want["dlog_decay"])
+        print(f"{what} dlog_decay: {(err / (size + 1e-30)).max():.2e} of the terms", flush=True)
+        assert np.all(err <= 4 * (16 + depth(T, max(dk, dv))) * 2.0 ** -24 * size + 1e-30), f"{what} dlog_decay: {err} of {size}"
+        assert np.linalg.norm(err) <= 1e-4 * np.linalg.norm(want["dlog_decay"]) + 1e-6
+    return g
+
+
+WIDTHS = [(16, 16), (16, 128), (32, 64), (64, 32), (64, 64), (64, 128), (128, 16), (128, 64), (128, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", WIDTHS)
+def test_widths(dk, dv, dtype):
+    d = inputs(2, 3, 150, dk, dv, IO[dtype], 40 + dk + dv)
+    check_forward(d, what=f"{dk}x{dv} {dtype}")
+    check_backward(d, what=f"{dk}x{dv} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300])
+def test_lengths_of_prompts(T, dtype):
+    d = inputs(1, 2, T, 32, 32, IO[dtype], 60 + T)
+    check_forward(d, what=f"T={T} {dtype}")
+    check_backward(d, what=f"T={T} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,T", [(1, 1, 1500), (1, 3, 2049), (3, 40, 260), (2, 400, 130)])
+def test_tiles(B, H, T, dtype):
+    """One head in many tiles, many heads in one."""
+    d = inputs(B, H, T, 16, 32, IO[dtype], 90 + T)
+    check_forward(d, what=f"{B}x{H}x{T} {dtype}")
+    check_backward(d, what=f"{B}x{H}x{T} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layouts", [("rows", "rows", "rows"), ("rows", "heads", "rows"), ("heads", "rows", "heads")])
+def test_layouts_and_columns(layouts, dtype):
+    d = inputs(2, 3, 140, 32, 64, IO[dtype], 120)
+    check_forward(d, layouts=layouts, wide=True, what=f"{layouts} {dtype}")
+    check_backward(d, layouts=layouts, wide=True, what=f"{layouts} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[0, 1, 64, 200], [65, 200, 0, 199], [0, 0, 0, 0]])
+def test_padded_batches(lengths, dtype):
+    """Rows behind the ends are not read, outputs there stay, gradients are zero."""
+    io, T = IO[dtype], 200
+    d = inputs(4, 2, T, 32, 32, io, 130)
+    for b, n in enumerate(lengths):
+        for name in ("q", "k", "v", "dO"):
+            d[name][b, :, n:] = float("nan")
+    clean = {n: None if t is None else torch.nan_to_num(t) for n, t in d.items()}
+    o = torch.full((4, 2, T, 32), 7.0, dtype=io, device="cuda")
+    ends = torch.tensor(lengths, dtype=torch.int32)
+    D = {n: cuda(t) for n, t in d.items()}
+    o, S_T = fb.falcon_linear_fwd(D["q"], D["k"], D["v"], D["log_decay"], S0=D["S0"], lengths=ends.cuda(), o=o)
+    want, S_want = lo.linear_forward(*(f64(clean[n]) for n in ("q", "k", "v", "log_decay")), S0=f64(d["S0"]), lengths=lengths)
+    for b, n in enumerate(lengths):
+        assert torch.all(o[b, :, n:] == 7.0)
+        o[b, :, n:] = 0.0
+    close(o, want, depth(T, 32), "o")
+    close(S_T, S_want, depth(T, 32), "S_T")
+    g = fb.falcon_linear_bwd(D["q"], D["k"], D["v"], D["log_decay"], D["dO"], S0=D["S0"], dS_T=D["dS_T"], lengths=ends.cuda(),
+                             learned_decay=True)
+    gw = lo.linear_backward(*(f64(clean[n]) for n in ("q", "k", "v", "log_decay", "dO")), S0=f64(d["S0"]), dS_T=f64(d["dS_T"]),
+                            lengths=lengths)
+    for name in ("dq", "dk", "dv", "dS0"):
+        close(g[name], gw[name], depth(T, 32), name)
+        if name != "dS0":
+            for b, n in enumerate(lengths):
+                assert torch.all(g[name][b, :, n:] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", [0.0, -1e-4, -20.0, -float("inf")])
+def test_decays(decay, dtype):
+    """Nothing forgotten, hardly anything, all but the token's own."""
+    d = inputs(1, 2, 400, 32, 32, IO[dtype], 140, decay=decay)
+    check_forward(d, what=f"log_decay={decay} {dtype}")
+    if decay != -float("inf"):
+        check_backward(d, what=f"log_decay={decay} {dtype}", learned=decay > -1.0)
+        return
+    g = fb.falcon_linear_bwd(*(d[n].cuda() for n in ("q", "k", "v", "log_decay", "dO")), S0=cuda(d["S0"]))
+    want = lo.linear_backward(*(f64(d[n]) for n in ("q", "k", "v", "log_decay", "dO")))
+    for name in ("dq", "dk", "dv"):
+        close(g[name], want[name], depth(1, 32), name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_without_states(dtype):
+    d = inputs(2, 2, 190, 64, 64, IO[dtype], 150, carry=False)
+    o, S_T = check_forward(d)
+    check_backward(d)
+    D = {n: cuda(t) for n, t in d.items()}
+    o2, none = fb.falcon_linear_fwd(D["q"], D["k"], D["v"], D["log_decay"], scale=0.3, return_state=False)
+    assert none is None and torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_in_parts_and_state_in_place(dtype):
+    d = inputs(2, 3, 300, 32, 64, IO[dtype], 160)
+    D = {n: cuda(t) for n, t in d.items()}
+    S, parts = D["S0"].clone(), []
+    for a, b in ((0, 70), (70, 71), (71, 300)):
+        cut = [D[n][:, :, a:b].contiguous() for n in "qkv"]
+        part, S2 = fb.falcon_linear_fwd(*cut, D["log_decay"], S0=S, S_T=S)
+        assert S2 is S
+        parts.append(part)
+    want, S_want = lo.linear_forward(*(f64(d[n]) for n in ("q", "k", "v", "log_decay")), S0=f64(d["S0"]))
+    close(torch.cat(parts, 2), want, depth(300, 32), "o")
+    close(S, S_want, depth(300, 32), "S_T")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 1, 16, 16), (3, 2, 32, 16), (2, 5, 64, 64), (2, 3, 16, 128), (2, 3, 128, 128)])
+def test_single_tokens(B, H, dk, dv, dtype):
+    """Token after token against the oracle's sequence; a fresh start in between."""
+    io, T = IO[dtype], 6
+    d = inputs(B, H, T, dk, dv, io, 170 + dk)
+    D = {n: cuda(t) for n, t in d.items()}
+    S = D["S0"].clone()
+    first = torch.zeros(B, dtype=torch.uint8)
+    first[-1] = 1
+    S[-1] = float("nan")   # counts as zero
+    S0 = d["S0"].clone()
+    S0[-1] = 0.0
+    want, S_want = lo.linear_forward(*(f64(d[n]) for n in ("q", "k", "v", "log_decay")), scale=0.3, S0=f64(S0))
+    outs = []
+    for t in range(T):
+        q, k, v = (D[n][:, :, t].contiguous() for n in "qkv")
+        if t % 2:   # columns of a wider projection
+            q, k, v = (columns(x.cpu().flatten(1)).unflatten(1, (H, -1)) for x in (q, k, v))
+        outs.append(fb.falcon_linear_step(q, k, v, D["log_decay"], S, scale=0.3, is_first=first.cuda() if t == 0 else None))
+    close(torch.stack(outs, 2), want, depth(T, dk), "o")
+    close(S, S_want, depth(T, dk), "S")
+
+
+def test_prompt_then_tokens_float32():
+    d = inputs(2, 3, 80, 64, 64, torch.float32, 180)
+    D = {n: cuda(t) for n, t in d.items()}
+    o, S = fb.falcon_linear_fwd(*(D[n][:, :, :70].contiguous() for n in "qkv"), D["log_decay"], S0=D["S0"])
+    outs = [o]
+    for t in range(70, 80):
+        outs.append(fb.falcon_linear_step(*(D[n][:, :, t].contiguous() for n in "qkv"), D["log_decay"], S)[:, :, None])
+    want, S_want = lo.linear_forward(*(f64(d[n]) for n in ("q", "k", "v", "log_decay")), S0=f64(d["S0"]))
+    close(torch.cat(outs, 2), want, depth(80, 64), "o")
+    close(S, S_want, depth(80, 64), "S")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_values_that_are_not_finite_stay_in_their_sequence(dtype):
+    """From the start of the token's chunk on, in its own head and sequence only."""
+    d = inputs(2, 2, 400, 32, 32, IO[dtype], 190)
+    D = {n: cuda(t) for n, t in d.items()}
+    o, S = fb.falcon_linear_fwd(*(D[n] for n in "qkv"), D["log_decay"], S0=D["S0"])
+    D["v"][1, 0, 200, 3] = float("inf")
+    D["k"][1, 0, 200, 5] = float("nan")
+    p, R = fb.falcon_linear_fwd(*(D[n] for n in "qkv"), D["log_decay"], S0=D["S0"])
+    same = torch.ones(2, 2, 400, dtype=torch.bool, device="cuda")
+    same[1, 0, 192:] = False
+    assert torch.equal(o[same], p[same])
+    assert not torch.isfinite(p[1, 0, 200:]).all(-1).any()
+    assert torch.equal(S[0], R[0]) and torch.equal(S[1, 1], R[1, 1])
+
+
+def test_empty_calls():
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    decay = torch.tensor([-0.5, -0.1], device="cuda")
+    S0 = torch.randn(3, 2, 16, 16, device="cuda")
+    o, S = fb.falcon_linear_fwd(z(3, 2, 0, 16), z(3, 2, 0, 16), z(3, 2, 0, 16), decay, S0=S0)
+    assert o.shape == (3, 2, 0, 16) and torch.equal(S, S0)
+    g = fb.falcon_linear_bwd(z(3, 2, 0, 16), z(3, 2, 0, 16), z(3, 2, 0, 16), decay, z(3, 2, 0, 16), S0=S0, dS_T=S0, learned_decay=True)
+    assert torch.equal(g["dS0"], S0) and torch.all(g["dlog_decay"] == 0)
+    g = fb.falcon_linear_bwd(z(0, 2, 5, 16), z(0, 2, 5, 16), z(0, 2, 5, 16), decay, z(0, 2, 5, 16), learned_decay=True)
+    assert torch.all(g["dlog_decay"] == 0)
+    assert fb.falcon_linear_step(z(0, 2, 16), z(0, 2, 16), z(0, 2, 16), decay, z(0, 2, 16, 16)).shape == (0, 2, 16)
