@@ -9,7 +9,7 @@
 
 namespace falcon {
 
-enum Activation : int { kActNone = 0, kActSilu = 1, kActElu1 = 2 };
+enum Activation : int { kActNone = 0, kActSilu = 1, kActElu1 = 2, kActSigmoid = 3 };
 
 struct ConvArgs {
   int B, T, C, W;
@@ -173,6 +173,44 @@ hipError_t launch_linear_sweep_16(const LinearSweep& s, hipStream_t st);
 hipError_t launch_linear_sweep_32(const LinearSweep& s, hipStream_t st);
 hipError_t launch_linear_sweep_64(const LinearSweep& s, hipStream_t st);
 hipError_t launch_linear_sweep_128(const LinearSweep& s, hipStream_t st);
+
+struct ResidualArgs {
+  int B, T, G, d;
+  bool bf16, stream_bf16;
+  int act;
+  bool post, pre;
+  float eps;
+  int64_t y_row, gate_row;
+  const void* y;              // null in a backward pass from 8 bits
+  const void* gate;           // may be null
+  const void* h;              // may be null (zero)
+  const float* post_weight;   // may be null (one)
+  const float* alpha;         // may be null (one)
+  const float* pre_weight;    // may be null (one)
+  const int32_t* lengths;     // may be null
+  void* h_out;
+  void* n;                    // null without the second norm
+  bool save;                  // 8 bits: written by the forward, read by the backward
+  int8_t* y_codes;
+  uint8_t* y_steps;
+  int8_t* gate_codes;         // null without a gate
+  uint8_t* gate_steps;
+  // backward
+  const void* dh_out;         // may be null (zero)
+  const void* dn;
+  bool dh_out_bf16, dn_bf16;
+  float* dy;
+  float* dgate;               // null without a gate
+  float* dh;                  // may be null
+  float* dalpha;              // may be null
+  float* dpost_weight;        // may be null
+  float* dpre_weight;         // may be null
+  float* workspace;
+};
+
+hipError_t launch_residual_fwd(const ResidualArgs& a, hipStream_t st);
+size_t residual_bwd_workspace_bytes(const ResidualArgs& a);
+hipError_t launch_residual_bwd(const ResidualArgs& a, hipStream_t st);
 
 // Columns of `parts` rows of n partial sums, `row` floats from one to the next, summed
 // in a fixed order: column i goes to out[0][i] below ends[0], to out[1][i - ends[0]] below ends[1], else to

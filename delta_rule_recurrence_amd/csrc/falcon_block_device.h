@@ -85,6 +85,7 @@ template <int ACT>
 __device__ __forceinline__ float act_f32(float p) {
   if constexpr (ACT == kActSilu) return p * sigmoid_f32(p);
   if constexpr (ACT == kActElu1) return p > 0.0f ? p + 1.0f : exp_f32(p);
+  if constexpr (ACT == kActSigmoid) return sigmoid_f32(p);
   return p;
 }
 template <int ACT>
@@ -94,6 +95,10 @@ __device__ __forceinline__ float act_slope_f32(float p) {
     return s * (1.0f + p * (1.0f - s));
   }
   if constexpr (ACT == kActElu1) return p > 0.0f ? 1.0f : exp_f32(p);
+  if constexpr (ACT == kActSigmoid) {
+    const float s = sigmoid_f32(p);
+    return s * (1.0f - s);
+  }
   return 1.0f;
 }
 

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -56,6 +56,18 @@ class FalconLinearProblem(ctypes.Structure):
                 ("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64)]
 
 
+class FalconResidualProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("G", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("y_row", ctypes.c_int64), ("gate_row", ctypes.c_int64)]
+
+
+class FalconSavedPointers(ctypes.Structure):
+    _fields_ = [("y_codes", ctypes.c_void_p), ("y_steps", ctypes.c_void_p), ("gate_codes", ctypes.c_void_p),
+                ("gate_steps", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "falcon_abi_version": (ctypes.c_int32, []),
@@ -94,6 +106,12 @@ _SIGNATURES = {
     "falcon_linear_step": (ctypes.c_int32, [ctypes.POINTER(FalconLinearProblem)] + [_P] * 8),
     "falcon_linear_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconLinearProblem)]),
     "falcon_linear_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconLinearProblem)] + [_P] * 14 + [ctypes.c_size_t, _P]),
+    "falcon_residual_fwd": (ctypes.c_int32, [ctypes.POINTER(FalconResidualProblem)] + [_P] * 9
+                            + [ctypes.POINTER(FalconSavedPointers), _P]),
+    "falcon_residual_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(FalconResidualProblem)]),
+    "falcon_residual_bwd": (ctypes.c_int32, [ctypes.POINTER(FalconResidualProblem)] + [_P] * 2
+                            + [ctypes.POINTER(FalconSavedPointers)] + [_P] * 6 + [ctypes.c_int32, _P, ctypes.c_int32]
+                            + [_P] * 7 + [ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -381,7 +399,7 @@ def falcon_bwd_chunked(phi_k, phi_q, v, beta, lam, dO, *, S0=None, k_prev=None, 
 
 
 # ---- around the recurrence: short convolution, group norm, selective scan,
-#      linear attention ------------------------------------------------------------
+#      linear attention, residual update --------------------------------------------
 #
 # Channels-last "rows" inputs ([B, T, width], or [B, width] for single tokens)
 # may be some of the columns of a wider contiguous projection; everything else
@@ -389,6 +407,7 @@ def falcon_bwd_chunked(phi_k, phi_q, v, beta, lam, dO, *, S0=None, k_prev=None, 
 # the inputs' device); what they allocate belongs to that stream.
 
 ACTIVATIONS = {"none": 0, "silu": 1, "elu1": 2}
+GATES = {"none": 0, "silu": 1, "sigmoid": 3}
 _LAYOUTS = ("rows", "heads")
 _F32 = (torch.float32,)
 
@@ -948,4 +967,164 @@ def falcon_linear_bwd(q, k, v, log_decay, dO, *, scale=1.0, S0=None, lengths=Non
         _check(load_library().falcon_linear_bwd(
             ctypes.byref(p), _ref(q), _ref(k), _ref(v), _ref(log_decay), _ref(S0), _ref(lengths), _ref(dO), _ref(dS_T),
             _ref(g["dq"]), _ref(g["dk"]), _ref(g["dv"]), _ref(g["dlog_decay"]), _ref(g["dS0"]), _ref(workspace), have, st))
+    return g
+
+
+class FalconSaved(NamedTuple):
+    """A block's output and gate in 8 bits: codes ``[B, T, C]`` int8 and, for every
+    32 channels, the exponent of their step, ``[B, T, ceil(C / 32)]`` uint8."""
+
+    y_codes: torch.Tensor
+    y_steps: torch.Tensor
+    gate_codes: Optional[torch.Tensor] = None
+    gate_steps: Optional[torch.Tensor] = None
+
+
+def _saved(saved, rows, gated, dev):
+    """Checks the tensors in 8 bits of [B, T, C] ``rows`` and returns their pointers."""
+    if not isinstance(saved, tuple) or len(saved) != 4:
+        raise TypeError(f"saved: expected a FalconSaved, got {type(saved).__name__}")
+    steps = rows[:2] + ((rows[2] + 31) // 32,)
+    for name, t, shape, dtype in zip(FalconSaved._fields, saved, (rows, steps) * 2, (torch.int8, torch.uint8) * 2):
+        if gated or not name.startswith("gate"):
+            _need(t, name, shape, dtype, dev)
+    return FalconSavedPointers(*(_ref(t) if gated or i < 2 else None for i, t in enumerate(saved)))
+
+
+def _residual_weights(C, dev, **weights):
+    for name, t in weights.items():
+        _need(t, name, (C,), torch.float32, dev, optional=True)
+
+
+def _groups(groups, C):
+    G = int(groups)
+    if G < 1 or C % G != 0:
+        raise ValueError(f"groups: {groups} does not divide {C} channels")
+    return G
+
+
+def _gate_activation(activation):
+    if activation not in GATES:
+        raise ValueError(f"unknown activation {activation!r}: expected one of {sorted(GATES)}")
+    return GATES[activation]
+
+
+def falcon_residual_fwd(y, h=None, *, gate=None, activation="silu", groups=1, post_norm=True, post_weight=None,
+                        alpha=None, pre_norm=True, pre_weight=None, eps=1e-6, lengths=None, h_out=None, n=None,
+                        save=False, saved=None, stream=None):
+    """From a block's output ``y [B, T, C]`` to the next block's input; returns
+    ``(h_out, n, saved)``.
+
+    ``h_out = h + alpha f(gate) z`` with ``z`` the groups of ``y`` over their root
+    mean squares, times ``post_weight`` (``post_norm`` false: ``y`` itself), and ``n``
+    the rows of ``h_out`` over theirs, times ``pre_weight`` (``pre_norm`` false:
+    None).  ``activation`` is "silu", "sigmoid" or "none"; weights and ``alpha`` are
+    ``[C]`` float32; ``h`` and ``h_out``, the stream, may be of another type than
+    ``y``, and ``h_out`` may be ``h``.  ``save`` (or a FalconSaved to fill) keeps
+    ``y`` and ``gate`` in 8 bits for the backward pass.  ``lengths`` (``[B]`` int32)
+    marks padded sequences: rows behind the end stay as they were, or zero where they
+    are allocated here.
+    """
+    act = _gate_activation(activation)
+    if not isinstance(y, torch.Tensor) or y.dim() != 3:
+        raise ValueError("y: expected a [B, T, C] tensor")
+    io, dev, rows = _io_dtype(y, "y"), y.device, tuple(y.shape)
+    B, T, C = rows
+    G = _groups(groups, C)
+    y_row = _row_step(y, "y", y.shape, io, dev)
+    gate_row = _row_step(gate, "gate", y.shape, io, dev) if gate is not None else C
+    kind = h if h is not None else h_out
+    stream_type = _io_dtype(kind, "h") if isinstance(kind, torch.Tensor) else io
+    _need(h, "h", rows, stream_type, dev, optional=True)
+    _need(h_out, "h_out", rows, stream_type, dev, optional=True)
+    _need(n, "n", rows, io, dev, optional=True)
+    if n is not None and not pre_norm:
+        raise ValueError("n: there is no pre_norm")
+    _residual_weights(C, dev, post_weight=post_weight, alpha=alpha, pre_weight=pre_weight)
+    _need(lengths, "lengths", (B,), torch.int32, dev, optional=True)
+    p = FalconResidualProblem(B, T, G, C // G, DTYPES[io], DTYPES[stream_type], act, int(bool(post_norm)),
+                              int(bool(pre_norm)), eps, y_row, gate_row)
+    with _on_stream(dev, stream) as st:
+        if h_out is None:
+            h_out = _new(rows, stream_type, dev, lengths)
+        if n is None and pre_norm:
+            n = _new(rows, io, dev, lengths)
+        if saved is None and save:
+            parts = 2 if gate is not None else 1
+            saved = FalconSaved(*(_new(shape, dtype, dev, lengths) for _ in range(parts)
+                                  for shape, dtype in ((rows, torch.int8), ((B, T, (C + 31) // 32), torch.uint8))))
+        at = None if saved is None else ctypes.byref(_saved(saved, rows, gate is not None, dev))
+        _check(load_library().falcon_residual_fwd(
+            ctypes.byref(p), _ref(y), _ref(gate), _ref(h), _ref(post_weight), _ref(alpha), _ref(pre_weight),
+            _ref(lengths), _ref(h_out), _ref(n), at, st))
+    return h_out, n, saved
+
+
+def falcon_residual_bwd_workspace_bytes(problem: FalconResidualProblem) -> int:
+    return int(load_library().falcon_residual_bwd_workspace_bytes(ctypes.byref(problem)))
+
+
+def falcon_residual_bwd(y, h_out, dh_out, dn=None, *, gate=None, saved=None, activation="silu", groups=1,
+                        post_norm=True, post_weight=None, alpha=None, pre_norm=True, pre_weight=None, eps=1e-6,
+                        lengths=None, added=True, grads=None, workspace=None, stream=None):
+    """Gradients of ``<dh_out, h_out> + <dn, n>``: a dict of float32 tensors dy, dgate
+    (None without a gate), dh (None unless ``added``: there was an ``h``), dalpha,
+    dpost_weight and dpre_weight (None where alpha or the weight is None); all but the
+    first two may still be asked for through ``grads``, the weights' where there is the
+    norm.  ``saved`` holds ``y`` and ``gate`` in 8 bits; both are None then.  ``h_out`` and ``dn`` belong to
+    ``pre_norm``; ``dh_out`` may be None (zero).  Rows behind the sequences' ends get
+    zero."""
+    act = _gate_activation(activation)
+    if saved is not None:
+        if y is not None or gate is not None:
+            raise ValueError("saved: y and gate are in it")
+        lead = saved[0] if isinstance(saved, tuple) and len(saved) == 4 else None
+    else:
+        lead = y
+    if not isinstance(lead, torch.Tensor) or lead.dim() != 3:
+        raise ValueError("saved: expected a FalconSaved of [B, T, C] codes" if saved is not None else "y: expected a [B, T, C] tensor")
+    dev, rows = lead.device, tuple(lead.shape)
+    B, T, C = rows
+    G = _groups(groups, C)
+    y_row = gate_row = C
+    io, at = torch.float32, None
+    if saved is not None:
+        gated = saved[2] is not None
+        at = _saved(saved, rows, gated, dev)
+    else:
+        io, gated = _io_dtype(y, "y"), gate is not None
+        y_row = _row_step(y, "y", y.shape, io, dev)
+        gate_row = _row_step(gate, "gate", y.shape, io, dev) if gated else C
+    stream_type = torch.float32
+    if pre_norm:
+        stream_type = _io_dtype(h_out, "h_out") if isinstance(h_out, torch.Tensor) else None
+        _need(h_out, "h_out", rows, stream_type, dev)
+        _expect(dn, "dn", rows, tuple(DTYPES), dev)
+    elif h_out is not None or dn is not None:
+        raise ValueError("h_out, dn: there is no pre_norm")
+    _expect(dh_out, "dh_out", rows, tuple(DTYPES), dev, optional=True)
+    _residual_weights(C, dev, post_weight=post_weight, alpha=alpha, pre_weight=pre_weight)
+    _need(lengths, "lengths", (B,), torch.int32, dev, optional=True)
+    shapes = {"dy": rows, "dgate": rows, "dh": rows, "dalpha": (C,), "dpost_weight": (C,), "dpre_weight": (C,)}
+    g = _grads(grads, shapes, dev)
+    for name, there in (("dgate", gated), ("dpost_weight", post_norm), ("dpre_weight", pre_norm)):
+        if g.get(name) is not None and not there:
+            raise ValueError(f"grads[{name!r}]: there is no {'gate' if name == 'dgate' else name[1:-7] + '_norm'}")
+    wanted = {"dy": True, "dgate": gated, "dh": added, "dalpha": alpha is not None,
+              "dpost_weight": post_norm and post_weight is not None, "dpre_weight": pre_norm and pre_weight is not None}
+    p = FalconResidualProblem(B, T, G, C // G, DTYPES[io], DTYPES[stream_type], act, int(bool(post_norm)),
+                              int(bool(pre_norm)), eps, y_row, gate_row)
+    need = falcon_residual_bwd_workspace_bytes(p)
+    _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
+    types = [DTYPES[t.dtype] if t is not None else 0 for t in (dh_out, dn)]
+    with _on_stream(dev, stream) as st:
+        for name, shape in shapes.items():
+            if g.get(name) is None:
+                g[name] = torch.empty(shape, dtype=torch.float32, device=dev) if wanted[name] else None
+        workspace, have = _workspace(workspace, need, dev)
+        _check(load_library().falcon_residual_bwd(
+            ctypes.byref(p), _ref(y), _ref(gate), None if at is None else ctypes.byref(at), _ref(h_out),
+            _ref(post_weight), _ref(alpha), _ref(pre_weight), _ref(lengths), _ref(dh_out), types[0], _ref(dn), types[1],
+            _ref(g["dy"]), _ref(g["dgate"]), _ref(g["dh"]), _ref(g["dalpha"]), _ref(g["dpost_weight"]),
+            _ref(g["dpre_weight"]), _ref(workspace), have, st))
     return g

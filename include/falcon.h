@@ -301,7 +301,9 @@ size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
  *                  it makes phi(k) and phi(q) in the [B, H, T, dk] layout that
  *                  falcon_fwd_* read, and norms the [B, H, T, dv] outputs;
  *   falcon_scan_*  the selective state space scan;
- *   falcon_linear_*  linear attention with a decay for each head.
+ *   falcon_linear_*  linear attention with a decay for each head;
+ *   falcon_residual_*  the residual update between two blocks: norm of the block's
+ *                  output, gate, scale, sum, norm for the next block.
  * Status codes, streams, the order of checks and launches and the absence of
  * allocation are those of the entry points above.  Also:
  *  - "Rows" tensors are channels last, [B, T, width].  Where a field *_row is
@@ -329,8 +331,10 @@ size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
 typedef enum {
   FALCON_ACT_NONE = 0,  /* f(p) = p                                   */
   FALCON_ACT_SILU = 1,  /* f(p) = p / (1 + exp(-p))                   */
-  FALCON_ACT_ELU1 = 2   /* f(p) = p + 1 for p > 0, exp(p) otherwise;
+  FALCON_ACT_ELU1 = 2,  /* f(p) = p + 1 for p > 0, exp(p) otherwise;
                            falcon_norm_* only                         */
+  FALCON_ACT_SIGMOID = 3 /* f(p) = 1 / (1 + exp(-p));
+                           falcon_residual_* only                     */
 } falcon_activation;
 
 /*
@@ -582,6 +586,80 @@ falcon_status falcon_linear_bwd(const falcon_linear_problem* p, const void* q, c
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 size_t falcon_linear_bwd_workspace_bytes(const falcon_linear_problem* p);
+
+/*
+ * falcon_residual_fwd -- from a block's output to the next block's input.  A token's
+ * C = G d channels are G groups (the heads) of d:
+ *
+ *     z     = post_weight y / sqrt( mean over the group(y^2) + eps ),  or y without post_norm
+ *     h_out = h + alpha f(gate) z                       (f(gate) = 1 without a gate)
+ *     n     = pre_weight h_out / sqrt( mean over the row(h_out^2) + eps ),  with pre_norm
+ *
+ * in float32, each result rounded once (n is made from h_out before its rounding).
+ * Without h and pre_norm it is the gated norm of the heads' outputs ahead of the output
+ * projection; without post_norm and gate, the plain pre-norm residual.  A group of zeros
+ * needs eps > 0 to stay finite.
+ *
+ *  y, gate    : [B, T, C] io dtype, rows of y_row and gate_row elements; gate may be NULL.
+ *  h          : [B, T, C] stream dtype, or NULL for zero.
+ *  post_weight, alpha, pre_weight : [C] float32, or NULL for one.
+ *  h_out      : [B, T, C] stream dtype; may alias h exactly.
+ *  n          : [B, T, C] io dtype; required with pre_norm, ignored without.
+ *  saved      : NULL, or where to leave y and gate in 8 bits for falcon_residual_bwd:
+ *               codes [B, T, C], steps [B, T, ceil(C / 32)].  Every 32 adjacent channels
+ *               (fewer at a row's end) share a step 2^(byte - 127), the smallest power of
+ *               two (from 2^-126 on) of which 127 reach their largest magnitude; a
+ *               value is code times step, the multiple nearest to it (ties to even).
+ *               Channels that are not all finite get byte 255 and come back as NaN.
+ *               The gate's arrays are required where there is a gate, ignored else.
+ * 1 <= C <= 8192.
+ */
+typedef struct {
+  int32_t B, T, G, d;
+  int32_t io_dtype;
+  int32_t stream_dtype;       /* of h and h_out: a falcon_dtype                  */
+  int32_t activation;         /* of the gate: FALCON_ACT_NONE, _SILU or _SIGMOID */
+  int32_t post_norm, pre_norm;
+  float eps;                  /* >= 0, finite */
+  int64_t y_row, gate_row;
+} falcon_residual_problem;
+
+typedef struct {
+  int8_t* y_codes;
+  uint8_t* y_steps;
+  int8_t* gate_codes;
+  uint8_t* gate_steps;
+} falcon_saved;
+
+falcon_status falcon_residual_fwd(const falcon_residual_problem* p, const void* y, const void* gate,
+                                  const void* h, const float* post_weight, const float* alpha,
+                                  const float* pre_weight, const int32_t* lengths, void* h_out,
+                                  void* n, const falcon_saved* saved, hipStream_t stream);
+
+/*
+ * falcon_residual_bwd -- gradients of <dh_out, h_out> + <dn, n>.
+ *  y, gate    : the forward's; NULL where `saved` holds them in 8 bits instead (a gate
+ *               where saved->gate_codes is not NULL).  y_row and gate_row are then ignored.
+ *  h_out      : the forward's, required with pre_norm.
+ *  dh_out     : [B, T, C] dh_out_dtype, or NULL for zero;  dn : [B, T, C] dn_dtype, required
+ *               with pre_norm, ignored without.
+ *  dy, dgate  : [B, T, C] float32; dgate is required where there is a gate, ignored else.
+ *  dh         : [B, T, C] float32, or NULL to skip; may alias a float32 dh_out exactly.
+ *  dalpha, dpost_weight, dpre_weight : [C] float32, or NULL to skip each (they may be asked
+ *               for where alpha or the weights are NULL, too; dpost_weight without
+ *               post_norm and dpre_weight without pre_norm are not written).
+ *  workspace  : at least falcon_residual_bwd_workspace_bytes(p) bytes, 16-byte aligned.
+ */
+falcon_status falcon_residual_bwd(const falcon_residual_problem* p, const void* y, const void* gate,
+                                  const falcon_saved* saved, const void* h_out,
+                                  const float* post_weight, const float* alpha,
+                                  const float* pre_weight, const int32_t* lengths,
+                                  const void* dh_out, int32_t dh_out_dtype, const void* dn,
+                                  int32_t dn_dtype, float* dy, float* dgate, float* dh,
+                                  float* dalpha, float* dpost_weight, float* dpre_weight,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t falcon_residual_bwd_workspace_bytes(const falcon_residual_problem* p);
 
 #ifdef __cplusplus
 }
