@@ -167,12 +167,19 @@ struct LinearSweep {
   int H, T, dv, tiles, chunks;   // chunks: of a tile
   int sf, sc;              // a state's element (f, c) lies at f sf + c sc
   float read, write;       // factors of what is read and of what is written
-  bool rev, bf16, out_bf16;
+  bool rev, bf16;
 };
-hipError_t launch_linear_sweep_16(const LinearSweep& s, hipStream_t st);
-hipError_t launch_linear_sweep_32(const LinearSweep& s, hipStream_t st);
-hipError_t launch_linear_sweep_64(const LinearSweep& s, hipStream_t st);
-hipError_t launch_linear_sweep_128(const LinearSweep& s, hipStream_t st);
+// What the tiles of one or two sweeps of the same sizes add to a state; the outputs of one;
+// the gradients' sweeps, dv's first.  By the width of the (first sweep's) keys.
+#define FALCON_LINEAR_OF(DK)                                                                                          \
+  hipError_t launch_linear_sums_##DK(const LinearSweep& s, const LinearSweep* second, hipStream_t st);                \
+  hipError_t launch_linear_outputs_##DK(const LinearSweep& s, hipStream_t st);                                        \
+  hipError_t launch_linear_gradients_##DK(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st);
+FALCON_LINEAR_OF(16)
+FALCON_LINEAR_OF(32)
+FALCON_LINEAR_OF(64)
+FALCON_LINEAR_OF(128)
+#undef FALCON_LINEAR_OF
 
 struct ResidualArgs {
   int B, T, G, d;

@@ -30,8 +30,10 @@ struct Tiles {
 
 Tiles cut(const LinearArgs& a) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
-  const int64_t want = std::max<int64_t>(1, (768 + heads - 1) / std::max<int64_t>(heads, 1));   // tiles of a head for three a CU
-  const int64_t chunks = std::max<int64_t>(2, (all + want - 1) / want);
+  // tiles of a head for three workgroups a CU, or for the two that wide heads leave room for
+  const int64_t all_tiles = a.dk * a.dv > 64 * 64 ? 512 : 768;
+  const int64_t want = std::max<int64_t>(1, (all_tiles + heads - 1) / std::max<int64_t>(heads, 1));
+  const int64_t chunks = std::max<int64_t>(1, (all + want - 1) / want);
   return {heads, int(chunks), int(std::max<int64_t>(1, (all + chunks - 1) / chunks))};
 }
 
@@ -39,7 +41,7 @@ Tiles cut(const LinearArgs& a) {
 // Slot of tile t holds what the tile adds; it gets the state that enters the tile.
 // Against time the tiles follow one another from the last to the first, and the state
 // that leaves the first goes to slot 0.
-constexpr int kAhead = 8;   // slots in flight
+constexpr int kAhead = 16;   // slots in flight
 
 struct Carry {
   float* slots;
@@ -47,65 +49,63 @@ struct Carry {
   int slot0;
   const float* start;      // may be null (zero)
   float* last;             // may be null
+  bool rev;
+};
+struct Carries {
+  Carry c[2];              // one or two of the same sizes
+  uint32_t blocks;         // of each
   const float* log_decay;
   const int32_t* lengths;
   int64_t heads;
   int H, T, tiles, chunks, size;   // size: elements of a state
-  bool rev;
 };
 
-__global__ __launch_bounds__(256) void carry_kernel(Carry c) {
-  const int64_t each = c.size / 4;
-  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= c.heads * each) return;
-  const int64_t bh = at / each;
-  const int64_t e = (at - bh * each) * 4;
-  const int b = int(bh / c.H), h = int(bh % c.H);
-  const int len = tokens_of(c.lengths, b, c.T), tokens = c.chunks * kChunk;
-  const float log2_a = c.log_decay[h] * kLog2e;
-  float4 s = make_float4(0, 0, 0, 0);
-  if (c.start) s = *reinterpret_cast<const float4*>(c.start + bh * c.size + e);
-  float* const slots = c.slots + (bh * c.slots_each + c.slot0) * c.size + e;
-  const int used = min((len + tokens - 1) / tokens, c.tiles);
+__global__ __launch_bounds__(256) void carry_kernel(Carries a) {
+  const uint32_t which = blockIdx.x >= a.blocks ? 1 : 0;
+  const Carry c = a.c[which];
+  const int64_t at = int64_t(blockIdx.x - which * a.blocks) * 256 + threadIdx.x;
+  const uint32_t bh = uint32_t(int64_t(blockIdx.x - which * a.blocks) * 256 / a.size);   // (256 divides the size)
+  const int e = int(at - int64_t(bh) * a.size);
+  const int b = int(bh / uint32_t(a.H)), h = int(bh % uint32_t(a.H));
+  const int len = tokens_of(a.lengths, b, a.T), tokens = a.chunks * kChunk;
+  const float log2_a = a.log_decay[h] * kLog2e;
+  float s = c.start ? c.start[at] : 0.0f;
+  float* const slots = c.slots + (bh * c.slots_each + c.slot0) * a.size + e;
+  const int used = min((len + tokens - 1) / tokens, a.tiles);
   const float whole = power(log2_a, tokens);
-  auto slot = [&](int t) { return reinterpret_cast<float4*>(slots + int64_t(t) * c.size); };
   for (int base = 0; base < used; base += kAhead) {
-    float4 add[kAhead];
+    float add[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int t = min(base + k, used - 1);
-      add[k] = *slot(c.rev ? used - 1 - t : t);
+      add[k] = slots[int64_t(c.rev ? used - 1 - t : t) * a.size];
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (base + k < used) {
         const int t = c.rev ? used - 1 - base - k : base + k;
-        *slot(t) = s;
-        const float across = t == used - 1 ? power(log2_a, len - t * tokens) : whole;
-        s.x = __builtin_fmaf(s.x, across, add[k].x);
-        s.y = __builtin_fmaf(s.y, across, add[k].y);
-        s.z = __builtin_fmaf(s.z, across, add[k].z);
-        s.w = __builtin_fmaf(s.w, across, add[k].w);
+        slots[int64_t(t) * a.size] = s;
+        s = __builtin_fmaf(s, t == used - 1 ? power(log2_a, len - t * tokens) : whole, add[k]);
       }
     }
   }
-  if (c.rev && c.slot0 > 0) *slot(-1) = s;
-  if (c.last) *reinterpret_cast<float4*>(c.last + bh * c.size + e) = s;
+  if (c.rev && c.slot0 > 0) slots[-int64_t(a.size)] = s;
+  if (c.last) c.last[at] = s;
 }
 
-hipError_t launch_carry(const Carry& c, hipStream_t st) {
-  carry_kernel<<<dim3(unsigned((c.heads * (c.size / 4) + 255) / 256)), dim3(256), 0, st>>>(c);
+hipError_t launch_carry(const LinearArgs& l, const Tiles& t, const Carry& c, const Carry* second, hipStream_t st) {
+  const int size = l.dk * l.dv;
+  const uint32_t blocks = uint32_t(t.heads * (size / 256));
+  carry_kernel<<<dim3(blocks * (second ? 2 : 1)), dim3(256), 0, st>>>(
+      {{c, second ? *second : c}, blocks, l.log_decay, l.lengths, t.heads, l.H, l.T, t.tiles, t.chunks, size});
   return hipGetLastError();
 }
 
-hipError_t launch_sweep(const LinearSweep& s, int dk, hipStream_t st) {
-  switch (dk) {
-    case 16: return launch_linear_sweep_16(s, st);
-    case 32: return launch_linear_sweep_32(s, st);
-    case 64: return launch_linear_sweep_64(s, st);
-    default: return launch_linear_sweep_128(s, st);
-  }
-}
+#define FALCON_BY_KEYS(what, dk, ...)                         \
+  ((dk) == 16   ? launch_linear_##what##_16(__VA_ARGS__)      \
+   : (dk) == 32 ? launch_linear_##what##_32(__VA_ARGS__)      \
+   : (dk) == 64 ? launch_linear_##what##_64(__VA_ARGS__)      \
+                : launch_linear_##what##_128(__VA_ARGS__))
 
 // What the sweeps of one call share.
 LinearSweep sweep_base(const LinearArgs& a, const Tiles& t) {
@@ -225,13 +225,22 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
   if (n > 0) {
     const float* s = a.S + (bh * a.tiles + tile) * a.size;
     const float* r = a.R + (bh * (a.tiles + 1) + tile) * a.size;
-    for (int e = threadIdx.x; e < a.size; e += 256) sum += double(s[e]) * r[e];
+    // (the size is a multiple of 256, of 1024 but for 16 x 16)
+#pragma unroll 4
+    for (int e = threadIdx.x * 4; e < a.size; e += 1024) {
+      float sv[4], rv[4];
+      load_vec<float, 4>(s + e, sv);
+      load_vec<float, 4>(r + e, rv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = __builtin_fma(double(sv[i]), double(rv[i]), sum);
+    }
     sum *= n;
     // d / 4 threads a token
     const int each = a.d / 4, part = threadIdx.x % each * 4;
     const int64_t at = b * a.d_at.b + h * a.d_at.h + part;
     const IO* q = static_cast<const IO*>(a.q) + b * a.q_at.b + h * a.q_at.h + part;
     const IO* k = static_cast<const IO*>(a.k) + b * a.k_at.b + h * a.k_at.h + part;
+#pragma unroll 4
     for (int j = threadIdx.x / each; j < n; j += 256 / each) {
       const int64_t t = first + j;
       float qv[4], kv[4], dqv[4], dkv[4];
@@ -241,17 +250,18 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
       load_vec<float, 4>(a.dk + at + t * a.d_at.t, dkv);
       double u = 0.0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u += double(kv[e]) * dkv[e] - double(qv[e]) * dqv[e];
+      for (int e = 0; e < 4; ++e) u = __builtin_fma(double(kv[e]), double(dkv[e]), __builtin_fma(-double(qv[e]), double(dqv[e]), u));
       sum += u * (n - 1 - j);
     }
   }
   sums[threadIdx.x] = sum;
   __syncthreads();
-  for (int half = 128; half > 0; half /= 2) {
-    if (int(threadIdx.x) < half) sums[threadIdx.x] += sums[threadIdx.x + half];
-    __syncthreads();
+  if (threadIdx.x < 64) {
+    sum = (sums[threadIdx.x] + sums[threadIdx.x + 64]) + (sums[threadIdx.x + 128] + sums[threadIdx.x + 192]);
+#pragma unroll
+    for (int m = 32; m > 0; m /= 2) sum += __shfl_xor(sum, m);
+    if (threadIdx.x == 0) a.parts[(int64_t(b) * a.tiles + tile) * a.H + h] = float(sum);
   }
-  if (threadIdx.x == 0) a.parts[(int64_t(b) * a.tiles + tile) * a.H + h] = float(sums[0]);
 }
 
 // ---- zeros behind the sequences' ends --------------------------------------------------------
@@ -306,10 +316,9 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
   if (t.tiles > 1) {
     s.slots = a.workspace;
     s.slots_each = t.tiles;
-    e = launch_sweep(s, a.dk, st);
+    e = FALCON_BY_KEYS(sums, a.dk, s, nullptr, st);
     if (e != hipSuccess) return e;
-    const Carry c{a.workspace, t.tiles, 0, a.S0, a.S_T, a.log_decay, a.lengths, t.heads, a.H, a.T, t.tiles, t.chunks, a.dk * a.dv, false};
-    e = launch_carry(c, st);
+    e = launch_carry(a, t, {a.workspace, t.tiles, 0, a.S0, a.S_T, false}, nullptr, st);
     if (e != hipSuccess) return e;
   } else {
     s.start = a.S0;
@@ -317,9 +326,8 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
   }
   s.q = a.q; s.q_at = a.q_at;
   s.out = a.o; s.out_at = a.o_at;
-  s.out_bf16 = a.bf16;
   s.read = a.scale;
-  return launch_sweep(s, a.dk, st);
+  return FALCON_BY_KEYS(outputs, a.dk, s, st);
 }
 
 hipError_t launch_linear_step(const LinearArgs& a, hipStream_t st) { return a.bf16 ? step_of<bf16_t>(a, st) : step_of<float>(a, st); }
@@ -349,7 +357,6 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   s.dv = a.dv;
   s.sf = a.dv; s.sc = 1;
   s.slots = S; s.slots_each = t.tiles;
-  FALCON_TRY(launch_sweep(s, a.dk, st));
   LinearSweep r = sweep_base(a, t);
   r.k = a.q; r.v = a.dO;
   r.k_at = a.q_at; r.v_at = a.o_at;
@@ -358,30 +365,31 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   r.slots = R; r.slots_each = t.tiles + 1; r.slot0 = 1;
   r.rev = true;
   r.write = a.scale;
-  FALCON_TRY(launch_sweep(r, a.dk, st));
-  FALCON_TRY(launch_carry({S, t.tiles, 0, a.S0, nullptr, a.log_decay, a.lengths, t.heads, a.H, a.T, t.tiles, t.chunks, size, false}, st));
-  FALCON_TRY(launch_carry({R, t.tiles + 1, 1, a.dS_T, a.dS0, a.log_decay, a.lengths, t.heads, a.H, a.T, t.tiles, t.chunks, size, true}, st));
+  FALCON_TRY(FALCON_BY_KEYS(sums, a.dk, s, &r, st));
+  const Carry back{R, t.tiles + 1, 1, a.dS_T, a.dS0, true};
+  FALCON_TRY(launch_carry(a, t, {S, t.tiles, 0, a.S0, nullptr, false}, &back, st));
   // dv = (k, q, dO) against time
-  r.q = a.k; r.q_at = a.k_at;
-  r.out = a.dv_out; r.out_at = a.dv_at;
-  FALCON_TRY(launch_sweep(r, a.dk, st));
+  LinearSweep dv = r;
+  dv.q = a.k; dv.q_at = a.k_at;
+  dv.out = a.dv_out; dv.out_at = a.dv_at;
   // dk = (v, dO, q) against time, from the transposed adjoint
-  r.q = a.v; r.q_at = a.v_at;
-  r.k = a.dO; r.k_at = a.o_at;
-  r.v = a.q; r.v_at = a.q_at;
-  r.dv = a.dk;
-  r.sf = 1; r.sc = a.dv;
-  r.out = a.dk_out; r.out_at = a.dqk_at;
-  FALCON_TRY(launch_sweep(r, a.dv, st));
+  LinearSweep dk = r;
+  dk.q = a.v; dk.q_at = a.v_at;
+  dk.k = a.dO; dk.k_at = a.o_at;
+  dk.v = a.q; dk.v_at = a.q_at;
+  dk.dv = a.dk;
+  dk.sf = 1; dk.sc = a.dv;
+  dk.out = a.dk_out; dk.out_at = a.dqk_at;
   // dq = (dO, v, k), from the transposed state
-  s.q = a.dO; s.q_at = a.o_at;
-  s.k = a.v; s.k_at = a.v_at;
-  s.v = a.k; s.v_at = a.k_at;
-  s.dv = a.dk;
-  s.sf = 1; s.sc = a.dv;
-  s.read = a.scale;
-  s.out = a.dq; s.out_at = a.dqk_at;
-  FALCON_TRY(launch_sweep(s, a.dv, st));
+  LinearSweep dq = s;
+  dq.q = a.dO; dq.q_at = a.o_at;
+  dq.k = a.v; dq.k_at = a.v_at;
+  dq.v = a.k; dq.v_at = a.k_at;
+  dq.dv = a.dk;
+  dq.sf = 1; dq.sc = a.dv;
+  dq.read = a.scale;
+  dq.out = a.dq; dq.out_at = a.dqk_at;
+  FALCON_TRY(FALCON_BY_KEYS(gradients, a.dk, dv, dk, dq, st));
   if (a.lengths) {
     tails_kernel<<<dim3(unsigned(t.heads)), dim3(256), 0, st>>>({a.dq, a.dqk_at, a.dk}, {a.dk_out, a.dqk_at, a.dk}, {a.dv_out, a.dv_at, a.dv},
                                                                 a.lengths, a.H, a.T);

@@ -11,7 +11,9 @@ namespace {
 using namespace falcon;
 
 // Most heads of one call (B H): every grid then fits its 32 bits.
-constexpr int64_t kMaxHeads = int64_t(1) << 22;
+constexpr int64_t kMaxHeads = int64_t(1) << 21;
+// Longest row: offsets within a chunk then fit 32 bits.
+constexpr int64_t kMaxRow = int64_t(1) << 22;
 
 bool width_ok(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
@@ -29,6 +31,8 @@ falcon_status check_linear(const falcon_linear_problem* p, bool step, LinearArgs
   if (heads > kMaxHeads || rows > kMaxTokens || elems(heads, int64_t(T) + 2 * p->dk, 128) < 0) return FALCON_ERR_SHAPE;
   const int64_t dk = int64_t(p->H) * p->dk, dv = int64_t(p->H) * p->dv;
   const bool qk_heads = !step && p->qk_heads, v_heads = !step && p->v_heads, o_heads = !step && p->o_heads;
+  if ((!qk_heads && (p->q_row > kMaxRow || p->k_row > kMaxRow)) || (!v_heads && p->v_row > kMaxRow) || (!o_heads && dv > kMaxRow))
+    return FALCON_ERR_SHAPE;
   if (!qk_heads && (!rows_ok(rows, p->q_row, dk) || !rows_ok(rows, p->k_row, dk))) return FALCON_ERR_SHAPE;
   if (!v_heads && !rows_ok(rows, p->v_row, dv)) return FALCON_ERR_SHAPE;
   if (!dtype_ok(p->io_dtype)) return FALCON_ERR_DTYPE;

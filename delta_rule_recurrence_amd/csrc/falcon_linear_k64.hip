@@ -3,6 +3,12 @@
 
 namespace falcon {
 
-hipError_t launch_linear_sweep_64(const LinearSweep& s, hipStream_t st) { return linear::sweep_of<64>(s, st); }
+hipError_t launch_linear_sums_64(const LinearSweep& s, const LinearSweep* second, hipStream_t st) {
+  return linear::sums_of<64>(s, second, st);
+}
+hipError_t launch_linear_outputs_64(const LinearSweep& s, hipStream_t st) { return linear::outputs_of<64>(s, st); }
+hipError_t launch_linear_gradients_64(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st) {
+  return linear::gradients_of<64>(dv, dk, dq, st);
+}
 
 }  // namespace falcon

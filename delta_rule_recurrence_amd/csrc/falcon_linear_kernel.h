@@ -16,13 +16,14 @@
 // so that the three gradients are sweeps of the same kernel: dq = (dO, v, k)
 // forward, dk = (v, dO, q) and dv = (k, q, dO) against time.
 //
-// Wave w works on the 16 tokens of row block w % 4 and, with eight waves, on every
-// second block of 16 output columns.  Its scores come out of the matrix unit
-// transposed (keys by queries), which is what the next product takes as its
-// second operand, so they never leave the registers; keys and values lie in LDS
-// as they came and are turned on the way out (transposing reads for bfloat16).
-// Wave w owns columns w, w + WAVES, ... of 16 of the state, in float32
-// registers, and leaves it in LDS as operand fragments for all waves.
+// Wave w owns columns w, w + waves, ... of 16 of the values: the state's, in float32
+// registers that are an operand of the read as they lie, and the outputs' of all 64
+// tokens.  Narrow values leave waves over, which share the tokens of a column.  The
+// scores of 16 tokens are made by one wave each and pass through LDS, as do the
+// queries, both as operand fragments; they come out of the matrix unit transposed (keys
+// by queries), which is what the next product takes as its second operand.  Keys and
+// values lie in LDS as they came and are turned on the way out (transposing reads for
+// bfloat16).  The rows of the next chunk are on their way while one is worked on.
 //
 // bfloat16 inputs enter the products as they are.  What is float32 (decayed
 // scores, states, decayed values) enters as a sum of bfloat16 terms, which keep 8
@@ -72,19 +73,26 @@ struct Operands<float, TERMS> {
   using Split = f32x8;
 };
 
+// Two floats to the nearest bfloat16s, and what is lost.
+__device__ __forceinline__ uint32_t split2(float& x, float& y) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const uint32_t t = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  x -= __uint_as_float(t << 16);
+  y -= __uint_as_float(t & 0xffff0000u);
+  return t;
+}
 template <int N>
 __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Terms<N>& out) {
+  float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    bf16x8 t;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      t[e] = static_cast<__bf16>(lo[e]);
-      t[e + 4] = static_cast<__bf16>(hi[e]);
-      lo[e] -= static_cast<float>(t[e]);
-      hi[e] -= static_cast<float>(t[e + 4]);
-    }
-    out.t[n] = t;
+    uint4 t;
+    t.x = split2(v[0], v[1]);
+    t.y = split2(v[2], v[3]);
+    t.z = split2(v[4], v[5]);
+    t.w = split2(v[6], v[7]);
+    out.t[n] = __builtin_bit_cast(bf16x8, t);
   }
 }
 __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, f32x8& out) { out = {lo, hi}; }
@@ -166,6 +174,29 @@ __device__ __forceinline__ f32x4 widened(bf16x8 v, int half) {
 }
 __device__ __forceinline__ f32x4 widened(const f32x8& v, int half) { return half ? v.hi : v.lo; }
 
+// Operand fragments in LDS, 64 lanes' parts of 16 bytes next to each other.
+__device__ __forceinline__ void put(char* lds, int frag, int l, bf16x8 v) { reinterpret_cast<bf16x8*>(lds)[frag * 64 + l] = v; }
+__device__ __forceinline__ void get(const char* lds, int frag, int l, bf16x8& v) { v = reinterpret_cast<const bf16x8*>(lds)[frag * 64 + l]; }
+template <int N>
+__device__ __forceinline__ void put(char* lds, int frag, int l, const Terms<N>& v) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) put(lds, frag * N + n, l, v.t[n]);
+}
+template <int N>
+__device__ __forceinline__ void get(const char* lds, int frag, int l, Terms<N>& v) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) get(lds, frag * N + n, l, v.t[n]);
+}
+__device__ __forceinline__ void put(char* lds, int frag, int l, const f32x8& v) {
+  f32x4* p = reinterpret_cast<f32x4*>(lds) + frag * 128 + l;
+  p[0] = v.lo;
+  p[64] = v.hi;
+}
+__device__ __forceinline__ void get(const char* lds, int frag, int l, f32x8& v) {
+  const f32x4* p = reinterpret_cast<const f32x4*>(lds) + frag * 128 + l;
+  v = {p[0], p[64]};
+}
+
 // A chunk's rows on the way from memory to LDS, 16 bytes a thread and access.
 template <typename IO, int D, int THREADS>
 struct Rows {
@@ -173,23 +204,25 @@ struct Rows {
   static constexpr int kSegs = D / kEach;                    // accesses of a row
   static constexpr int kAll = kChunk * kSegs;
   static constexpr int kMine = (kAll + THREADS - 1) / THREADS;
+  static_assert(THREADS % kSegs == 0);
   uint4 r[kMine];
 
   // Rows behind the chunk's n tokens are not read: their threads take the last one.
-  __device__ __forceinline__ void fetch(const IO* first, int64_t t_step, int n, int tid) {
+  // (Offsets within a chunk fit 32 bits: rows have at most 2^22 elements.)
+  __device__ __forceinline__ void fetch(const IO* first, int t_step, int n, int tid) {
+    const char* const p = reinterpret_cast<const char*>(first);
+    const uint32_t seg = uint32_t(tid % kSegs) * 16;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      const int piece = tid + i * THREADS;
-      const int row = min(piece / kSegs, n - 1), seg = piece % kSegs;
-      r[i] = *reinterpret_cast<const uint4*>(first + row * t_step + seg * kEach);
+      const int row = min(tid / kSegs + i * (THREADS / kSegs), n - 1);
+      r[i] = *reinterpret_cast<const uint4*>(p + (uint32_t(row) * uint32_t(t_step) * uint32_t(sizeof(IO)) + seg));
     }
   }
   __device__ __forceinline__ void store(IO* rows, int n, int tid) const {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      const int piece = tid + i * THREADS;
-      const int row = piece / kSegs, seg = piece % kSegs;
-      if (kAll % THREADS == 0 || piece < kAll)
+      const int row = tid / kSegs + i * (THREADS / kSegs), seg = tid % kSegs;
+      if (kAll % THREADS == 0 || row < kChunk)
         *reinterpret_cast<uint4*>(rows + row * Stage<IO, D>::kPitch + seg * kEach) = row < n ? r[i] : make_uint4(0, 0, 0, 0);
     }
   }
@@ -200,46 +233,61 @@ __device__ __forceinline__ float power(float log2_a, int n) {
   return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(log2_a * float(n));
 }
 
-template <int DV>
+// Waves of a workgroup: eight where float32 operands of 128 columns would not fit the
+// registers of four.
+template <typename IO, int DK, int DV>
 constexpr int waves() {
-  // eight where the state of 128 columns would not fit a wave's registers next to the rest
-  return DV >= 128 ? 8 : 4;
+  return sizeof(IO) == 4 && (DK >= 128 || DV >= 128) ? 8 : 4;
 }
-// LDS: keys, values and, for outputs, the state as fragments.
-template <typename IO, int DK, int DV, int TERMS, bool OUT>
+// Waves of a SIMD that the registers are to leave room for: as many as LDS does.
+template <int DK, int DV>
+constexpr int waves_simd() {
+  return 2;
+}
+// LDS: keys, values and, for outputs, queries and scores as fragments.
+template <typename IO, typename O, int DK, int DV, bool OUT>
 constexpr int lds_bytes() {
-  const int frags = sizeof(IO) == 2 ? TERMS * 16 : 32;
-  return Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes + (OUT ? (DV / 16) * (Stage<IO, DK>::kWidth / 32) * 64 * frags : 0);
+  const int terms = sizeof(O) == 2 ? 2 : 3;
+  const int scores = 8 * 64 * (sizeof(IO) == 2 ? terms * 16 : 32);
+  return Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes + (OUT ? kChunk * Stage<IO, DK>::kWidth * int(sizeof(IO)) + scores : 0);
 }
 
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void store4(bf16_t* p, f32x4 v) { frag::store_half(reinterpret_cast<uint16_t*>(p), v); }
 
-// OUT false: only what the tile's chunks add to a state, from zero, into the tile's slot.
-template <typename IO, typename O, int DK, int DV, bool OUT>
-__global__ __launch_bounds__(64 * waves<DV>()) void sweep_kernel(LinearSweep s) {
+// The tile `block` of a sweep.  OUT false: only what the tile's chunks add to a state,
+// from zero, into the tile's slot.  WRITTEN: terms of what is written into the state, two
+// where only outputs in bfloat16 come of it.
+template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN>
+__device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char* lds) {
   constexpr int kTerms = sizeof(O) == 2 ? 2 : 3;
-  constexpr int kWaves = waves<DV>(), kThreads = 64 * kWaves, kHalves = kWaves / 4;
+  constexpr int kWaves = waves<IO, DK, DV>(), kThreads = 64 * kWaves;
   constexpr int kB = Stage<IO, DK>::kWidth / 32;           // 32-wide blocks of the key axis
   constexpr int kCols = DV / 16;                           // 16-wide blocks of the value axis
-  constexpr int kOwn = (kCols + kWaves - 1) / kWaves;      // of these, a wave's part of the state
+  constexpr int kOwn = kCols >= kWaves ? kCols / kWaves : 1;   // of these, a wave's
+  constexpr int kShare = kCols >= kWaves ? 1 : kWaves / kCols; // waves that share a block of columns
+  constexpr int kRows = kShare >= 4 ? 1 : 4 / kShare;      // blocks of 16 tokens whose outputs a wave makes
   constexpr int kPk = Stage<IO, DK>::kPitch, kPv = Stage<IO, DV>::kPitch;
   using Ops = Operands<IO, kTerms>;
   using Exact = typename Ops::Exact;
   using Split = typename Ops::Split;
-  using Written = typename Operands<IO, 3>::Split;
 
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   IO* const ks = reinterpret_cast<IO*>(lds);
   IO* const vs = reinterpret_cast<IO*>(lds + Stage<IO, DK>::kBytes);
-  Split* const ss = reinterpret_cast<Split*>(lds + Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes);
+  char* const qs = lds + Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes;   // [4][kB] fragments
+  char* const ps = qs + kChunk * Stage<IO, DK>::kWidth * int(sizeof(IO)); // [4][2] fragments
 
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, c16 = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rw = w & 3, half = w >> 2;
-  const int64_t bh = blockIdx.x / s.tiles;
-  const int tile = int(blockIdx.x % s.tiles);
-  const int b = int(bh / s.H), h = int(bh % s.H);
+  const int rw = w & 3;                                    // the block of tokens whose scores this wave makes
+  const int share = kShare > 1 ? w / kCols : 0;
+  auto column = [&](int j) { return kShare > 1 ? w % kCols : w + j * kWaves; };
+  auto tokens = [&](int x) { return share + x * kShare; };  // block x of this wave's outputs
+  const bool makes = kShare <= 4 || share < 4;
+
+  const int64_t bh = block / uint32_t(s.tiles);
+  const int tile = int(block % uint32_t(s.tiles));
+  const int b = int(uint32_t(bh) / uint32_t(s.H)), h = int(uint32_t(bh) % uint32_t(s.H));
   const int len = tokens_of(s.lengths, b, s.T);
   const int first = tile * s.chunks * kChunk;
   const int chunks = min((len - first + kChunk - 1) / kChunk, s.chunks);
@@ -249,7 +297,39 @@ __global__ __launch_bounds__(64 * waves<DV>()) void sweep_kernel(LinearSweep s) 
   const IO* const V = static_cast<const IO*>(s.v) + b * s.v_at.b + h * s.v_at.h + first * s.v_at.t;
   const IO* const Q = OUT ? static_cast<const IO*>(s.q) + b * s.q_at.b + h * s.q_at.h + first * s.q_at.t : nullptr;
   O* const out = OUT ? static_cast<O*>(s.out) + b * s.out_at.b + h * s.out_at.h + first * s.out_at.t : nullptr;
+  const int k_step = int(s.k_at.t), v_step = int(s.v_at.t), q_step = int(s.q_at.t), out_step = int(s.out_at.t);
   float* const slot = s.slots ? s.slots + (bh * s.slots_each + s.slot0 + tile) * (DK * DV) : nullptr;
+
+  Rows<IO, DK, kThreads> kr;
+  Rows<IO, DV, kThreads> vr;
+  Exact qr[OUT ? kB : 1];
+  auto chunk_at = [&](int step) { return s.rev ? chunks - 1 - step : step; };
+  auto tokens_in = [&](int c) { return min(len - first - c * kChunk, kChunk); };
+  auto fetch = [&](int c) {
+    const int n = tokens_in(c);
+    kr.fetch(K + int64_t(c) * kChunk * k_step, k_step, n, tid);
+    vr.fetch(V + int64_t(c) * kChunk * v_step, v_step, n, tid);
+    if constexpr (OUT) {
+      if (w < 4) {
+        // rows of queries as fragments: columns 32 bb + 8 g .. + 7 of token 16 rw + c16
+        const bool there = DK >= 32 || g < 2;
+        const char* p = reinterpret_cast<const char*>(Q + int64_t(c) * kChunk * q_step);
+        const uint32_t row = uint32_t(min(16 * rw + c16, n - 1)) * uint32_t(q_step);
+#pragma unroll
+        for (int bb = 0; bb < kB; ++bb) {
+          const uint32_t at = (row + 32 * bb + (there ? 8 * g : 0)) * uint32_t(sizeof(IO));
+          if constexpr (sizeof(IO) == 2) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + at);
+            qr[bb] = __builtin_bit_cast(bf16x8, there ? v : make_uint4(0, 0, 0, 0));
+          } else {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(p + at), hi = *reinterpret_cast<const f32x4*>(p + at + 16);
+            qr[bb] = {there ? lo : frag::zero4(), there ? hi : frag::zero4()};
+          }
+        }
+      }
+    }
+  };
+  if (chunks > 0) fetch(chunk_at(0));
 
   // A state's element (f, c) at f sf + c sc.  Rows 32 b + 8 g + 4 t + r of column
   // 16 cb + c16 lie in S[.][b][t][r]: two tiles stacked are eight neighbours of the
@@ -263,22 +343,23 @@ __global__ __launch_bounds__(64 * waves<DV>()) void sweep_kernel(LinearSweep s) 
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         S[j][bb][t] = frag::zero4();
-        const int f = 32 * bb + 8 * g + 4 * t, cb = w + j * kWaves;
-        if (OUT && from && cb < kCols && f < DK)
+        const int f = 32 * bb + 8 * g + 4 * t;
+        if (OUT && from && f < DK)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[j][bb][t][r] = from[(f + r) * s.sf + (16 * cb + c16) * s.sc];
+          for (int r = 0; r < 4; ++r) S[j][bb][t][r] = from[(f + r) * s.sf + (16 * column(j) + c16) * s.sc];
       }
   auto keep = [&](float* to) {
+    if (share > 0) return;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j)
 #pragma unroll
       for (int bb = 0; bb < kB; ++bb)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const int f = 32 * bb + 8 * g + 4 * t, cb = w + j * kWaves;
-          if (cb < kCols && f < DK)
+          const int f = 32 * bb + 8 * g + 4 * t;
+          if (f < DK)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) to[(f + r) * s.sf + (16 * cb + c16) * s.sc] = S[j][bb][t][r];
+            for (int r = 0; r < 4; ++r) to[(f + r) * s.sf + (16 * column(j) + c16) * s.sc] = S[j][bb][t][r];
         }
   };
   if (chunks <= 0) {   // nothing of the sequence is left for this tile
@@ -287,39 +368,31 @@ __global__ __launch_bounds__(64 * waves<DV>()) void sweep_kernel(LinearSweep s) 
     }
     return;
   }
-  // The state as the first operand S^T of the read, for every wave.
-  auto publish = [&]() {
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j)
-#pragma unroll
-      for (int bb = 0; bb < kB; ++bb) {
-        const int cb = w + j * kWaves;
-        if (cb < kCols) {
-          Split t;
-          split(S[j][bb][0], S[j][bb][1], t);
-          ss[(cb * kB + bb) * 64 + l] = t;
-        }
-      }
-  };
   if constexpr (DK < 32) {
     for (int i = tid; i < kChunk * kPk; i += kThreads) ks[i] = IO{};
     __syncthreads();
   }
   // Decays between this lane's query token i = 16 rw + c16 and the keys of its score
-  // rows, 16 sb + 4 g + r; of the entering state at token i; of this lane's tokens
-  // 32 m + 16 u + 4 g + r at the chunk's end (a whole chunk's).
-  f32x4 mask[OUT ? 4 : 1];
-  const int i = 16 * rw + c16;
+  // rows, 16 sb + 4 g + r, of the pairs m of 16 keys that are this wave's.
+  constexpr int kPairs = kWaves == 8 ? 1 : 2;
+  auto pair = [&](int x) { return kWaves == 8 ? w >> 2 : x; };
+  f32x4 mask[OUT ? kPairs : 1][2];
   if constexpr (OUT) {
+    const int i = 16 * rw + c16;
 #pragma unroll
-    for (int sb = 0; sb < 4; ++sb)
+    for (int x = 0; x < kPairs; ++x)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int gap = s.rev ? 16 * sb + 4 * g + r - i : i - (16 * sb + 4 * g + r);
-        mask[sb][r] = gap >= 0 ? power(e, max(gap, 0)) * s.write : 0.0f;
-      }
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int key = 32 * pair(x) + 16 * u + 4 * g + r, gap = s.rev ? key - i : i - key;
+          mask[x][u][r] = gap >= 0 ? power(e, max(gap, 0)) * s.write : 0.0f;
+        }
   }
+  // Decays of this lane's tokens 32 m + 16 u + 4 g + r up to the chunk's end, and of the
+  // entering state at the tokens of its outputs.
   f32x4 to_end[2][2];
+  float into[OUT ? kRows : 1];
   auto ends = [&](int n) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -330,103 +403,132 @@ __global__ __launch_bounds__(64 * waves<DV>()) void sweep_kernel(LinearSweep s) 
           const int t = 32 * m + 16 * u + 4 * g + r;
           to_end[m][u][r] = power(e, s.rev ? min(t + 1, n) : max(n - 1 - t, 0)) * s.write;
         }
+    if constexpr (OUT) {
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        const int i = 16 * tokens(x) + c16;
+        into[x] = power(e, s.rev ? max(n - 1 - i, 0) : i + 1);
+      }
+    }
   };
   ends(kChunk);
+  const float whole = power(e, kChunk);
 
-  Rows<IO, DK, kThreads> kr;
-  Rows<IO, DV, kThreads> vr;
-  auto chunk_at = [&](int step) { return s.rev ? chunks - 1 - step : step; };
-  auto tokens_in = [&](int c) { return min(len - first - c * kChunk, kChunk); };
-  {
-    const int c = chunk_at(0), n = tokens_in(c);
-    kr.fetch(K + int64_t(c) * kChunk * s.k_at.t, s.k_at.t, n, tid);
-    vr.fetch(V + int64_t(c) * kChunk * s.v_at.t, s.v_at.t, n, tid);
-  }
   for (int step = 0; step < chunks; ++step) {
     const int c = chunk_at(step), n = tokens_in(c);
     const bool more = step + 1 < chunks;
-    if constexpr (OUT) publish();
     kr.store(ks, n, tid);
     vr.store(vs, n, tid);
-    Exact qf[kB];
     if constexpr (OUT) {
-      const IO* q = Q + (int64_t(c) * kChunk + min(i, n - 1)) * s.q_at.t;
+      if (w < 4) {
 #pragma unroll
-      for (int bb = 0; bb < kB; ++bb) {
-        const bool there = DK >= 32 || g < 2;
-        const IO* p = q + 32 * bb + (there ? 8 * g : 0);
-        if constexpr (sizeof(IO) == 2) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p);
-          qf[bb] = __builtin_bit_cast(bf16x8, there ? v : make_uint4(0, 0, 0, 0));
-        } else {
-          const f32x4* p4 = reinterpret_cast<const f32x4*>(p);
-          qf[bb] = {there ? p4[0] : frag::zero4(), there ? p4[1] : frag::zero4()};
-        }
+        for (int bb = 0; bb < kB; ++bb) put(qs, rw * kB + bb, l, qr[bb]);
       }
     }
+    if (n < kChunk) ends(n);
     __syncthreads();
-    if (more) {
-      const int next = chunk_at(step + 1), nn = tokens_in(next);
-      kr.fetch(K + int64_t(next) * kChunk * s.k_at.t, s.k_at.t, nn, tid);
-      vr.fetch(V + int64_t(next) * kChunk * s.v_at.t, s.v_at.t, nn, tid);
-    }
+    if (more) fetch(chunk_at(step + 1));
+    Exact vf[kOwn][2];
+    f32x4 o[OUT ? kRows : 1][kOwn];
     if constexpr (OUT) {
       // scores, keys by queries, decayed
-      f32x4 p[4];
+      Exact qf[kB];
 #pragma unroll
-      for (int sb = 0; sb < 4; ++sb) {
-        p[sb] = frag::zero4();
-        if (s.rev ? sb >= rw : sb <= rw) {
+      for (int bb = 0; bb < kB; ++bb) get(qs, rw * kB + bb, l, qf[bb]);
 #pragma unroll
-          for (int bb = 0; bb < kB; ++bb) p[sb] = mma(row_frag<kPk>(ks, 16 * sb + c16, bb, g), qf[bb], p[sb]);
-          // (a product with the mask's zero would keep what is not finite)
+      for (int x = 0; x < kPairs; ++x) {
+        const int m = pair(x);
+        if (!(s.rev ? m == 1 || rw < 2 : m == 0 || rw >= 2)) continue;   // all behind (before) these tokens
+        f32x4 p[2];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[sb][r] = mask[sb][r] != 0.0f ? p[sb][r] * mask[sb][r] : 0.0f;
+        for (int u = 0; u < 2; ++u) {
+          p[u] = frag::zero4();
+#pragma unroll
+          for (int bb = 0; bb < kB; ++bb) p[u] = mma(row_frag<kPk>(ks, 32 * m + 16 * u + c16, bb, g), qf[bb], p[u]);
+          // (a product with the mask's zero would keep what is not finite; the comparisons
+          // made ahead of the loop would fill the scalar registers)
+          asm volatile("" : "+v"(mask[x][u]));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[u][r] = mask[x][u][r] != 0.0f ? p[u][r] * mask[x][u][r] : 0.0f;
+        }
+        Split pf;
+        split(p[0], p[1], pf);
+        put(ps, rw * 2 + m, l, pf);
+      }
+      // what the entering state gives
+#pragma unroll
+      for (int x = 0; x < kRows; ++x)
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) o[x][j] = frag::zero4();
+      if (makes) {
+#pragma unroll
+        for (int bb = 0; bb < kB; ++bb) {
+          Split sf[kOwn];
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) split(S[j][bb][0], S[j][bb][1], sf[j]);
+#pragma unroll
+          for (int x = 0; x < kRows; ++x) {
+            Exact q;
+            get(qs, tokens(x) * kB + bb, l, q);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) o[x][j] = mma(sf[j], q, o[x][j]);
+          }
         }
       }
-      Split pf[2];
-      split(p[0], p[1], pf[0]);
-      split(p[2], p[3], pf[1]);
-      const float into = power(e, s.rev ? max(n - 1 - i, 0) : i + 1);
-      const bool low = s.rev ? rw < 2 : true, high = s.rev ? true : rw >= 2;
+    }
 #pragma unroll
-      for (int j = 0; j < (kCols + kHalves - 1) / kHalves; ++j) {
-        const int cb = j * kHalves + half;
-        f32x4 o = frag::zero4();
+    for (int j = 0; j < kOwn; ++j)
 #pragma unroll
-        for (int bb = 0; bb < kB; ++bb) o = mma(ss[(cb * kB + bb) * 64 + l], qf[bb], o);
-        o = o * into;
-        if (low) o = mma(turned_frag<kPv>(vs, 0, 16 * cb, 4, g, c16), pf[0], o);
-        if (high) o = mma(turned_frag<kPv>(vs, 1, 16 * cb, 4, g, c16), pf[1], o);
-        if (i < n) store4(out + (int64_t(c) * kChunk + i) * s.out_at.t + 16 * cb + 4 * g, o * s.read);
+      for (int m = 0; m < 2; ++m) vf[j][m] = turned_frag<kPv>(vs, m, 16 * column(j), 4, g, c16);
+    if constexpr (OUT) {
+      __syncthreads();
+      if (makes) {
+        char* const to = reinterpret_cast<char*>(out + int64_t(c) * kChunk * out_step);
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+          const int rb = tokens(x), i = 16 * rb + c16;
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) o[x][j] = o[x][j] * into[x];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (!(s.rev ? m == 1 || rb < 2 : m == 0 || rb >= 2)) continue;
+            Split pf;
+            get(ps, rb * 2 + m, l, pf);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) o[x][j] = mma(vf[j][m], pf, o[x][j]);
+          }
+          if (i < n) {
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+              store4(reinterpret_cast<O*>(to + (uint32_t(i) * uint32_t(out_step) + 16 * column(j) + 4 * g) * uint32_t(sizeof(O))), o[x][j] * s.read);
+          }
+        }
       }
     }
     if (!OUT || more || s.last) {
-      if (n < kChunk) ends(n);
-      const float across = power(e, n);
+      const float across = n < kChunk ? power(e, n) : whole;
+      typename Operands<IO, WRITTEN>::Split wf[kOwn][2];
 #pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        const int cb = w + j * kWaves;
-        if (cb < kCols) {
-          Written vf[2];
+      for (int j = 0; j < kOwn; ++j)
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const Exact v = turned_frag<kPv>(vs, m, 16 * cb, 4, g, c16);
-            split(widened(v, 0) * to_end[m][0], widened(v, 1) * to_end[m][1], vf[m]);
+        for (int m = 0; m < 2; ++m) split(widened(vf[j][m], 0) * to_end[m][0], widened(vf[j][m], 1) * to_end[m][1], wf[j][m]);
+#pragma unroll
+      for (int bb = 0; bb < kB; ++bb)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          Exact kf[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) kf[m] = turned_frag<kPk>(ks, m, 32 * bb + 4 * t, 8, g, c16);
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            f32x4 acc = S[j][bb][t] * across;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) acc = mma(kf[m], wf[j][m], acc);
+            S[j][bb][t] = acc;
           }
-#pragma unroll
-          for (int bb = 0; bb < kB; ++bb)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              f32x4 acc = S[j][bb][t] * across;
-#pragma unroll
-              for (int m = 0; m < 2; ++m) acc = mma(turned_frag<kPk>(ks, m, 32 * bb + 4 * t, 8, g, c16), vf[m], acc);
-              S[j][bb][t] = acc;
-            }
         }
-      }
-      if (n < kChunk) ends(kChunk);   // (against time the short chunk comes first)
     }
+    if (n < kChunk) ends(kChunk);   // (against time the short chunk comes first)
     __syncthreads();
   }
   if constexpr (OUT) {
@@ -436,35 +538,97 @@ __global__ __launch_bounds__(64 * waves<DV>()) void sweep_kernel(LinearSweep s) 
   }
 }
 
-template <typename IO, typename O, int DK, int DV, bool OUT>
-hipError_t launch_sweep(const LinearSweep& s, hipStream_t st) {
-  auto* const kernel = sweep_kernel<IO, O, DK, DV, OUT>;
-  constexpr int lds = lds_bytes<IO, DK, DV, sizeof(O) == 2 ? 2 : 3, OUT>();
-  static_assert(lds <= 160 * 1024);
-  if constexpr (lds > 64 * 1024) {
+// One sweep, or what two sweeps' tiles add, one after the other.
+struct Sweeps2 {
+  LinearSweep s[2];
+  uint32_t blocks;     // of each
+};
+template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN>
+__global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<DK, DV>())) void sweep_kernel(Sweeps2 p) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const uint32_t which = blockIdx.x >= p.blocks ? 1 : 0;
+  sweep<IO, O, DK, DV, OUT, WRITTEN>(p.s[which], blockIdx.x - which * p.blocks, lds);
+}
+
+// The three gradients' sweeps, dv's over keys of DK, dk's and dq's over keys of DV.  The
+// three workgroups of a tile read the same rows: they lie eight apart, which is the
+// same XCD, so that two of them find the rows in its L2.
+struct Sweeps3 {
+  LinearSweep s[3];
+  uint32_t blocks;
+};
+template <typename IO, int DK, int DV>
+__global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<DK, DV>())) void gradients_kernel(Sweeps3 p) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const uint32_t which = blockIdx.x / 8 % 3, block = blockIdx.x / 24 * 8 + blockIdx.x % 8;
+  if (block >= p.blocks) return;
+  if constexpr (DK == DV) {
+    sweep<IO, float, DK, DV, true, 3>(p.s[which], block, lds);
+  } else if (which == 0) {
+    sweep<IO, float, DK, DV, true, 3>(p.s[0], block, lds);
+  } else {
+    sweep<IO, float, DV, DK, true, 3>(p.s[which], block, lds);
+  }
+}
+
+template <typename Kernel, typename Args>
+hipError_t launch(Kernel kernel, uint32_t blocks, int threads, int lds, const Args& args, hipStream_t st) {
+  if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  kernel<<<dim3(unsigned(s.heads * s.tiles)), dim3(64 * waves<DV>()), lds, st>>>(s);
+  kernel<<<dim3(blocks), dim3(threads), lds, st>>>(args);
   return hipGetLastError();
 }
 
-// The sweeps of keys of DK, by value width, types and whether there are outputs.
-template <int DK>
-hipError_t sweep_of(const LinearSweep& s, hipStream_t st) {
-  auto by_type = [&](auto dv) -> hipError_t {
-    constexpr int DV = decltype(dv)::value;
-    if (!s.out) return s.bf16 ? launch_sweep<bf16_t, float, DK, DV, false>(s, st) : launch_sweep<float, float, DK, DV, false>(s, st);
-    if (!s.bf16) return launch_sweep<float, float, DK, DV, true>(s, st);
-    return s.out_bf16 ? launch_sweep<bf16_t, bf16_t, DK, DV, true>(s, st) : launch_sweep<bf16_t, float, DK, DV, true>(s, st);
-  };
+template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN = 3>
+hipError_t launch_sweep(const LinearSweep& s, const LinearSweep* second, hipStream_t st) {
+  constexpr int lds = lds_bytes<IO, O, DK, DV, OUT>();
+  static_assert(lds <= 160 * 1024);
+  const uint32_t blocks = uint32_t(s.heads * s.tiles);
+  return launch(sweep_kernel<IO, O, DK, DV, OUT, WRITTEN>, blocks * (second ? 2 : 1), 64 * waves<IO, DK, DV>(), lds,
+                Sweeps2{{s, second ? *second : s}, blocks}, st);
+}
+
+template <typename IO, int DK, int DV>
+hipError_t launch_gradients(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st) {
+  constexpr int a = lds_bytes<IO, float, DK, DV, true>(), b = lds_bytes<IO, float, DV, DK, true>(), lds = a > b ? a : b;
+  static_assert(lds <= 160 * 1024);
+  const uint32_t blocks = uint32_t(dv.heads * dv.tiles);
+  return launch(gradients_kernel<IO, DK, DV>, (blocks + 7) / 8 * 24, 64 * waves<IO, DK, DV>(), lds, Sweeps3{{dv, dk, dq}, blocks}, st);
+}
+
+template <typename F>
+hipError_t by_width(int dv, F f) {
   using std::integral_constant;
-  switch (s.dv) {
-    case 16: return by_type(integral_constant<int, 16>{});
-    case 32: return by_type(integral_constant<int, 32>{});
-    case 64: return by_type(integral_constant<int, 64>{});
-    default: return by_type(integral_constant<int, 128>{});
+  switch (dv) {
+    case 16: return f(integral_constant<int, 16>{});
+    case 32: return f(integral_constant<int, 32>{});
+    case 64: return f(integral_constant<int, 64>{});
+    default: return f(integral_constant<int, 128>{});
   }
+}
+
+// What tiles with keys of DK add, of one or two sweeps of the same sizes; outputs of a
+// prompt; the gradients.
+template <int DK>
+hipError_t sums_of(const LinearSweep& s, const LinearSweep* second, hipStream_t st) {
+  return by_width(s.dv, [&](auto dv) {
+    return s.bf16 ? launch_sweep<bf16_t, float, DK, dv(), false>(s, second, st) : launch_sweep<float, float, DK, dv(), false>(s, second, st);
+  });
+}
+template <int DK>
+hipError_t outputs_of(const LinearSweep& s, hipStream_t st) {
+  return by_width(s.dv, [&](auto dv) {
+    if (!s.bf16) return launch_sweep<float, float, DK, dv(), true>(s, nullptr, st);
+    return s.last ? launch_sweep<bf16_t, bf16_t, DK, dv(), true>(s, nullptr, st) : launch_sweep<bf16_t, bf16_t, DK, dv(), true, 2>(s, nullptr, st);
+  });
+}
+template <int DK>
+hipError_t gradients_of(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st) {
+  return by_width(dv.dv, [&](auto width) {
+    return dv.bf16 ? launch_gradients<bf16_t, DK, width()>(dv, dk, dq, st) : launch_gradients<float, DK, width()>(dv, dk, dq, st);
+  });
 }
 
 }  // namespace linear

@@ -538,7 +538,8 @@ size_t falcon_scan_bwd_workspace_bytes(const falcon_scan_problem* p);
  *               may alias S0 exactly.
  *  workspace  : at least falcon_linear_workspace_bytes(p) bytes (may be NULL when
  *               that is 0), 16-byte aligned, overlapping nothing else.
- * dk, dv in {16, 32, 64, 128}; at most 2^22 heads (B H).  The prompt is worked on in
+ * dk, dv in {16, 32, 64, 128}; at most 2^21 heads (B H) and 2^22 elements of a
+ * row.  The prompt is worked on in
  * chunks of 64 tokens: float32 throughout with float32 inputs, and with bf16 inputs
  * by bf16 products with float32 sums in which every float32 operand is a sum of two
  * bf16 numbers (three for the state and for gradients), so results are those of
