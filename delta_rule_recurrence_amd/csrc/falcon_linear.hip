@@ -31,8 +31,8 @@ struct Tiles {
 Tiles cut(const LinearArgs& a) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
   // tiles of a head for three workgroups a CU, or for the two that wide heads leave room for
-  const int64_t all_tiles = a.dk * a.dv > 64 * 64 ? 512 : 768;
-  const int64_t want = std::max<int64_t>(1, (all_tiles + heads - 1) / std::max<int64_t>(heads, 1));
+  const int64_t all_tiles = a.dk * a.dv > 64 * 128 ? 256 : a.dk * a.dv > 64 * 64 ? 512 : 768;
+  const int64_t want = std::max<int64_t>(1, all_tiles / std::max<int64_t>(heads, 1));   // (one more would take a round of its own)
   const int64_t chunks = std::max<int64_t>(1, (all + want - 1) / want);
   return {heads, int(chunks), int(std::max<int64_t>(1, (all + chunks - 1) / chunks))};
 }

@@ -51,6 +51,8 @@ using frag::s16x4;
 constexpr int kChunk = 64;
 
 // ---- operands: eight values a lane of a 32-wide block of the summed axis ---------
+// Lanes 16 g .. 16 g + 15 hold indices {4 g .. + 3, 16 + 4 g .. + 3} of a block: what two
+// stacked result tiles hold, and neighbours in LDS for the transposing reads.
 struct f32x8 {
   f32x4 lo, hi;
 };
@@ -130,33 +132,33 @@ struct Stage {
   static constexpr int kBytes = kChunk * kPitch * int(sizeof(IO));
 };
 
-// A row's eight values 32 b + 8 g .. + 7 of its columns.
+// A row's eight values of block b of its columns.
 template <int PITCH>
 __device__ __forceinline__ bf16x8 row_frag(const bf16_t* rows, int row, int b, int g) {
-  return *reinterpret_cast<const bf16x8*>(rows + row * PITCH + 32 * b + 8 * g);
+  const s16x4* p = reinterpret_cast<const s16x4*>(rows + row * PITCH + 32 * b + 4 * g);
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(p[0], p[4], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 template <int PITCH>
 __device__ __forceinline__ f32x8 row_frag(const float* rows, int row, int b, int g) {
-  const f32x4* p = reinterpret_cast<const f32x4*>(rows + row * PITCH + 32 * b + 8 * g);
-  return {p[0], p[1]};
+  const f32x4* p = reinterpret_cast<const f32x4*>(rows + row * PITCH + 32 * b + 4 * g);
+  return {p[0], p[4]};
 }
 
 __device__ __forceinline__ s16x4 read_turned(const bf16_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
 }
-// Tokens {32 m + 4 g .. + 3, 32 m + 16 + 4 g .. + 3} (the order in which stacked
-// result tiles hold them) of one column a lane: column first + step (l / 4) + l % 4
-// of lane l < 16 of a group.  The transposing read takes from each lane the address
-// of four neighbours and gives lane l the element l % 4 of segment l / 4 of four rows.
+// The eight tokens of block m of column first + c16.  The transposing read takes from
+// each lane the address of four neighbours and gives lane l < 16 of a group the element
+// l % 4 of segment l / 4 of four rows.
 template <int PITCH>
-__device__ __forceinline__ bf16x8 turned_frag(const bf16_t* rows, int m, int first, int step, int g, int c16) {
-  const bf16_t* p = rows + (32 * m + 4 * g + (c16 >> 2)) * PITCH + first + step * (c16 & 3);
+__device__ __forceinline__ bf16x8 turned_frag(const bf16_t* rows, int m, int first, int g, int c16) {
+  const bf16_t* p = rows + (32 * m + 4 * g + (c16 >> 2)) * PITCH + first + 4 * (c16 & 3);
   const s16x4 lo = read_turned(p), hi = read_turned(p + 16 * PITCH);
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 template <int PITCH>
-__device__ __forceinline__ f32x8 turned_frag(const float* rows, int m, int first, int step, int g, int c16) {
-  const float* p = rows + (32 * m + 4 * g) * PITCH + first + step * (c16 >> 2) + (c16 & 3);
+__device__ __forceinline__ f32x8 turned_frag(const float* rows, int m, int first, int g, int c16) {
+  const float* p = rows + (32 * m + 4 * g) * PITCH + first + c16;
   f32x8 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -197,6 +199,19 @@ __device__ __forceinline__ void get(const char* lds, int frag, int l, f32x8& v) 
   v = {p[0], p[64]};
 }
 
+// Columns 8 g .. + 7 of a row, the lane's own, to where the fragment has them.
+__device__ __forceinline__ void put_row(char* lds, int frag, int g, int c16, bf16x8 v) {
+  uint2* p = reinterpret_cast<uint2*>(lds) + (frag * 64 + 32 * (g & 1) + c16) * 2 + (g >> 1);
+  const uint4 u = __builtin_bit_cast(uint4, v);
+  p[0] = make_uint2(u.x, u.y);
+  p[32] = make_uint2(u.z, u.w);
+}
+__device__ __forceinline__ void put_row(char* lds, int frag, int g, int c16, const f32x8& v) {
+  f32x4* p = reinterpret_cast<f32x4*>(lds) + frag * 128 + 64 * (g >> 1) + 32 * (g & 1) + c16;
+  p[0] = v.lo;
+  p[16] = v.hi;
+}
+
 // A chunk's rows on the way from memory to LDS, 16 bytes a thread and access.
 template <typename IO, int D, int THREADS>
 struct Rows {
@@ -207,23 +222,36 @@ struct Rows {
   static_assert(THREADS % kSegs == 0);
   uint4 r[kMine];
 
-  // Rows behind the chunk's n tokens are not read: their threads take the last one.
-  // (Offsets within a chunk fit 32 bits: rows have at most 2^22 elements.)
-  __device__ __forceinline__ void fetch(const IO* first, int t_step, int n, int tid) {
+  // The chunk's n tokens are rows `shift` on.  Threads of other rows read its first or last
+  // token.  (Offsets within a chunk fit 32 bits: rows have at most 2^22 elements.)
+  __device__ __forceinline__ void fetch(const IO* first, int t_step, int n, int shift, int tid) {
     const char* const p = reinterpret_cast<const char*>(first);
-    const uint32_t seg = uint32_t(tid % kSegs) * 16;
+    const uint32_t seg = uint32_t(tid % kSegs) * 16, step = uint32_t(t_step) * uint32_t(sizeof(IO));
+    if (n == kChunk && kAll % THREADS == 0) {
+      const uint32_t at = uint32_t(tid / kSegs) * step + seg;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int row = min(tid / kSegs + i * (THREADS / kSegs), n - 1);
-      r[i] = *reinterpret_cast<const uint4*>(p + (uint32_t(row) * uint32_t(t_step) * uint32_t(sizeof(IO)) + seg));
+      for (int i = 0; i < kMine; ++i) r[i] = *reinterpret_cast<const uint4*>(p + int64_t(i * (THREADS / kSegs)) * step + at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int row = min(max(tid / kSegs + i * (THREADS / kSegs) - shift, 0), n - 1);
+        r[i] = *reinterpret_cast<const uint4*>(p + (uint32_t(row) * step + seg));
+      }
     }
   }
-  __device__ __forceinline__ void store(IO* rows, int n, int tid) const {
+  __device__ __forceinline__ void store(IO* rows, int n, int shift, int tid) const {
+    const int first = tid / kSegs, seg = tid % kSegs;
+    uint4* const p = reinterpret_cast<uint4*>(rows + first * Stage<IO, D>::kPitch + seg * kEach);
+    constexpr int kStep = THREADS / kSegs * Stage<IO, D>::kPitch * int(sizeof(IO)) / 16;
+    if (n == kChunk && kAll % THREADS == 0) {
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int row = tid / kSegs + i * (THREADS / kSegs), seg = tid % kSegs;
-      if (kAll % THREADS == 0 || row < kChunk)
-        *reinterpret_cast<uint4*>(rows + row * Stage<IO, D>::kPitch + seg * kEach) = row < n ? r[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kMine; ++i) p[i * kStep] = r[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int row = first + i * (THREADS / kSegs);
+        if (kAll % THREADS == 0 || row < kChunk) p[i * kStep] = uint32_t(row - shift) < uint32_t(n) ? r[i] : make_uint4(0, 0, 0, 0);
+      }
     }
   }
 };
@@ -233,11 +261,11 @@ __device__ __forceinline__ float power(float log2_a, int n) {
   return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(log2_a * float(n));
 }
 
-// Waves of a workgroup: eight where float32 operands of 128 columns would not fit the
-// registers of four.
+// Waves of a workgroup: eight where what four hold would not fit their registers, float32
+// operands of 128 columns and states of 128 x 128.
 template <typename IO, int DK, int DV>
 constexpr int waves() {
-  return sizeof(IO) == 4 && (DK >= 128 || DV >= 128) ? 8 : 4;
+  return (sizeof(IO) == 4 && (DK >= 128 || DV >= 128)) || (DK >= 128 && DV >= 128) ? 8 : 4;
 }
 // Waves of a SIMD that the registers are to leave room for: as many as LDS does.
 template <int DK, int DV>
@@ -305,16 +333,19 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   Exact qr[OUT ? kB : 1];
   auto chunk_at = [&](int step) { return s.rev ? chunks - 1 - step : step; };
   auto tokens_in = [&](int c) { return min(len - first - c * kChunk, kChunk); };
+  // A short chunk's tokens are its last rows, or its first against time: what is written
+  // decays by the row alone.
+  auto shift_of = [&](int n) { return s.rev ? 0 : kChunk - n; };
   auto fetch = [&](int c) {
-    const int n = tokens_in(c);
-    kr.fetch(K + int64_t(c) * kChunk * k_step, k_step, n, tid);
-    vr.fetch(V + int64_t(c) * kChunk * v_step, v_step, n, tid);
+    const int n = tokens_in(c), shift = shift_of(n);
+    kr.fetch(K + int64_t(c) * kChunk * k_step, k_step, n, shift, tid);
+    vr.fetch(V + int64_t(c) * kChunk * v_step, v_step, n, shift, tid);
     if constexpr (OUT) {
       if (w < 4) {
-        // rows of queries as fragments: columns 32 bb + 8 g .. + 7 of token 16 rw + c16
+        // columns 32 bb + 8 g .. + 7 of query row 16 rw + c16
         const bool there = DK >= 32 || g < 2;
         const char* p = reinterpret_cast<const char*>(Q + int64_t(c) * kChunk * q_step);
-        const uint32_t row = uint32_t(min(16 * rw + c16, n - 1)) * uint32_t(q_step);
+        const uint32_t row = uint32_t(min(max(16 * rw + c16 - shift, 0), n - 1)) * uint32_t(q_step);
 #pragma unroll
         for (int bb = 0; bb < kB; ++bb) {
           const uint32_t at = (row + 32 * bb + (there ? 8 * g : 0)) * uint32_t(sizeof(IO));
@@ -331,9 +362,8 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   };
   if (chunks > 0) fetch(chunk_at(0));
 
-  // A state's element (f, c) at f sf + c sc.  Rows 32 b + 8 g + 4 t + r of column
-  // 16 cb + c16 lie in S[.][b][t][r]: two tiles stacked are eight neighbours of the
-  // key axis, as a row of queries is read.
+  // A state's element (f, c) at f sf + c sc.  Rows 32 b + 16 t + 4 g + r of column
+  // 16 cb + c16 lie in S[.][b][t][r].
   f32x4 S[kOwn][kB][2];
   const float* const from = OUT ? (slot ? slot : s.start ? s.start + bh * (DK * DV) : nullptr) : nullptr;
 #pragma unroll
@@ -343,7 +373,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         S[j][bb][t] = frag::zero4();
-        const int f = 32 * bb + 8 * g + 4 * t;
+        const int f = 32 * bb + 16 * t + 4 * g;
         if (OUT && from && f < DK)
 #pragma unroll
           for (int r = 0; r < 4; ++r) S[j][bb][t][r] = from[(f + r) * s.sf + (16 * column(j) + c16) * s.sc];
@@ -356,7 +386,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
       for (int bb = 0; bb < kB; ++bb)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const int f = 32 * bb + 8 * g + 4 * t;
+          const int f = 32 * bb + 16 * t + 4 * g;
           if (f < DK)
 #pragma unroll
             for (int r = 0; r < 4; ++r) to[(f + r) * s.sf + (16 * column(j) + c16) * s.sc] = S[j][bb][t][r];
@@ -372,60 +402,49 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
     for (int i = tid; i < kChunk * kPk; i += kThreads) ks[i] = IO{};
     __syncthreads();
   }
-  // Decays between this lane's query token i = 16 rw + c16 and the keys of its score
-  // rows, 16 sb + 4 g + r, of the pairs m of 16 keys that are this wave's.
-  constexpr int kPairs = kWaves == 8 ? 1 : 2;
+  // Decays, as products of a factor of the four rows 4 g + r of a block of 16 and one of
+  // the row r: from a key row 32 m + 16 u + 4 g + r to the chunk's end, and to this lane's
+  // query row 16 rw + c16.  In the block of the queries themselves they have a mask.
+  constexpr int kPairs = kWaves == 8 ? 1 : 2;              // pairs m of 16 keys that are this wave's
   auto pair = [&](int x) { return kWaves == 8 ? w >> 2 : x; };
-  f32x4 mask[OUT ? kPairs : 1][2];
+  float by_row[4], to_end[2][2], to_query[OUT ? kPairs : 1][2];
+  f32x4 own;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    by_row[r] = power(e, s.rev ? r : 3 - r);
+    const int gap = s.rev ? 4 * g + r - c16 : c16 - (4 * g + r);
+    own[r] = gap >= 0 ? power(e, max(gap, 0)) * s.write : 0.0f;
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int row = 32 * m + 16 * u + 4 * g;
+      to_end[m][u] = power(e, s.rev ? row + 1 : kChunk - 4 - row) * s.write;
+    }
   if constexpr (OUT) {
-    const int i = 16 * rw + c16;
 #pragma unroll
     for (int x = 0; x < kPairs; ++x)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = 32 * pair(x) + 16 * u + 4 * g + r, gap = s.rev ? key - i : i - key;
-          mask[x][u][r] = gap >= 0 ? power(e, max(gap, 0)) * s.write : 0.0f;
-        }
-  }
-  // Decays of this lane's tokens 32 m + 16 u + 4 g + r up to the chunk's end, and of the
-  // entering state at the tokens of its outputs.
-  f32x4 to_end[2][2];
-  float into[OUT ? kRows : 1];
-  auto ends = [&](int n) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 32 * m + 16 * u + 4 * g + r;
-          to_end[m][u][r] = power(e, s.rev ? min(t + 1, n) : max(n - 1 - t, 0)) * s.write;
-        }
-    if constexpr (OUT) {
-#pragma unroll
-      for (int x = 0; x < kRows; ++x) {
-        const int i = 16 * tokens(x) + c16;
-        into[x] = power(e, s.rev ? max(n - 1 - i, 0) : i + 1);
+      for (int u = 0; u < 2; ++u) {
+        const int row = 32 * pair(x) + 16 * u + 4 * g, i = 16 * rw + c16;
+        to_query[x][u] = power(e, max(s.rev ? row - i : i - row - 3, 0)) * s.write;
       }
-    }
-  };
-  ends(kChunk);
+  }
   const float whole = power(e, kChunk);
 
   for (int step = 0; step < chunks; ++step) {
     const int c = chunk_at(step), n = tokens_in(c);
     const bool more = step + 1 < chunks;
-    kr.store(ks, n, tid);
-    vr.store(vs, n, tid);
+    const int shift = shift_of(n);
+    kr.store(ks, n, shift, tid);
+    vr.store(vs, n, shift, tid);
     if constexpr (OUT) {
       if (w < 4) {
 #pragma unroll
-        for (int bb = 0; bb < kB; ++bb) put(qs, rw * kB + bb, l, qr[bb]);
+        for (int bb = 0; bb < kB; ++bb) put_row(qs, rw * kB + bb, g, c16, qr[bb]);
       }
     }
-    if (n < kChunk) ends(n);
     __syncthreads();
     if (more) fetch(chunk_at(step + 1));
     Exact vf[kOwn][2];
@@ -445,11 +464,17 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           p[u] = frag::zero4();
 #pragma unroll
           for (int bb = 0; bb < kB; ++bb) p[u] = mma(row_frag<kPk>(ks, 32 * m + 16 * u + c16, bb, g), qf[bb], p[u]);
-          // (a product with the mask's zero would keep what is not finite; the comparisons
-          // made ahead of the loop would fill the scalar registers)
-          asm volatile("" : "+v"(mask[x][u]));
+          const int block = 2 * m + u;
+          if (block == rw) {
+            // (a product with the mask's zero would keep what is not finite)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[u][r] = mask[x][u][r] != 0.0f ? p[u][r] * mask[x][u][r] : 0.0f;
+            for (int r = 0; r < 4; ++r) p[u][r] = own[r] != 0.0f ? p[u][r] * own[r] : 0.0f;
+          } else if (s.rev ? block > rw : block < rw) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[u][r] *= to_query[x][u] * by_row[r];
+          } else {
+            p[u] = frag::zero4();
+          }
         }
         Split pf;
         split(p[0], p[1], pf);
@@ -479,16 +504,17 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
     for (int j = 0; j < kOwn; ++j)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) vf[j][m] = turned_frag<kPv>(vs, m, 16 * column(j), 4, g, c16);
+      for (int m = 0; m < 2; ++m) vf[j][m] = turned_frag<kPv>(vs, m, 16 * column(j), g, c16);
     if constexpr (OUT) {
       __syncthreads();
       if (makes) {
         char* const to = reinterpret_cast<char*>(out + int64_t(c) * kChunk * out_step);
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
-          const int rb = tokens(x), i = 16 * rb + c16;
+          const int rb = tokens(x), i = 16 * rb + c16 - shift;
+          const float into = power(e, max(s.rev ? n - 1 - i : i + 1, 0));
 #pragma unroll
-          for (int j = 0; j < kOwn; ++j) o[x][j] = o[x][j] * into[x];
+          for (int j = 0; j < kOwn; ++j) o[x][j] = o[x][j] * into;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (!(s.rev ? m == 1 || rb < 2 : m == 0 || rb >= 2)) continue;
@@ -497,7 +523,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) o[x][j] = mma(vf[j][m], pf, o[x][j]);
           }
-          if (i < n) {
+          if (uint32_t(i) < uint32_t(n)) {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
               store4(reinterpret_cast<O*>(to + (uint32_t(i) * uint32_t(out_step) + 16 * column(j) + 4 * g) * uint32_t(sizeof(O))), o[x][j] * s.read);
@@ -511,14 +537,23 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
       for (int j = 0; j < kOwn; ++j)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) split(widened(vf[j][m], 0) * to_end[m][0], widened(vf[j][m], 1) * to_end[m][1], wf[j][m]);
+        for (int m = 0; m < 2; ++m) {
+          f32x4 part[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            part[u] = widened(vf[j][m], u) * to_end[m][u];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) part[u][r] *= by_row[r];
+          }
+          split(part[0], part[1], wf[j][m]);
+        }
 #pragma unroll
       for (int bb = 0; bb < kB; ++bb)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           Exact kf[2];
 #pragma unroll
-          for (int m = 0; m < 2; ++m) kf[m] = turned_frag<kPk>(ks, m, 32 * bb + 4 * t, 8, g, c16);
+          for (int m = 0; m < 2; ++m) kf[m] = turned_frag<kPk>(ks, m, 32 * bb + 16 * t, g, c16);
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
             f32x4 acc = S[j][bb][t] * across;
@@ -528,7 +563,6 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           }
         }
     }
-    if (n < kChunk) ends(kChunk);   // (against time the short chunk comes first)
     __syncthreads();
   }
   if constexpr (OUT) {
