@@ -413,7 +413,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   for (int r = 0; r < 4; ++r) {
     by_row[r] = power(e, s.rev ? r : 3 - r);
     const int gap = s.rev ? 4 * g + r - c16 : c16 - (4 * g + r);
-    own[r] = gap >= 0 ? power(e, max(gap, 0)) * s.write : 0.0f;
+    own[r] = gap >= 0 ? power(e, max(gap, 0)) * s.write * s.read : 0.0f;
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -428,8 +428,14 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int row = 32 * pair(x) + 16 * u + 4 * g, i = 16 * rw + c16;
-        to_query[x][u] = power(e, max(s.rev ? row - i : i - row - 3, 0)) * s.write;
+        to_query[x][u] = power(e, max(s.rev ? row - i : i - row - 3, 0)) * s.write * s.read;
       }
+  }
+  // ... and of the entering state at the rows of this wave's outputs, of whole chunks.
+  float into[OUT ? kRows : 1];
+  if constexpr (OUT) {
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) into[x] = power(e, s.rev ? kChunk - 1 - (16 * tokens(x) + c16) : 16 * tokens(x) + c16 + 1) * s.read;
   }
   const float whole = power(e, kChunk);
 
@@ -512,9 +518,9 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
           const int rb = tokens(x), i = 16 * rb + c16 - shift;
-          const float into = power(e, max(s.rev ? n - 1 - i : i + 1, 0));
+          const float at_row = n == kChunk ? into[x] : power(e, max(s.rev ? n - 1 - i : i + 1, 0)) * s.read;
 #pragma unroll
-          for (int j = 0; j < kOwn; ++j) o[x][j] = o[x][j] * into;
+          for (int j = 0; j < kOwn; ++j) o[x][j] = o[x][j] * at_row;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (!(s.rev ? m == 1 || rb < 2 : m == 0 || rb >= 2)) continue;
@@ -526,7 +532,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           if (uint32_t(i) < uint32_t(n)) {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
-              store4(reinterpret_cast<O*>(to + (uint32_t(i) * uint32_t(out_step) + 16 * column(j) + 4 * g) * uint32_t(sizeof(O))), o[x][j] * s.read);
+              store4(reinterpret_cast<O*>(to + (uint32_t(i) * uint32_t(out_step) + 16 * column(j) + 4 * g) * uint32_t(sizeof(O))), o[x][j]);
           }
         }
       }
