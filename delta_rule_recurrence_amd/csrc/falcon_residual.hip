@@ -10,8 +10,8 @@
 //   dalpha = post_weight A,  dpost_weight = alpha A,  A = sum D f yhat;  dpre_weight = sum dn hhat
 //
 // Bound by bytes: every tensor is read or written once.  A row of C channels is held by
-// 64 to 512 threads, up to two pieces of 8 channels each, from its loads to its stores;
-// a thread keeps its channels' weights and walks over rows.  Sums of squares are made in
+// one to sixteen waves, a piece of 8 channels a thread, from its loads to its stores; a
+// thread keeps its channels' weights and walks over rows.  Sums of squares are made in
 // double, so that no row of float32 numbers leaves their range.  A group's sum is a sum
 // over lanes where a group is 1, 2, 4, ... 64 pieces of 8, else it goes through LDS; a
 // whole row's over the row's waves.
@@ -31,11 +31,11 @@ namespace {
 
 constexpr int kPiece = 8;
 constexpr int kBlock = 32;        // channels of one step
-constexpr int kRowsEach = 64;     // rows whose parts of the parameters' gradients one thread sums: float32 sums stay short
+constexpr int rowsEach = 64;     // rows whose parts of the parameters' gradients one thread sums: float32 sums stay short
 
 // How rows and groups lie on threads.
 struct Shape {
-  int threads_row, nc, rows_block;   // threads of a row, pieces of a thread, rows of a workgroup at a time
+  int threads_row, rows_block;       // threads of a row (whole waves), rows of a workgroup at a time
   int64_t blocks;
   int rows_each;                     // rows a thread walks over
   int group_lanes;                   // lanes of a group; 0: through LDS; -1: the group is the row
@@ -45,87 +45,141 @@ struct Shape {
 // ---- rows; their types are met at run time (a uniform branch a tensor) ---------------
 // WIDE: pieces of 8 adjacent channels, one wide access each; else neighbours go to
 // neighbouring lanes, element by element.
-template <int NC, bool WIDE, int TPR>
+template <bool WIDE>
 struct Lane {
-  int t, C;
-  __device__ __forceinline__ int channel(int k, int i) const { return WIDE ? (k * TPR + t) * kPiece + i : (k * kPiece + i) * TPR + t; }
+  int t, C, threads;      // of the row's threads
+  __device__ __forceinline__ int channel(int i) const { return WIDE ? t * kPiece + i : i * threads + t; }
 };
 
-template <int NC, bool WIDE, int TPR, typename E>
-__device__ __forceinline__ void load_typed(const E* p, const Lane<NC, WIDE, TPR>& at, float missing, float (&v)[NC][kPiece]) {
+template <bool WIDE, typename E>
+__device__ __forceinline__ void load_typed(const E* p, const Lane<WIDE>& at, float missing, float (&v)[kPiece]) {
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    if constexpr (WIDE) {
+    for (int i = 0; i < kPiece; ++i) v[i] = missing;
+    const int c = at.channel(0);
+    if (c < at.C) load_vec<E, kPiece>(p + c, v);
+  } else {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[k][i] = missing;
-      const int c = at.channel(k, 0);
-      if (c < at.C) load_vec<E, kPiece>(p + c, v[k]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        const int c = at.channel(k, i);
-        v[k][i] = c < at.C ? io<E>::load(p, c) : missing;
-      }
+    for (int i = 0; i < kPiece; ++i) {
+      const int c = at.channel(i);
+      v[i] = c < at.C ? io<E>::load(p, c) : missing;
     }
   }
 }
-// Row `row` of `step` elements; `on` false: not read, zeros.
-template <int NC, bool WIDE, int TPR>
-__device__ __forceinline__ void load_row(const void* p, bool bf16, int64_t at_row, const Lane<NC, WIDE, TPR>& at, bool on, float (&v)[NC][kPiece]) {
-  if (on && p) {
-    if (bf16) {
-      load_typed<NC, WIDE, TPR>(static_cast<const bf16_t*>(p) + at_row, at, 0.0f, v);
-    } else {
-      load_typed<NC, WIDE, TPR>(static_cast<const float*>(p) + at_row, at, 0.0f, v);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[k][i] = 0.0f;
-  }
-}
-template <int NC, bool WIDE, int TPR, typename E>
-__device__ __forceinline__ void store_typed(E* p, const Lane<NC, WIDE, TPR>& at, const float (&v)[NC][kPiece]) {
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    if constexpr (WIDE) {
-      const int c = at.channel(k, 0);
-      if (c < at.C) store_vec<E, kPiece>(p + c, v[k]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        const int c = at.channel(k, i);
-        if (c < at.C) io<E>::store(p, c, v[k][i]);
-      }
-    }
-  }
-}
-template <int NC, bool WIDE, int TPR>
-__device__ __forceinline__ void store_row(void* p, bool bf16, int64_t at_row, const Lane<NC, WIDE, TPR>& at, const float (&v)[NC][kPiece]) {
-  if (bf16) {
-    store_typed<NC, WIDE, TPR>(static_cast<bf16_t*>(p) + at_row, at, v);
-  } else {
-    store_typed<NC, WIDE, TPR>(static_cast<float*>(p) + at_row, at, v);
-  }
-}
-template <int NC, bool WIDE, int TPR>
-__device__ __forceinline__ void load_params(const float* p, float missing, const Lane<NC, WIDE, TPR>& at, float (&v)[NC][kPiece]) {
-  if (p) {
-    load_typed<NC, WIDE, TPR>(p, at, missing, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[k][i] = missing;
-  }
-}
-
-// ---- 8 bits ---------------------------------------------------------------------------
 // A step's byte is its float32 exponent field; 255, whose step is infinite, with codes of
 // zero stands for channels that were not all finite: they come back as NaN.
 __device__ __forceinline__ float step_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// A thread's channels of a row as they lie in memory: a row's loads are all under way before
+// the first is waited for, which conversions right behind each would do.
+template <bool WIDE>
+struct Raw {
+  uint32_t w[kPiece];                 // packed where WIDE, else a channel each
+  uint32_t step[WIDE ? 1 : kPiece];   // of 8 bits
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < (WIDE ? 1 : kPiece); ++i) step[i] = 0;
+  }
+  // (WIDE: by threads whose channels there are)
+  __device__ __forceinline__ void fetch(const void* p, bool bf16, int64_t at_row, const Lane<WIDE>& at) {
+    if constexpr (WIDE) {
+      if (bf16) {
+        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const bf16_t*>(p) + at_row + at.channel(0));
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+      } else {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at_row + at.channel(0));
+        const uint4 a = q[0], b = q[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) {
+        const int c = at.channel(i);
+        if (c < at.C) w[i] = bf16 ? static_cast<const uint16_t*>(p)[at_row + c] : static_cast<const uint32_t*>(p)[at_row + c];
+      }
+    }
+  }
+  __device__ __forceinline__ void fetch8(const int8_t* codes, const uint8_t* steps, const Lane<WIDE>& at) {
+    if constexpr (WIDE) {
+      const int c = at.channel(0);
+      const uint2 a = *reinterpret_cast<const uint2*>(codes + c);
+      w[0] = a.x, w[1] = a.y;
+      step[0] = steps[c / kBlock];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) {
+        const int c = at.channel(i);
+        if (c < at.C) w[i] = uint8_t(codes[c]), step[i] = steps[c / kBlock];
+      }
+    }
+  }
+  __device__ __forceinline__ void values(bool bf16, float (&v)[kPiece]) const {
+    if (bf16) {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i)
+        v[i] = __uint_as_float(!WIDE ? w[i] << 16 : i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) v[i] = __uint_as_float(w[i]);
+    }
+  }
+  __device__ __forceinline__ void values8(float (&v)[kPiece]) const {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+      v[i] = float(int8_t(WIDE ? w[i / 4] >> (8 * (i % 4)) : w[i])) * step_of(step[WIDE ? 0 : i]);
+  }
+};
+
+// Outputs are written past the caches' usual order (nontemporal): the gradients of
+// 16384 x 768 took 74 us against 79, of 5555 x 2304 71 against 81.
+__device__ __forceinline__ void store_piece(float* p, const float (&v)[kPiece]) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p) + 1);
+}
+__device__ __forceinline__ void store_piece(bf16_t* p, const float (&v)[kPiece]) {
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const bf16x8 b = __builtin_convertvector((f32x8{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}), bf16x8);
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, b), reinterpret_cast<u32x4*>(p));
+}
+template <bool WIDE, typename E>
+__device__ __forceinline__ void store_typed(E* p, const Lane<WIDE>& at, const float (&v)[kPiece]) {
+  if constexpr (WIDE) {
+    const int c = at.channel(0);
+    if (c < at.C) store_piece(p + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const int c = at.channel(i);
+      if (c < at.C) io<E>::store(p, c, v[i]);
+    }
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_row(void* p, bool bf16, int64_t at_row, const Lane<WIDE>& at, const float (&v)[kPiece]) {
+  if (bf16) {
+    store_typed<WIDE>(static_cast<bf16_t*>(p) + at_row, at, v);
+  } else {
+    store_typed<WIDE>(static_cast<float*>(p) + at_row, at, v);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void load_params(const float* p, float missing, const Lane<WIDE>& at, float (&v)[kPiece]) {
+  if (p) {
+    load_typed<WIDE>(p, at, missing, v);
+  } else {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) v[i] = missing;
+  }
+}
+
+// ---- 8 bits ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t step_byte(uint32_t largest) {
   if (largest >= 0x7f800000u) return 255;
   // largest = 1.m 2^E fits 127 steps of 2^(E - 6) = 1.984375 2^E, or of twice that
@@ -140,64 +194,37 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-template <int NC, bool WIDE, int TPR>
-__device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const Lane<NC, WIDE, TPR>& at, bool on, const float (&v)[NC][kPiece]) {
+template <bool WIDE>
+__device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const Lane<WIDE>& at, bool on, const float (&v)[kPiece]) {
+  if constexpr (WIDE) {
+    uint32_t largest = 0;
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    if constexpr (WIDE) {
-      uint32_t largest = 0;
+    for (int i = 0; i < kPiece; ++i) largest = max(largest, magnitude(v[i]));
+    const uint32_t byte = step_byte(lanes_max<kBlock / kPiece>(largest));
+    const float inverse = byte == 255 ? 0.0f : step_of(254 - byte);
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) largest = max(largest, magnitude(v[k][i]));
-      const uint32_t byte = step_byte(lanes_max<kBlock / kPiece>(largest));
-      const float inverse = byte == 255 ? 0.0f : step_of(254 - byte);
-      uint32_t w[2] = {0, 0};
+    for (int i = 0; i < kPiece; ++i) {
+      const int code = byte == 255 ? 0 : int(__builtin_rintf(v[i] * inverse));
+      w[i / 4] |= (uint32_t(code) & 255u) << (8 * (i % 4));
+    }
+    const int c = at.channel(0);
+    if (on && c < at.C) {
+      *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+      if (c % kBlock == 0) steps[c / kBlock] = uint8_t(byte);
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        const int code = byte == 255 ? 0 : int(__builtin_rintf(v[k][i] * inverse));
-        w[i / 4] |= (uint32_t(code) & 255u) << (8 * (i % 4));
-      }
-      const int c = at.channel(k, 0);
+    for (int i = 0; i < kPiece; ++i) {
+      const uint32_t byte = step_byte(lanes_max<kBlock>(magnitude(v[i])));
+      const int c = at.channel(i);
       if (on && c < at.C) {
-        *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+        codes[c] = byte == 255 ? int8_t(0) : int8_t(int(__builtin_rintf(v[i] * step_of(254 - byte))));
         if (c % kBlock == 0) steps[c / kBlock] = uint8_t(byte);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        const uint32_t byte = step_byte(lanes_max<kBlock>(magnitude(v[k][i])));
-        const int c = at.channel(k, i);
-        if (on && c < at.C) {
-          codes[c] = byte == 255 ? int8_t(0) : int8_t(int(__builtin_rintf(v[k][i] * step_of(254 - byte))));
-          if (c % kBlock == 0) steps[c / kBlock] = uint8_t(byte);
-        }
-      }
     }
   }
 }
-template <int NC, bool WIDE, int TPR>
-__device__ __forceinline__ void unpack_row(const int8_t* codes, const uint8_t* steps, const Lane<NC, WIDE, TPR>& at, bool on, float (&v)[NC][kPiece]) {
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[k][i] = 0.0f;
-    if constexpr (WIDE) {
-      const int c = at.channel(k, 0);
-      if (on && c < at.C) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + c);
-        const float step = step_of(steps[c / kBlock]);
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) v[k][i] = float(int8_t((i < 4 ? w.x : w.y) >> (8 * (i % 4)))) * step;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        const int c = at.channel(k, i);
-        if (on && c < at.C) v[k][i] = float(codes[c]) * step_of(steps[c / kBlock]);
-      }
-    }
-  }
-}
-
 // ---- sums --------------------------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ double dpp_plus(double v) {
@@ -236,68 +263,58 @@ __device__ __forceinline__ Inverse inverse_root(double m) {
 // The sums of one row over its groups.  `mine`: this thread's part, of each of its
 // pieces (WIDE) or channels.  The result is in place: each piece's (channel's) group's sum.
 // Every thread of the workgroup takes part.
-template <int NC, bool WIDE, int TPR>
+template <bool WIDE>
 struct Sums {
   static constexpr int kParts = WIDE ? 1 : kPiece;
-  static constexpr int kWaves = TPR / 64;
-  double* lds;            // of this row: [3 slots][2 turns][2 sums][kWaves], then [items + G] where groups go through it
-  int lanes, G, d;        // Shape::group_lanes
+  double* lds;            // of this row: [3 slots][2 turns][2 sums][waves], then [items + G] where groups go through it
+  int lanes, G, d, waves; // Shape::group_lanes; the row's waves
 
   // One sum over the row, or two at once.  Rounds with the same `slot` must have another barrier
   // between them; `turn` alternates.
   template <bool BOTH>
-  __device__ __forceinline__ void row(double& a, double& b, int slot, int turn, const Lane<NC, WIDE, TPR>& at) const {
+  __device__ __forceinline__ void row(double& a, double& b, int slot, int turn, const Lane<WIDE>& at) const {
     a = lanes_sum(a, 64);
     if constexpr (BOTH) b = lanes_sum(b, 64);
-    if constexpr (kWaves > 1) {
-      double* const mine = lds + (slot * 2 + turn) * 2 * kWaves;
+    if (waves > 1) {
+      double* const mine = lds + (slot * 2 + turn) * 2 * waves;
       const int w = at.t / 64;
       if (at.t % 64 == 0) {
         mine[w] = a;
-        if constexpr (BOTH) mine[kWaves + w] = b;
+        if constexpr (BOTH) mine[waves + w] = b;
       }
       __syncthreads();
       a = b = 0.0;
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
+      for (int k = 0; k < waves; ++k) {
         a += mine[k];
-        if constexpr (BOTH) b += mine[kWaves + k];
+        if constexpr (BOTH) b += mine[waves + k];
       }
     }
   }
-  __device__ __forceinline__ void groups(double (&part)[NC][kParts], int slot, int turn, const Lane<NC, WIDE, TPR>& at) const {
+  __device__ __forceinline__ void groups(double (&part)[kParts], int slot, int turn, const Lane<WIDE>& at) const {
     if (lanes < 0) {
       double all = 0.0, none = 0.0;
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) all += part[k][i];
+        for (int i = 0; i < kParts; ++i) all += part[i];
       row<false>(all, none, slot, turn, at);
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) part[k][i] = all;
+        for (int i = 0; i < kParts; ++i) part[i] = all;
     } else if (WIDE && lanes > 0) {
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) part[k][i] = lanes_sum(part[k][i], lanes);
+        for (int i = 0; i < kParts; ++i) part[i] = lanes_sum(part[i], lanes);
     } else {
       constexpr int kUnit = WIDE ? kPiece : 1;
       const int items = at.C / kUnit, each = d / kUnit;
-      double* const item = lds + 12 * kWaves;
+      double* const item = lds + 12 * waves;
       double* const sum = item + items;
       __syncthreads();    // the last round's sums have been read
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          const int c = at.channel(k, i);
-          if (c < at.C) item[c / kUnit] = part[k][i];
+          const int c = at.channel(i);
+          if (c < at.C) item[c / kUnit] = part[i];
         }
       __syncthreads();
       // a wave a group at a time
-      for (int g = at.t / 64; g < G; g += kWaves) {
+      for (int g = at.t / 64; g < G; g += waves) {
         double s = 0.0;
         for (int j = at.t % 64; j < each; j += 64) s += item[g * each + j];
         s = lanes_sum(s, 64);
@@ -305,24 +322,20 @@ struct Sums {
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          const int c = at.channel(k, i);
-          part[k][i] = c < at.C ? sum[c / d] : 0.0;
+          const int c = at.channel(i);
+          part[i] = c < at.C ? sum[c / d] : 0.0;
         }
     }
   }
 };
 
-// f(k, i) for every channel of a thread, with the activation's number as a constant.
-template <int NC, typename F>
+// f(i) for every channel of a thread, with the activation's number as a constant.
+template <typename F>
 __device__ __forceinline__ void each_channel(int act, F f) {
   auto all = [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) f(k, i, kind);
+    for (int i = 0; i < kPiece; ++i) f(i, kind);
   };
   if (act == kActSilu) {
     all(std::integral_constant<int, kActSilu>{});
@@ -350,229 +363,237 @@ __device__ __forceinline__ RowAt row_at(int64_t row, const ResidualArgs& a) {
   return r;
 }
 
-template <int TPR>
-constexpr int threads_of() {
-  return TPR < 256 ? 256 : TPR;
-}
+// A workgroup's rows: LDS of each, and which is this thread's.
+template <bool WIDE>
+struct Block {
+  Lane<WIDE> at;
+  Sums<WIDE> sums;
+  int rows, mine;
+  __device__ __forceinline__ Block(const ResidualArgs& a, int threads_row, int group_lanes, double* lds) {
+    const int C = a.G * a.d, waves = threads_row / 64;
+    const int row_lds = waves * 12 + (group_lanes == 0 ? C / (WIDE ? kPiece : 1) + a.G : 0);
+    rows = int(blockDim.x) / threads_row;
+    mine = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / threads_row);
+    at = {int(threadIdx.x) - mine * threads_row, C, threads_row};
+    sums = {lds + mine * row_lds, group_lanes, a.G, a.d, waves};
+  }
+};
 
-template <int TPR, int NC, bool WIDE>
-__global__ __launch_bounds__(threads_of<TPR>()) void residual_fwd_kernel(ResidualArgs a, int rows_each, int group_lanes) {
-  constexpr int kRows = threads_of<TPR>() / TPR;
-  using At = Lane<NC, WIDE, TPR>;
-  using S = Sums<NC, WIDE, TPR>;
+template <int MOST, bool WIDE>
+__global__ __launch_bounds__(MOST) void residual_fwd_kernel(ResidualArgs a, int threads_row, int rows_each, int group_lanes) {
+  using S = Sums<WIDE>;
   extern __shared__ double lds[];
   const int C = a.G * a.d;
-  const At at{int(threadIdx.x) % TPR, C};
-  const int mine = int(threadIdx.x) / TPR;
-  const int row_lds = S::kWaves * 12 + (group_lanes == 0 ? C / (WIDE ? kPiece : 1) + a.G : 0);
-  const S sums{lds + mine * row_lds, group_lanes, a.G, a.d};
+  const Block<WIDE> block(a, threads_row, group_lanes, lds);
+  const Lane<WIDE>& at = block.at;
+  const S& sums = block.sums;
+  const int mine = block.mine, rows = block.rows;
   const double inv_d = 1.0 / a.d, inv_C = 1.0 / C;
-  float aw[NC][kPiece], wn[NC][kPiece];
-  load_params<NC, WIDE, TPR>(a.alpha, 1.0f, at, aw);
-  load_params<NC, WIDE, TPR>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
+  float aw[kPiece], wn[kPiece];
+  load_params<WIDE>(a.alpha, 1.0f, at, aw);
+  load_params<WIDE>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
 #pragma unroll
-  for (int k = 0; k < NC; ++k)
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) aw[k][i] *= wn[k][i];
-  load_params<NC, WIDE, TPR>(a.pre_weight, 1.0f, at, wn);
-  const int64_t first = int64_t(blockIdx.x) * rows_each * kRows;
+    for (int i = 0; i < kPiece; ++i) aw[i] *= wn[i];
+  load_params<WIDE>(a.pre_weight, 1.0f, at, wn);
+  const int64_t first = int64_t(blockIdx.x) * rows + mine, stride = int64_t(gridDim.x) * rows;
+  Raw<WIDE> yr, hr, ur;
+  auto fetch = [&](const RowAt& r) {
+    yr.clear(), hr.clear(), ur.clear();
+    if (r.live && (!WIDE || at.channel(0) < C)) {
+      yr.fetch(a.y, a.bf16, r.row * a.y_row, at);
+      if (a.h) hr.fetch(a.h, a.stream_bf16, r.row * C, at);
+      if (a.gate) ur.fetch(a.gate, a.bf16, r.row * a.gate_row, at);
+    }
+  };
+  RowAt next = row_at(first, a);
+  fetch(next);
   for (int it = 0; it < rows_each; ++it) {
-    const RowAt r = row_at(first + int64_t(it) * kRows + mine, a);
-    float y[NC][kPiece], h[NC][kPiece];
-    load_row<NC, WIDE, TPR>(a.y, a.bf16, r.row * a.y_row, at, r.live, y);
-    load_row<NC, WIDE, TPR>(a.h, a.stream_bf16, r.row * C, at, r.live, h);
-    float u[NC][kPiece];
-    if (a.gate) load_row<NC, WIDE, TPR>(a.gate, a.bf16, r.row * a.gate_row, at, r.live, u);
+    const RowAt r = next;
+    float y[kPiece], h[kPiece], u[kPiece];
+    yr.values(a.bf16, y);
+    hr.values(a.stream_bf16, h);
+    ur.values(a.bf16, u);
+    if (it + 1 < rows_each) {
+      next = row_at(r.row + stride, a);
+      fetch(next);
+    }
     if (a.save) {
       const int64_t blocks = (C + kBlock - 1) / kBlock;
-      pack_row<NC, WIDE, TPR>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live, y);
-      if (a.gate) pack_row<NC, WIDE, TPR>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live, u);
+      pack_row<WIDE>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live, y);
+      if (a.gate) pack_row<WIDE>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live, u);
     }
     if (a.post) {
-      double part[NC][S::kParts];
+      double part[S::kParts];
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
+      for (int i = 0; i < S::kParts; ++i) part[i] = 0.0;
 #pragma unroll
-        for (int i = 0; i < S::kParts; ++i) part[k][i] = 0.0;
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) part[k][WIDE ? 0 : i] = __builtin_fma(double(y[k][i]), double(y[k][i]), part[k][WIDE ? 0 : i]);
-      }
+      for (int i = 0; i < kPiece; ++i) part[WIDE ? 0 : i] = __builtin_fma(double(y[i]), double(y[i]), part[WIDE ? 0 : i]);
       sums.groups(part, 0, it & 1, at);
+      Inverse inv;
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
-        Inverse inv;
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) {
-          if (!WIDE || i == 0) inv = inverse_root(__builtin_fma(part[k][WIDE ? 0 : i], inv_d, double(a.eps)));
-          y[k][i] = inv.times(y[k][i]);
-        }
+      for (int i = 0; i < kPiece; ++i) {
+        if (!WIDE || i == 0) inv = inverse_root(__builtin_fma(part[WIDE ? 0 : i], inv_d, double(a.eps)));
+        y[i] = inv.times(y[i]);
       }
     }
     if (a.gate) {
-      each_channel<NC>(a.act, [&](int k, int i, auto kind) { y[k][i] *= act_f32<kind()>(u[k][i]); });
+      each_channel(a.act, [&](int i, auto kind) { y[i] *= act_f32<kind()>(u[i]); });
     }
     double squares = 0.0, none = 0.0;
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        h[k][i] = __builtin_fmaf(aw[k][i], y[k][i], h[k][i]);
-        const double x = at.channel(k, i) < C ? double(h[k][i]) : 0.0;
+        h[i] = __builtin_fmaf(aw[i], y[i], h[i]);
+        const double x = at.channel(i) < C ? double(h[i]) : 0.0;
         squares = __builtin_fma(x, x, squares);
       }
-    if (r.live) store_row<NC, WIDE, TPR>(a.h_out, a.stream_bf16, r.row * C, at, h);
+    if (r.live) store_row<WIDE>(a.h_out, a.stream_bf16, r.row * C, at, h);
     if (a.pre) {
       sums.template row<false>(squares, none, 1, it & 1, at);
       const Inverse inv = inverse_root(__builtin_fma(squares, inv_C, double(a.eps)));
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) h[k][i] = inv.times(h[k][i]) * wn[k][i];
-      if (r.live) store_row<NC, WIDE, TPR>(a.n, a.bf16, r.row * C, at, h);
+        for (int i = 0; i < kPiece; ++i) h[i] = inv.times(h[i]) * wn[i];
+      if (r.live) store_row<WIDE>(a.n, a.bf16, r.row * C, at, h);
     }
   }
 }
 
-template <int TPR, int NC, bool WIDE>
-__global__ __launch_bounds__(threads_of<TPR>()) void residual_bwd_kernel(ResidualArgs a, int rows_each, int group_lanes, float* parts) {
-  constexpr int kThreads = threads_of<TPR>(), kRows = kThreads / TPR;
-  using At = Lane<NC, WIDE, TPR>;
-  using S = Sums<NC, WIDE, TPR>;
+template <int MOST, bool WIDE>
+__global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(ResidualArgs a, int threads_row, int rows_each, int group_lanes, float* parts) {
+  using S = Sums<WIDE>;
   extern __shared__ double lds[];
   const int C = a.G * a.d;
-  const At at{int(threadIdx.x) % TPR, C};
-  const int mine = int(threadIdx.x) / TPR;
-  const int row_lds = S::kWaves * 12 + (group_lanes == 0 ? C / (WIDE ? kPiece : 1) + a.G : 0);
-  const S sums{lds + mine * row_lds, group_lanes, a.G, a.d};
+  const Block<WIDE> block(a, threads_row, group_lanes, lds);
+  const Lane<WIDE>& at = block.at;
+  const S& sums = block.sums;
+  const int mine = block.mine, rows = block.rows;
   const double inv_d = 1.0 / a.d, inv_C = 1.0 / C;
-  float aw[NC][kPiece], wn[NC][kPiece], A[NC][kPiece], N[NC][kPiece];
-  load_params<NC, WIDE, TPR>(a.alpha, 1.0f, at, aw);
-  load_params<NC, WIDE, TPR>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
-#pragma unroll
-  for (int k = 0; k < NC; ++k)
+  float aw[kPiece], wn[kPiece], A[kPiece], N[kPiece];
+  load_params<WIDE>(a.alpha, 1.0f, at, aw);
+  load_params<WIDE>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
-      aw[k][i] *= wn[k][i];
-      A[k][i] = N[k][i] = 0.0f;
+      aw[i] *= wn[i];
+      A[i] = N[i] = 0.0f;
     }
-  load_params<NC, WIDE, TPR>(a.pre_weight, 1.0f, at, wn);
+  load_params<WIDE>(a.pre_weight, 1.0f, at, wn);
   const int64_t blocks = (C + kBlock - 1) / kBlock;
-  const int64_t first = int64_t(blockIdx.x) * rows_each * kRows;
-  for (int it = 0; it < rows_each; ++it) {
-    const RowAt r = row_at(first + int64_t(it) * kRows + mine, a);
-    float y[NC][kPiece], u[NC][kPiece], D[NC][kPiece];
-    if (a.save) {
-      unpack_row<NC, WIDE, TPR>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live, y);
-      if (a.gate_codes) unpack_row<NC, WIDE, TPR>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live, u);
-    } else {
-      load_row<NC, WIDE, TPR>(a.y, a.bf16, r.row * a.y_row, at, r.live, y);
-      if (a.gate) load_row<NC, WIDE, TPR>(a.gate, a.bf16, r.row * a.gate_row, at, r.live, u);
+  const int64_t first = int64_t(blockIdx.x) * rows + mine, stride = int64_t(gridDim.x) * rows;
+  Raw<WIDE> yr, ur, Dr, hr, tr;
+  const bool gated = a.gate || a.gate_codes;
+  auto fetch = [&](const RowAt& r) {
+    yr.clear(), ur.clear(), Dr.clear(), hr.clear(), tr.clear();
+    if (r.live && (!WIDE || at.channel(0) < C)) {
+      if (a.save) {
+        yr.fetch8(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at);
+        if (gated) ur.fetch8(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at);
+      } else {
+        yr.fetch(a.y, a.bf16, r.row * a.y_row, at);
+        if (gated) ur.fetch(a.gate, a.bf16, r.row * a.gate_row, at);
+      }
+      if (a.pre) {
+        hr.fetch(a.h_out, a.stream_bf16, r.row * C, at);
+        tr.fetch(a.dn, a.dn_bf16, r.row * C, at);
+      }
+      if (a.dh_out) Dr.fetch(a.dh_out, a.dh_out_bf16, r.row * C, at);
     }
-    load_row<NC, WIDE, TPR>(a.dh_out, a.dh_out_bf16, r.row * C, at, r.live, D);
+  };
+  for (int it = 0; it < rows_each; ++it) {
+    const RowAt r = row_at(first + int64_t(it) * stride, a);
+    fetch(r);
+    float y[kPiece], u[kPiece], D[kPiece], h[kPiece], t[kPiece];
+    if (a.save) {
+      yr.values8(y);
+      ur.values8(u);
+    } else {
+      yr.values(a.bf16, y);
+      ur.values(a.bf16, u);
+    }
+    Dr.values(a.dh_out_bf16, D);
+    hr.values(a.stream_bf16, h);
+    tr.values(a.dn_bf16, t);
     if (a.pre) {
-      float h[NC][kPiece], t[NC][kPiece];
-      load_row<NC, WIDE, TPR>(a.h_out, a.stream_bf16, r.row * C, at, r.live, h);
-      load_row<NC, WIDE, TPR>(a.dn, a.dn_bf16, r.row * C, at, r.live, t);
       double squares = 0.0, dots = 0.0;
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
         for (int i = 0; i < kPiece; ++i) {
-          const double x = double(h[k][i]);
+          const double x = double(h[i]);
           squares = __builtin_fma(x, x, squares);
-          dots = __builtin_fma(x, double(t[k][i] * wn[k][i]), dots);
+          dots = __builtin_fma(x, double(t[i] * wn[i]), dots);
         }
       sums.template row<true>(squares, dots, 0, it & 1, at);
       // (a row that is not there is zero throughout, whatever eps)
       const Inverse inv = inverse_root(r.live ? __builtin_fma(squares, inv_C, double(a.eps)) : 1.0);
       const float mean = float(dots * inv_C * double(inv.power) * double(inv.rest)), whole = inv.whole();
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
         for (int i = 0; i < kPiece; ++i) {
-          const float hhat = inv.times(h[k][i]);
-          N[k][i] = __builtin_fmaf(t[k][i], hhat, N[k][i]);
-          D[k][i] = __builtin_fmaf(whole, __builtin_fmaf(-hhat, mean, t[k][i] * wn[k][i]), D[k][i]);
+          const float hhat = inv.times(h[i]);
+          N[i] = __builtin_fmaf(t[i], hhat, N[i]);
+          D[i] = __builtin_fmaf(whole, __builtin_fmaf(-hhat, mean, t[i] * wn[i]), D[i]);
         }
     }
-    if (a.dh && r.inside) store_row<NC, WIDE, TPR>(a.dh, false, r.row * C, at, D);
+    if (a.dh && r.inside) store_row<WIDE>(a.dh, false, r.row * C, at, D);
     // D becomes D f, and dgate is made next to it
-    Inverse inv[NC][S::kParts];
+    Inverse inv[S::kParts];
     if (a.post) {
-      double part[NC][S::kParts];
+      double part[S::kParts];
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
+      for (int i = 0; i < S::kParts; ++i) part[i] = 0.0;
 #pragma unroll
-        for (int i = 0; i < S::kParts; ++i) part[k][i] = 0.0;
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) part[k][WIDE ? 0 : i] = __builtin_fma(double(y[k][i]), double(y[k][i]), part[k][WIDE ? 0 : i]);
-      }
+      for (int i = 0; i < kPiece; ++i) part[WIDE ? 0 : i] = __builtin_fma(double(y[i]), double(y[i]), part[WIDE ? 0 : i]);
       sums.groups(part, 1, it & 1, at);
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
+      for (int i = 0; i < S::kParts; ++i) inv[i] = inverse_root(r.live ? __builtin_fma(part[i], inv_d, double(a.eps)) : 1.0);
 #pragma unroll
-        for (int i = 0; i < S::kParts; ++i) inv[k][i] = inverse_root(r.live ? __builtin_fma(part[k][i], inv_d, double(a.eps)) : 1.0);
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) y[k][i] = inv[k][WIDE ? 0 : i].times(y[k][i]);
-      }
+      for (int i = 0; i < kPiece; ++i) y[i] = inv[WIDE ? 0 : i].times(y[i]);
     }
     if (a.dgate) {
-      each_channel<NC>(a.act, [&](int k, int i, auto kind) {
-        const float x = u[k][i];
-        u[k][i] = D[k][i] * aw[k][i] * y[k][i] * act_slope_f32<kind()>(x);
-        D[k][i] *= act_f32<kind()>(x);
+      each_channel(a.act, [&](int i, auto kind) {
+        const float x = u[i];
+        u[i] = D[i] * aw[i] * y[i] * act_slope_f32<kind()>(x);
+        D[i] *= act_f32<kind()>(x);
       });
-      if (r.inside) store_row<NC, WIDE, TPR>(a.dgate, false, r.row * C, at, u);
+      if (r.inside) store_row<WIDE>(a.dgate, false, r.row * C, at, u);
     }
-    double part[NC][S::kParts];
+    double part[S::kParts];
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
+    for (int i = 0; i < S::kParts; ++i) part[i] = 0.0;
 #pragma unroll
-      for (int i = 0; i < S::kParts; ++i) part[k][i] = 0.0;
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        A[k][i] = __builtin_fmaf(D[k][i], y[k][i], A[k][i]);
-        D[k][i] *= aw[k][i];
-        part[k][WIDE ? 0 : i] = __builtin_fma(double(D[k][i]), double(y[k][i]), part[k][WIDE ? 0 : i]);
-      }
+    for (int i = 0; i < kPiece; ++i) {
+      A[i] = __builtin_fmaf(D[i], y[i], A[i]);
+      D[i] *= aw[i];
+      part[WIDE ? 0 : i] = __builtin_fma(double(D[i]), double(y[i]), part[WIDE ? 0 : i]);
     }
     if (a.post) {
       sums.groups(part, 2, it & 1, at);
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-#pragma unroll
         for (int i = 0; i < kPiece; ++i) {
-          const Inverse& v = inv[k][WIDE ? 0 : i];
-          D[k][i] = v.whole() * __builtin_fmaf(-y[k][i], float(part[k][WIDE ? 0 : i] * inv_d), D[k][i]);
+          const Inverse& v = inv[WIDE ? 0 : i];
+          D[i] = v.whole() * __builtin_fmaf(-y[i], float(part[WIDE ? 0 : i] * inv_d), D[i]);
         }
     }
-    if (r.inside) store_row<NC, WIDE, TPR>(a.dy, false, r.row * C, at, D);
+    if (r.inside) store_row<WIDE>(a.dy, false, r.row * C, at, D);
   }
   if (!parts) return;
   // the workgroup's sums over its rows, in a fixed order: one row of partial sums, [C]
   // each of alpha, post_weight and pre_weight
   float* const out = parts + int64_t(blockIdx.x) * 3 * C;
-  float* const shared = reinterpret_cast<float*>(lds);   // [kThreads][kPiece]
+  float* const shared = reinterpret_cast<float*>(lds);   // [threads][kPiece]
   for (int which = 0; which < 2; ++which) {
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      __syncthreads();
+    for (int i = 0; i < kPiece; ++i) shared[threadIdx.x * kPiece + i] = which ? N[i] : A[i];
+    __syncthreads();
+    if (mine == 0) {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) shared[threadIdx.x * kPiece + i] = which ? N[k][i] : A[k][i];
-      __syncthreads();
-      if (mine == 0) {
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) {
-          const int c = at.channel(k, i);
-          if (c < C) {
-            double s = 0.0;
-            for (int m = 0; m < kRows; ++m) s += shared[(m * TPR + at.t) * kPiece + i];
-            if (which) {
-              out[2 * C + c] = float(s);
-            } else {
-              out[c] = float(s * (a.post && a.post_weight ? a.post_weight[c] : 1.0f));
-              out[C + c] = float(s * (a.alpha ? a.alpha[c] : 1.0f));
-            }
+      for (int i = 0; i < kPiece; ++i) {
+        const int c = at.channel(i);
+        if (c < C) {
+          double s = 0.0;
+          for (int m = 0; m < rows; ++m) s += shared[(m * threads_row + at.t) * kPiece + i];
+          if (which) {
+            out[2 * C + c] = float(s);
+          } else {
+            out[c] = float(s * (a.post && a.post_weight ? a.post_weight[c] : 1.0f));
+            out[C + c] = float(s * (a.alpha ? a.alpha[c] : 1.0f));
           }
         }
       }
@@ -588,14 +609,15 @@ bool wide(const ResidualArgs& a) {
 Shape shape_of(const ResidualArgs& a, bool bwd) {
   Shape s{};
   const int C = a.G * a.d;
-  s.nc = C <= 512 ? 1 : 2;
-  s.threads_row = 64;
-  while (s.threads_row * s.nc * kPiece < C) s.threads_row *= 2;
+  s.threads_row = (C + 64 * kPiece - 1) / (64 * kPiece) * 64;
   s.rows_block = std::max(1, 256 / s.threads_row);
   const int64_t rows = int64_t(a.B) * a.T;
-  const int64_t most = bwd ? 1024 : 2048;
+  // as many workgroups as the CUs hold at a time, at four waves a SIMD: one more round of a
+  // few costs what a whole one does (5555 rows of 2304, five waves each, gradients: 81 us
+  // with two a CU, 111 us with three)
+  const int64_t most = 256 * (4 / ((s.rows_block * s.threads_row / 64 + 3) / 4));
   const int64_t each = std::max<int64_t>(1, (rows + most * s.rows_block - 1) / (most * s.rows_block));
-  s.rows_each = int(bwd ? std::min<int64_t>(each, kRowsEach) : each);
+  s.rows_each = int(bwd ? std::min<int64_t>(each, rowsEach) : each);
   s.blocks = (rows + int64_t(s.rows_each) * s.rows_block - 1) / (int64_t(s.rows_each) * s.rows_block);
   const bool w = wide(a);
   const int lanes = a.d / kPiece;
@@ -606,19 +628,14 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   return s;
 }
 
-// Calls go(threads of a row, pieces, wide) with compile-time values.
+// Calls go(most threads, wide) with compile-time values: a workgroup of 1024 threads has 128
+// registers a thread, one of 256 up to 512.
 template <typename Go>
 hipError_t by_shape(const ResidualArgs& a, const Shape& s, Go go) {
-  using std::integral_constant;
-  auto by_wide = [&](auto tpr, auto nc) { return wide(a) ? go(tpr, nc, std::true_type{}) : go(tpr, nc, std::false_type{}); };
-  const integral_constant<int, 2> two{};
-  if (s.nc == 1) return by_wide(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  switch (s.threads_row) {
-    case 64: return by_wide(integral_constant<int, 64>{}, two);
-    case 128: return by_wide(integral_constant<int, 128>{}, two);
-    case 256: return by_wide(integral_constant<int, 256>{}, two);
-    default: return by_wide(integral_constant<int, 512>{}, two);
-  }
+  auto by_wide = [&](auto most) { return wide(a) ? go(most, std::true_type{}) : go(most, std::false_type{}); };
+  if (s.threads_row <= 256) return by_wide(std::integral_constant<int, 256>{});
+  if (s.threads_row <= 512) return by_wide(std::integral_constant<int, 512>{});
+  return by_wide(std::integral_constant<int, 1024>{});
 }
 
 template <typename Kernel>
@@ -631,11 +648,11 @@ hipError_t allow_lds(Kernel kernel, size_t lds) {
 
 hipError_t launch_residual_fwd(const ResidualArgs& a, hipStream_t st) {
   const Shape s = shape_of(a, false);
-  return by_shape(a, s, [&](auto tpr, auto nc, auto w) {
-    auto* const kernel = residual_fwd_kernel<tpr(), nc(), w()>;
+  return by_shape(a, s, [&](auto most, auto w) {
+    auto* const kernel = residual_fwd_kernel<most(), w()>;
     const hipError_t e = allow_lds(kernel, s.lds);
     if (e != hipSuccess) return e;
-    kernel<<<dim3(unsigned(s.blocks)), dim3(threads_of<tpr()>()), s.lds, st>>>(a, s.rows_each, s.group_lanes);
+    kernel<<<dim3(unsigned(s.blocks)), dim3(s.threads_row * s.rows_block), s.lds, st>>>(a, s.threads_row, s.rows_each, s.group_lanes);
     return hipGetLastError();
   });
 }
@@ -648,11 +665,11 @@ hipError_t launch_residual_bwd(const ResidualArgs& a, hipStream_t st) {
   const Shape s = shape_of(a, true);
   const bool params = a.dalpha || a.dpost_weight || a.dpre_weight;
   if (s.blocks > 0) {
-    const hipError_t e = by_shape(a, s, [&](auto tpr, auto nc, auto w) {
-      auto* const kernel = residual_bwd_kernel<tpr(), nc(), w()>;
+    const hipError_t e = by_shape(a, s, [&](auto most, auto w) {
+      auto* const kernel = residual_bwd_kernel<most(), w()>;
       const hipError_t e = allow_lds(kernel, s.lds);
       if (e != hipSuccess) return e;
-      kernel<<<dim3(unsigned(s.blocks)), dim3(threads_of<tpr()>()), s.lds, st>>>(a, s.rows_each, s.group_lanes, params ? a.workspace : nullptr);
+      kernel<<<dim3(unsigned(s.blocks)), dim3(s.threads_row * s.rows_block), s.lds, st>>>(a, s.threads_row, s.rows_each, s.group_lanes, params ? a.workspace : nullptr);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
