@@ -374,9 +374,15 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
       for (int t = 0; t < 2; ++t) {
         S[j][bb][t] = frag::zero4();
         const int f = 32 * bb + 16 * t + 4 * g;
-        if (OUT && from && f < DK)
+        if (OUT && from && f < DK) {
+          const float* p = from + f * s.sf + (16 * column(j) + c16) * s.sc;
+          if (s.sf == 1) {   // the transposed state
+            S[j][bb][t] = *reinterpret_cast<const f32x4*>(p);
+          } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[j][bb][t][r] = from[(f + r) * s.sf + (16 * column(j) + c16) * s.sc];
+            for (int r = 0; r < 4; ++r) S[j][bb][t][r] = p[r * s.sf];
+          }
+        }
       }
   auto keep = [&](float* to) {
     if (share > 0) return;
