@@ -31,7 +31,10 @@ namespace {
 
 constexpr int kPiece = 8;
 constexpr int kBlock = 32;        // channels of one step
-constexpr int rowsEach = 64;     // rows whose parts of the parameters' gradients one thread sums: float32 sums stay short
+// Bytes of gradients from which they are written past the last cache (256 MiB), which would
+// hold little of them for their reader.
+constexpr int64_t kPastCache = int64_t(128) << 20;
+constexpr int kRowsEach = 64;     // rows whose parts of the parameters' gradients one thread sums: float32 sums stay short
 
 // How rows and groups lie on threads.
 struct Shape {
@@ -473,8 +476,8 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
       A[i] = N[i] = 0.0f;
     }
   load_params<WIDE>(a.pre_weight, 1.0f, at, wn);
-  // (16384 rows of 768, 151 MB of gradients: 74 us past the cache, 79 us through it; 5555 of
-  // 2304: 71 us and 81 us)
+  // (with inputs from memory: gradients of 16384 rows of 768, 151 MB, 85.5 us past the cache,
+  // 87.5 us through it; with the forward ahead of them, 122 and 128 us)
   const bool past_cache = int64_t(a.B) * a.T * C * (1 + (a.dgate != nullptr) + (a.dh != nullptr)) * 4 > kPastCache;
   const int64_t blocks = (C + kBlock - 1) / kBlock;
   const int64_t first = int64_t(blockIdx.x) * rows + mine, stride = int64_t(gridDim.x) * rows;
@@ -617,7 +620,7 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   // with two a CU, 111 us with three)
   const int64_t most = 256 * (4 / ((s.rows_block * s.threads_row / 64 + 3) / 4));
   const int64_t each = std::max<int64_t>(1, (rows + most * s.rows_block - 1) / (most * s.rows_block));
-  s.rows_each = int(bwd ? std::min<int64_t>(each, rowsEach) : each);
+  s.rows_each = int(bwd ? std::min<int64_t>(each, kRowsEach) : each);
   s.blocks = (rows + int64_t(s.rows_each) * s.rows_block - 1) / (int64_t(s.rows_each) * s.rows_block);
   const bool w = wide(a);
   const int lanes = a.d / kPiece;
