@@ -52,6 +52,7 @@ template <bool WIDE>
 struct Lane {
   int t, C, threads;      // of the row's threads
   __device__ __forceinline__ int channel(int i) const { return WIDE ? t * kPiece + i : i * threads + t; }
+  __device__ __forceinline__ int inside() const { return min(t * kPiece, C - kPiece); }
 };
 
 template <bool WIDE, typename E>
@@ -86,14 +87,15 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < (WIDE ? 1 : kPiece); ++i) step[i] = 0;
   }
-  // (WIDE: by threads whose channels there are)
+  // WIDE: threads behind the row's end read its last piece, and `end` takes it back.  (A branch
+  // around the loads would be in the way of the sums over lanes behind them.)
   __device__ __forceinline__ void fetch(const void* p, bool bf16, int64_t at_row, const Lane<WIDE>& at) {
     if constexpr (WIDE) {
       if (bf16) {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const bf16_t*>(p) + at_row + at.channel(0));
+        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const bf16_t*>(p) + at_row + at.inside());
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
       } else {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at_row + at.channel(0));
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at_row + at.inside());
         const uint4 a = q[0], b = q[1];
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
@@ -108,7 +110,7 @@ struct Raw {
   }
   __device__ __forceinline__ void fetch8(const int8_t* codes, const uint8_t* steps, const Lane<WIDE>& at) {
     if constexpr (WIDE) {
-      const int c = at.channel(0);
+      const int c = at.inside();
       const uint2 a = *reinterpret_cast<const uint2*>(codes + c);
       w[0] = a.x, w[1] = a.y;
       step[0] = steps[c / kBlock];
@@ -118,6 +120,13 @@ struct Raw {
         const int c = at.channel(i);
         if (c < at.C) w[i] = uint8_t(codes[c]), step[i] = steps[c / kBlock];
       }
+    }
+  }
+  __device__ __forceinline__ void end(const Lane<WIDE>& at) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) w[i] = at.channel(0) < at.C ? w[i] : 0;
+      step[0] = at.channel(0) < at.C ? step[0] : 0;
     }
   }
   __device__ __forceinline__ void values(bool bf16, float (&v)[kPiece]) const {
@@ -399,7 +408,7 @@ __global__ __launch_bounds__(MOST) void residual_fwd_kernel(ResidualArgs a, int 
   Raw<WIDE> yr, hr, ur;
   auto fetch = [&](const RowAt& r) {
     yr.clear(), hr.clear(), ur.clear();
-    if (r.live && (!WIDE || at.channel(0) < C)) {
+    if (r.live) {
       yr.fetch(a.y, a.bf16, r.row * a.y_row, at);
       if (a.h) hr.fetch(a.h, a.stream_bf16, r.row * C, at);
       if (a.gate) ur.fetch(a.gate, a.bf16, r.row * a.gate_row, at);
@@ -410,6 +419,7 @@ __global__ __launch_bounds__(MOST) void residual_fwd_kernel(ResidualArgs a, int 
   for (int it = 0; it < rows_each; ++it) {
     const RowAt r = next;
     float y[kPiece], h[kPiece], u[kPiece];
+    yr.end(at), hr.end(at), ur.end(at);
     yr.values(a.bf16, y);
     hr.values(a.stream_bf16, h);
     ur.values(a.bf16, u);
@@ -485,7 +495,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
   const bool gated = a.gate || a.gate_codes;
   auto fetch = [&](const RowAt& r) {
     yr.clear(), ur.clear(), Dr.clear(), hr.clear(), tr.clear();
-    if (r.live && (!WIDE || at.channel(0) < C)) {
+    if (r.live) {
       if (a.save) {
         yr.fetch8(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at);
         if (gated) ur.fetch8(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at);
@@ -504,6 +514,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
     const RowAt r = row_at(first + int64_t(it) * stride, a);
     fetch(r);
     float y[kPiece], u[kPiece], D[kPiece], h[kPiece], t[kPiece];
+    yr.end(at), ur.end(at), Dr.end(at), hr.end(at), tr.end(at);
     if (a.save) {
       yr.values8(y);
       ur.values8(u);
