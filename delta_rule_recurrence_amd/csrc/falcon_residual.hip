@@ -372,6 +372,14 @@ __device__ __forceinline__ RowAt row_at(int64_t row, const ResidualArgs& a) {
   return r;
 }
 
+// Zeros behind a sequence's end, also where a weight is not finite.
+__device__ __forceinline__ void none_behind(const RowAt& r, float (&v)[kPiece]) {
+  if (!r.live) {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) v[i] = 0.0f;
+  }
+}
+
 // A workgroup's rows: LDS of each, and which is this thread's.
 template <bool WIDE>
 struct Block {
@@ -544,6 +552,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
           D[i] = __builtin_fmaf(whole, __builtin_fmaf(-hhat, mean, t[i] * wn[i]), D[i]);
         }
     }
+    none_behind(r, D);
     if (a.dh && r.inside) store_row<WIDE>(a.dh, false, r.row * C, at, D, past_cache);
     // D becomes D f, and dgate is made next to it
     Inverse inv[S::kParts];
@@ -565,6 +574,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
         u[i] = D[i] * aw[i] * y[i] * act_slope_f32<kind()>(x);
         D[i] *= act_f32<kind()>(x);
       });
+      none_behind(r, u);
       if (r.inside) store_row<WIDE>(a.dgate, false, r.row * C, at, u, past_cache);
     }
     double part[S::kParts];
@@ -584,6 +594,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
           D[i] = v.whole() * __builtin_fmaf(-y[i], float(part[WIDE ? 0 : i] * inv_d), D[i]);
         }
     }
+    none_behind(r, D);
     if (r.inside) store_row<WIDE>(a.dy, false, r.row * C, at, D, past_cache);
   }
   if (!parts) return;

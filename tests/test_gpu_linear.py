@@ -254,3 +254,14 @@ def test_empty_calls():
     g = fb.falcon_linear_bwd(z(0, 2, 5, 16), z(0, 2, 5, 16), z(0, 2, 5, 16), decay, z(0, 2, 5, 16), learned_decay=True)
     assert torch.all(g["dlog_decay"] == 0)
     assert fb.falcon_linear_step(z(0, 2, 16), z(0, 2, 16), z(0, 2, 16), decay, z(0, 2, 16, 16)).shape == (0, 2, 16)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dv", [16, 32, 64, 128])
+@pytest.mark.parametrize("dk", [16, 32, 64, 128])
+def test_every_pair_of_widths_on_padded_batches(dk, dv, dtype):
+    """Short chunks at both ends of the sweeps, whole ones between."""
+    d = inputs(3, 2, 197, dk, dv, IO[dtype], 200 + dk + dv)
+    layouts = ("rows", "heads", "rows") if (dk + dv) % 48 else ("heads", "rows", "heads")
+    check_forward(d, lengths=[197, 70, 3], layouts=layouts, what=f"{dk}x{dv} {dtype}")
+    check_backward(d, lengths=[197, 70, 3], layouts=layouts, what=f"{dk}x{dv} {dtype}")

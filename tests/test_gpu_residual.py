@@ -333,3 +333,14 @@ def test_sums_of_one_sign_over_many_tokens(C):
     g = fb.falcon_residual_bwd(one, None, dn, pre_norm=False, post_weight=w, alpha=w)
     for k in ("dalpha", "dpost_weight"):
         assert float((g[k].double() / want - 1).abs().max()) <= (64 + 2 + 8) * UNIT, k
+
+
+@pytest.mark.parametrize("d", [64, 33])
+def test_zeros_behind_the_ends_whatever_the_weights(d):
+    n, C = draws(47), 2 * d
+    y, h, dh, dn, gate = (n(2, 9, C).cuda() for _ in range(5))
+    w = torch.full((C,), float("inf"), device="cuda")
+    ends = torch.tensor([4, 0], dtype=torch.int32, device="cuda")
+    g = fb.falcon_residual_bwd(y, h, dh, dn, gate=gate, groups=2, post_weight=w, alpha=w, pre_weight=w, lengths=ends)
+    for k in ("dy", "dgate", "dh"):
+        assert torch.all(g[k][0, 4:] == 0) and torch.all(g[k][1] == 0)
