@@ -46,59 +46,77 @@ struct Shape {
 };
 
 // ---- rows; their types are met at run time (a uniform branch a tensor) ---------------
-// WIDE: pieces of 8 adjacent channels, one wide access each; else neighbours go to
-// neighbouring lanes, element by element.
-template <bool WIDE>
+// A thread has 8 channels: a piece of 8 neighbours, read and written at once at whatever
+// alignment, or, of rows shorter than that, one element after the other of those a thread
+// apart.  A row's last piece may be short: its thread reads the row's last 8 channels, and
+// those that are the thread's before it count as absent (rows of whole pieces by a form of
+// their own: 76 us against 86 for the gradients of 16384 rows of 768).  Where groups are whole
+// pieces (or the row) a piece is one part of a group's sum, else each of its channels is.
+enum Form { kElements, kChannels, kRagged, kPieces };
+constexpr bool by_piece(int form) { return form >= kRagged; }
+
+template <int FORM>
 struct Lane {
   int t, C, threads;      // of the row's threads
-  __device__ __forceinline__ int channel(int i) const { return WIDE ? t * kPiece + i : i * threads + t; }
-  __device__ __forceinline__ int inside() const { return min(t * kPiece, C - kPiece); }
+  // channels of a piece ahead of the thread's own; 8 or more behind the row's end
+  __device__ __forceinline__ int skip() const { return FORM == kPieces ? (t * kPiece < C ? 0 : kPiece) : max(t * kPiece - (C - kPiece), 0); }
+  __device__ __forceinline__ int channel(int i) const { return FORM == kElements ? i * threads + t : min(t * kPiece, C - kPiece) + i; }
+  __device__ __forceinline__ bool has(int i) const { return FORM == kElements ? channel(i) < C : i >= skip(); }
 };
 
-template <bool WIDE, typename E>
-__device__ __forceinline__ void load_typed(const E* p, const Lane<WIDE>& at, float missing, float (&v)[kPiece]) {
-  if constexpr (WIDE) {
+// Whatever the alignment of its elements, a piece is read and written in 16 bytes.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 __attribute__((aligned(2))) u32x4_at2;
+typedef u32x4 __attribute__((aligned(4))) u32x4_at4;
+typedef u32x2 __attribute__((aligned(1))) u32x2_at1;
+
+template <int FORM>
+__device__ __forceinline__ void load_params(const float* p, float missing, const Lane<FORM>& at, float (&v)[kPiece]) {
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] = missing;
-    const int c = at.channel(0);
-    if (c < at.C) load_vec<E, kPiece>(p + c, v);
+  for (int i = 0; i < kPiece; ++i) v[i] = missing;
+  if (!p) return;
+  if constexpr (FORM == kElements) {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) v[i] = at.has(i) ? p[at.channel(i)] : missing;
   } else {
+    const u32x4_at4* q = reinterpret_cast<const u32x4_at4*>(p + at.channel(0));
+    const u32x4 a = q[0], b = q[1];
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) {
-      const int c = at.channel(i);
-      v[i] = c < at.C ? io<E>::load(p, c) : missing;
-    }
+    for (int i = 0; i < kPiece; ++i) v[i] = at.has(i) ? __uint_as_float(i < 4 ? a[i] : b[i - 4]) : missing;
   }
 }
+
 // A step's byte is its float32 exponent field; 255, whose step is infinite, with codes of
 // zero stands for channels that were not all finite: they come back as NaN.
 __device__ __forceinline__ float step_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // A thread's channels of a row as they lie in memory: a row's loads are all under way before
 // the first is waited for, which conversions right behind each would do.
-template <bool WIDE>
+template <int FORM>
 struct Raw {
-  uint32_t w[kPiece];                 // packed where WIDE, else a channel each
-  uint32_t step[WIDE ? 1 : kPiece];   // of 8 bits
+  static constexpr bool kPiecewise = FORM != kElements;
+  uint32_t w[kPiece];                       // of a piece packed, else a channel each
+  uint32_t step[kPiecewise ? 1 : kPiece];   // of 8 bits
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) w[i] = 0;
 #pragma unroll
-    for (int i = 0; i < (WIDE ? 1 : kPiece); ++i) step[i] = 0;
+    for (int i = 0; i < (kPiecewise ? 1 : kPiece); ++i) step[i] = 0;
   }
-  // WIDE: threads behind the row's end read its last piece, and `end` takes it back.  (A branch
-  // around the loads would be in the way of the sums over lanes behind them.)
-  __device__ __forceinline__ void fetch(const void* p, bool bf16, int64_t at_row, const Lane<WIDE>& at) {
-    if constexpr (WIDE) {
+  // Threads behind a row's end read its last piece, too: a branch around the loads would be in
+  // the way of the sums over lanes behind them.
+  __device__ __forceinline__ void fetch(const void* p, bool bf16, int64_t at_row, const Lane<FORM>& at) {
+    if constexpr (kPiecewise) {
       if (bf16) {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const bf16_t*>(p) + at_row + at.inside());
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        const u32x4 a = *reinterpret_cast<const u32x4_at2*>(static_cast<const bf16_t*>(p) + at_row + at.channel(0));
+        w[0] = a[0], w[1] = a[1], w[2] = a[2], w[3] = a[3];
       } else {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at_row + at.inside());
-        const uint4 a = q[0], b = q[1];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        const u32x4_at4* q = reinterpret_cast<const u32x4_at4*>(static_cast<const float*>(p) + at_row + at.channel(0));
+        const u32x4 a = q[0], b = q[1];
+        w[0] = a[0], w[1] = a[1], w[2] = a[2], w[3] = a[3];
+        w[4] = b[0], w[5] = b[1], w[6] = b[2], w[7] = b[3];
       }
     } else {
 #pragma unroll
@@ -108,12 +126,11 @@ struct Raw {
       }
     }
   }
-  __device__ __forceinline__ void fetch8(const int8_t* codes, const uint8_t* steps, const Lane<WIDE>& at) {
-    if constexpr (WIDE) {
-      const int c = at.inside();
-      const uint2 a = *reinterpret_cast<const uint2*>(codes + c);
-      w[0] = a.x, w[1] = a.y;
-      step[0] = steps[c / kBlock];
+  __device__ __forceinline__ void fetch8(const int8_t* codes, const uint8_t* steps, const Lane<FORM>& at) {
+    if constexpr (kPiecewise) {
+      const u32x2 a = *reinterpret_cast<const u32x2_at1*>(codes + at.channel(0));
+      w[0] = a[0], w[1] = a[1];
+      step[0] = steps[min(at.t * kPiece, at.C - 1) / kBlock];
     } else {
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
@@ -122,72 +139,73 @@ struct Raw {
       }
     }
   }
-  __device__ __forceinline__ void end(const Lane<WIDE>& at) {
-    if constexpr (WIDE) {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) w[i] = at.channel(0) < at.C ? w[i] : 0;
-      step[0] = at.channel(0) < at.C ? step[0] : 0;
-    }
-  }
-  __device__ __forceinline__ void values(bool bf16, float (&v)[kPiece]) const {
+  // (absent channels: zero)
+  __device__ __forceinline__ uint32_t word(int k, const Lane<FORM>& at) const { return FORM == kPieces && at.skip() != 0 ? 0 : w[k]; }
+  __device__ __forceinline__ void values(bool bf16, const Lane<FORM>& at, float (&v)[kPiece]) const {
     if (bf16) {
 #pragma unroll
       for (int i = 0; i < kPiece; ++i)
-        v[i] = __uint_as_float(!WIDE ? w[i] << 16 : i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        v[i] = __uint_as_float(!kPiecewise ? w[i] << 16 : i % 2 ? word(i / 2, at) & 0xffff0000u : word(i / 2, at) << 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < kPiece; ++i) v[i] = __uint_as_float(word(i, at));
     }
+    none_absent(at, v);
   }
-  __device__ __forceinline__ void values8(float (&v)[kPiece]) const {
+  __device__ __forceinline__ void values8(const Lane<FORM>& at, float (&v)[kPiece]) const {
+    const float size = step_of(FORM == kPieces && at.skip() != 0 ? 0 : step[0]);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i)
-      v[i] = float(int8_t(WIDE ? w[i / 4] >> (8 * (i % 4)) : w[i])) * step_of(step[WIDE ? 0 : i]);
+      v[i] = kPiecewise ? float(int8_t(word(i / 4, at) >> (8 * (i % 4)))) * size : float(int8_t(w[i])) * step_of(step[kPiecewise ? 0 : i]);
+    none_absent(at, v);
+  }
+  __device__ __forceinline__ void none_absent(const Lane<FORM>& at, float (&v)[kPiece]) const {
+    if constexpr (kPiecewise && FORM != kPieces) {
+      int skip = at.skip();
+      asm volatile("" : "+v"(skip));   // (eight comparisons made ahead would fill the scalar registers)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) v[i] = i >= skip ? v[i] : 0.0f;
+    }
   }
 };
 
 // `past`: past the cache.
 __device__ __forceinline__ void store_piece(float* p, const float (&v)[kPiece], bool past) {
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  u32x4_at4* const q = reinterpret_cast<u32x4_at4*>(p);
+  const u32x4 a = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+  const u32x4 b = {__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
   if (past) {
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
-    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p) + 1);
+    asm volatile("");   // (else both ways become one, through the cache)
+    __builtin_nontemporal_store(a, q);
+    __builtin_nontemporal_store(b, q + 1);
+    asm volatile("");
   } else {
-    store_vec<float, kPiece>(p, v);
+    q[0] = a;
+    q[1] = b;
   }
 }
-__device__ __forceinline__ void store_piece(bf16_t* p, const float (&v)[kPiece], bool) { store_vec<bf16_t, kPiece>(p, v); }
-template <bool WIDE, typename E>
-__device__ __forceinline__ void store_typed(E* p, const Lane<WIDE>& at, const float (&v)[kPiece], bool past) {
-  if constexpr (WIDE) {
-    const int c = at.channel(0);
-    if (c < at.C) store_piece(p + c, v, past);
-  } else {
+__device__ __forceinline__ void store_piece(bf16_t* p, const float (&v)[kPiece], bool) {
+  *reinterpret_cast<u32x4_at2*>(p) = u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+}
+template <int FORM, typename E>
+__device__ __forceinline__ void store_typed(E* p, const Lane<FORM>& at, const float (&v)[kPiece], bool past) {
+  if (FORM != kElements && at.skip() == 0) {
+    store_piece(p + at.channel(0), v, past);
+  } else if (FORM == kElements || (FORM != kPieces && at.skip() < kPiece)) {
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
-      const int c = at.channel(i);
-      if (c < at.C) io<E>::store(p, c, v[i]);
+      if (at.has(i)) io<E>::store(p, at.channel(i), v[i]);
     }
   }
 }
-template <bool WIDE>
-__device__ __forceinline__ void store_row(void* p, bool bf16, int64_t at_row, const Lane<WIDE>& at, const float (&v)[kPiece], bool past = false) {
+template <int FORM>
+__device__ __forceinline__ void store_row(void* p, bool bf16, int64_t at_row, const Lane<FORM>& at, const float (&v)[kPiece], bool past = false) {
   if (bf16) {
-    store_typed<WIDE>(static_cast<bf16_t*>(p) + at_row, at, v, past);
+    store_typed<FORM>(static_cast<bf16_t*>(p) + at_row, at, v, past);
   } else {
-    store_typed<WIDE>(static_cast<float*>(p) + at_row, at, v, past);
+    store_typed<FORM>(static_cast<float*>(p) + at_row, at, v, past);
   }
 }
-template <bool WIDE>
-__device__ __forceinline__ void load_params(const float* p, float missing, const Lane<WIDE>& at, float (&v)[kPiece]) {
-  if (p) {
-    load_typed<WIDE>(p, at, missing, v);
-  } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[i] = missing;
-  }
-}
-
 // ---- 8 bits ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t step_byte(uint32_t largest) {
   if (largest >= 0x7f800000u) return 255;
@@ -203,24 +221,30 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-template <bool WIDE>
-__device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const Lane<WIDE>& at, bool on, const float (&v)[kPiece]) {
-  if constexpr (WIDE) {
+template <int FORM>
+__device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const Lane<FORM>& at, bool on, const float (&v)[kPiece]) {
+  if constexpr (FORM != kElements) {
     uint32_t largest = 0;
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) largest = max(largest, magnitude(v[i]));
     const uint32_t byte = step_byte(lanes_max<kBlock / kPiece>(largest));
     const float inverse = byte == 255 ? 0.0f : step_of(254 - byte);
-    uint32_t w[2] = {0, 0};
+    u32x2 w = {0, 0};
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
       const int code = byte == 255 ? 0 : int(__builtin_rintf(v[i] * inverse));
       w[i / 4] |= (uint32_t(code) & 255u) << (8 * (i % 4));
     }
-    const int c = at.channel(0);
-    if (on && c < at.C) {
-      *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
-      if (c % kBlock == 0) steps[c / kBlock] = uint8_t(byte);
+    if (on && at.skip() < kPiece) {
+      if (FORM == kPieces || at.skip() == 0) {
+        *reinterpret_cast<u32x2_at1*>(codes + at.channel(0)) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) {
+          if (at.has(i)) codes[at.channel(i)] = int8_t(w[i / 4] >> (8 * (i % 4)));
+        }
+      }
+      if (at.t % (kBlock / kPiece) == 0) steps[at.t / (kBlock / kPiece)] = uint8_t(byte);
     }
   } else {
 #pragma unroll
@@ -269,19 +293,19 @@ __device__ __forceinline__ Inverse inverse_root(double m) {
   return {__builtin_amdgcn_ldexpf(1.0f, first), __builtin_amdgcn_ldexpf(__builtin_amdgcn_rsqf(f), half - first)};
 }
 
-// The sums of one row over its groups.  `mine`: this thread's part, of each of its
-// pieces (WIDE) or channels.  The result is in place: each piece's (channel's) group's sum.
+// The sums of one row over its groups, of each thread's parts.  The result is in place: each
+// part's group's sum.
 // Every thread of the workgroup takes part.
-template <bool WIDE>
+template <int FORM>
 struct Sums {
-  static constexpr int kParts = WIDE ? 1 : kPiece;
+  static constexpr int kParts = by_piece(FORM) ? 1 : kPiece;
   double* lds;            // of this row: [3 slots][2 turns][2 sums][waves], then [items + G] where groups go through it
   int lanes, G, d, waves; // Shape::group_lanes; the row's waves
 
   // One sum over the row, or two at once.  Rounds with the same `slot` must have another barrier
   // between them; `turn` alternates.
   template <bool BOTH>
-  __device__ __forceinline__ void row(double& a, double& b, int slot, int turn, const Lane<WIDE>& at) const {
+  __device__ __forceinline__ void row(double& a, double& b, int slot, int turn, const Lane<FORM>& at) const {
     a = lanes_sum(a, 64);
     if constexpr (BOTH) b = lanes_sum(b, 64);
     if (waves > 1) {
@@ -299,7 +323,7 @@ struct Sums {
       }
     }
   }
-  __device__ __forceinline__ void groups(double (&part)[kParts], int slot, int turn, const Lane<WIDE>& at) const {
+  __device__ __forceinline__ void groups(double (&part)[kParts], int slot, int turn, const Lane<FORM>& at) const {
     if (lanes < 0) {
       double all = 0.0, none = 0.0;
 #pragma unroll
@@ -307,19 +331,18 @@ struct Sums {
       row<false>(all, none, slot, turn, at);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) part[i] = all;
-    } else if (WIDE && lanes > 0) {
+    } else if (by_piece(FORM) && lanes > 0) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) part[i] = lanes_sum(part[i], lanes);
     } else {
-      constexpr int kUnit = WIDE ? kPiece : 1;
+      constexpr int kUnit = by_piece(FORM) ? kPiece : 1;
       const int items = at.C / kUnit, each = d / kUnit;
       double* const item = lds + 12 * waves;
       double* const sum = item + items;
       __syncthreads();    // the last round's sums have been read
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          const int c = at.channel(i);
-          if (c < at.C) item[c / kUnit] = part[i];
+          if (at.has(i)) item[at.channel(i) / kUnit] = part[i];
         }
       __syncthreads();
       // a wave a group at a time
@@ -332,8 +355,7 @@ struct Sums {
       __syncthreads();
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          const int c = at.channel(i);
-          part[i] = c < at.C ? sum[c / d] : 0.0;
+          part[i] = at.has(i) ? sum[at.channel(i) / d] : 0.0;
         }
     }
   }
@@ -381,14 +403,14 @@ __device__ __forceinline__ void none_behind(const RowAt& r, float (&v)[kPiece]) 
 }
 
 // A workgroup's rows: LDS of each, and which is this thread's.
-template <bool WIDE>
+template <int FORM>
 struct Block {
-  Lane<WIDE> at;
-  Sums<WIDE> sums;
+  Lane<FORM> at;
+  Sums<FORM> sums;
   int rows, mine;
   __device__ __forceinline__ Block(const ResidualArgs& a, int threads_row, int group_lanes, double* lds) {
     const int C = a.G * a.d, waves = threads_row / 64;
-    const int row_lds = waves * 12 + (group_lanes == 0 ? C / (WIDE ? kPiece : 1) + a.G : 0);
+    const int row_lds = waves * 12 + (group_lanes == 0 ? C / (by_piece(FORM) ? kPiece : 1) + a.G : 0);
     rows = int(blockDim.x) / threads_row;
     mine = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / threads_row);
     at = {int(threadIdx.x) - mine * threads_row, C, threads_row};
@@ -396,24 +418,24 @@ struct Block {
   }
 };
 
-template <int MOST, bool WIDE>
-__global__ __launch_bounds__(MOST) void residual_fwd_kernel(ResidualArgs a, int threads_row, int rows_each, int group_lanes) {
-  using S = Sums<WIDE>;
+template <int MOST, int FORM>
+__global__ __launch_bounds__(MOST, (FORM == kElements ? 2 : 4)) void residual_fwd_kernel(ResidualArgs a, int threads_row, int rows_each, int group_lanes) {
+  using S = Sums<FORM>;
   extern __shared__ double lds[];
   const int C = a.G * a.d;
-  const Block<WIDE> block(a, threads_row, group_lanes, lds);
-  const Lane<WIDE>& at = block.at;
+  const Block<FORM> block(a, threads_row, group_lanes, lds);
+  const Lane<FORM>& at = block.at;
   const S& sums = block.sums;
   const int mine = block.mine, rows = block.rows;
   const double inv_d = 1.0 / a.d, inv_C = 1.0 / C;
   float aw[kPiece], wn[kPiece];
-  load_params<WIDE>(a.alpha, 1.0f, at, aw);
-  load_params<WIDE>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
+  load_params<FORM>(a.alpha, 1.0f, at, aw);
+  load_params<FORM>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) aw[i] *= wn[i];
-  load_params<WIDE>(a.pre_weight, 1.0f, at, wn);
+  load_params<FORM>(a.pre_weight, 1.0f, at, wn);
   const int64_t first = int64_t(blockIdx.x) * rows + mine, stride = int64_t(gridDim.x) * rows;
-  Raw<WIDE> yr, hr, ur;
+  Raw<FORM> yr, hr, ur;
   auto fetch = [&](const RowAt& r) {
     yr.clear(), hr.clear(), ur.clear();
     if (r.live) {
@@ -427,30 +449,29 @@ __global__ __launch_bounds__(MOST) void residual_fwd_kernel(ResidualArgs a, int 
   for (int it = 0; it < rows_each; ++it) {
     const RowAt r = next;
     float y[kPiece], h[kPiece], u[kPiece];
-    yr.end(at), hr.end(at), ur.end(at);
-    yr.values(a.bf16, y);
-    hr.values(a.stream_bf16, h);
-    ur.values(a.bf16, u);
+    yr.values(a.bf16, at, y);
+    hr.values(a.stream_bf16, at, h);
+    ur.values(a.bf16, at, u);
     if (it + 1 < rows_each) {
       next = row_at(r.row + stride, a);
       fetch(next);
     }
     if (a.save) {
       const int64_t blocks = (C + kBlock - 1) / kBlock;
-      pack_row<WIDE>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live, y);
-      if (a.gate) pack_row<WIDE>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live, u);
+      pack_row<FORM>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live, y);
+      if (a.gate) pack_row<FORM>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live, u);
     }
     if (a.post) {
       double part[S::kParts];
 #pragma unroll
       for (int i = 0; i < S::kParts; ++i) part[i] = 0.0;
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) part[WIDE ? 0 : i] = __builtin_fma(double(y[i]), double(y[i]), part[WIDE ? 0 : i]);
+      for (int i = 0; i < kPiece; ++i) part[by_piece(FORM) ? 0 : i] = __builtin_fma(double(y[i]), double(y[i]), part[by_piece(FORM) ? 0 : i]);
       sums.groups(part, 0, it & 1, at);
       Inverse inv;
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        if (!WIDE || i == 0) inv = inverse_root(__builtin_fma(part[WIDE ? 0 : i], inv_d, double(a.eps)));
+        if (!by_piece(FORM) || i == 0) inv = inverse_root(__builtin_fma(part[by_piece(FORM) ? 0 : i], inv_d, double(a.eps)));
         y[i] = inv.times(y[i]);
       }
     }
@@ -461,45 +482,46 @@ __global__ __launch_bounds__(MOST) void residual_fwd_kernel(ResidualArgs a, int 
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
         h[i] = __builtin_fmaf(aw[i], y[i], h[i]);
-        const double x = at.channel(i) < C ? double(h[i]) : 0.0;
+        // (absent groups of zeros are not finite with eps = 0)
+        const double x = (by_piece(FORM) ? at.skip() < kPiece : at.has(i)) ? double(h[i]) : 0.0;
         squares = __builtin_fma(x, x, squares);
       }
-    if (r.live) store_row<WIDE>(a.h_out, a.stream_bf16, r.row * C, at, h);
+    if (r.live) store_row<FORM>(a.h_out, a.stream_bf16, r.row * C, at, h);
     if (a.pre) {
       sums.template row<false>(squares, none, 1, it & 1, at);
       const Inverse inv = inverse_root(__builtin_fma(squares, inv_C, double(a.eps)));
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) h[i] = inv.times(h[i]) * wn[i];
-      if (r.live) store_row<WIDE>(a.n, a.bf16, r.row * C, at, h);
+      if (r.live) store_row<FORM>(a.n, a.bf16, r.row * C, at, h);
     }
   }
 }
 
-template <int MOST, bool WIDE>
-__global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(ResidualArgs a, int threads_row, int rows_each, int group_lanes, float* parts) {
-  using S = Sums<WIDE>;
+template <int MOST, int FORM>
+__global__ __launch_bounds__(MOST, (by_piece(FORM) ? 4 : FORM == kChannels ? 3 : 2)) void residual_bwd_kernel(ResidualArgs a, int threads_row, int rows_each, int group_lanes, float* parts) {
+  using S = Sums<FORM>;
   extern __shared__ double lds[];
   const int C = a.G * a.d;
-  const Block<WIDE> block(a, threads_row, group_lanes, lds);
-  const Lane<WIDE>& at = block.at;
+  const Block<FORM> block(a, threads_row, group_lanes, lds);
+  const Lane<FORM>& at = block.at;
   const S& sums = block.sums;
   const int mine = block.mine, rows = block.rows;
   const double inv_d = 1.0 / a.d, inv_C = 1.0 / C;
   float aw[kPiece], wn[kPiece], A[kPiece], N[kPiece];
-  load_params<WIDE>(a.alpha, 1.0f, at, aw);
-  load_params<WIDE>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
+  load_params<FORM>(a.alpha, 1.0f, at, aw);
+  load_params<FORM>(a.post ? a.post_weight : nullptr, 1.0f, at, wn);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
       aw[i] *= wn[i];
       A[i] = N[i] = 0.0f;
     }
-  load_params<WIDE>(a.pre_weight, 1.0f, at, wn);
+  load_params<FORM>(a.pre_weight, 1.0f, at, wn);
   // (with inputs from memory: gradients of 16384 rows of 768, 151 MB, 85.5 us past the cache,
   // 87.5 us through it; with the forward ahead of them, 122 and 128 us)
   const bool past_cache = int64_t(a.B) * a.T * C * (1 + (a.dgate != nullptr) + (a.dh != nullptr)) * 4 > kPastCache;
   const int64_t blocks = (C + kBlock - 1) / kBlock;
   const int64_t first = int64_t(blockIdx.x) * rows + mine, stride = int64_t(gridDim.x) * rows;
-  Raw<WIDE> yr, ur, Dr, hr, tr;
+  Raw<FORM> yr, ur, Dr, hr, tr;
   const bool gated = a.gate || a.gate_codes;
   auto fetch = [&](const RowAt& r) {
     yr.clear(), ur.clear(), Dr.clear(), hr.clear(), tr.clear();
@@ -522,17 +544,16 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
     const RowAt r = row_at(first + int64_t(it) * stride, a);
     fetch(r);
     float y[kPiece], u[kPiece], D[kPiece], h[kPiece], t[kPiece];
-    yr.end(at), ur.end(at), Dr.end(at), hr.end(at), tr.end(at);
     if (a.save) {
-      yr.values8(y);
-      ur.values8(u);
+      yr.values8(at, y);
+      ur.values8(at, u);
     } else {
-      yr.values(a.bf16, y);
-      ur.values(a.bf16, u);
+      yr.values(a.bf16, at, y);
+      ur.values(a.bf16, at, u);
     }
-    Dr.values(a.dh_out_bf16, D);
-    hr.values(a.stream_bf16, h);
-    tr.values(a.dn_bf16, t);
+    Dr.values(a.dh_out_bf16, at, D);
+    hr.values(a.stream_bf16, at, h);
+    tr.values(a.dn_bf16, at, t);
     if (a.pre) {
       double squares = 0.0, dots = 0.0;
 #pragma unroll
@@ -553,7 +574,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
         }
     }
     none_behind(r, D);
-    if (a.dh && r.inside) store_row<WIDE>(a.dh, false, r.row * C, at, D, past_cache);
+    if (a.dh && r.inside) store_row<FORM>(a.dh, false, r.row * C, at, D, past_cache);
     // D becomes D f, and dgate is made next to it
     Inverse inv[S::kParts];
     if (a.post) {
@@ -561,12 +582,12 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
 #pragma unroll
       for (int i = 0; i < S::kParts; ++i) part[i] = 0.0;
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) part[WIDE ? 0 : i] = __builtin_fma(double(y[i]), double(y[i]), part[WIDE ? 0 : i]);
+      for (int i = 0; i < kPiece; ++i) part[by_piece(FORM) ? 0 : i] = __builtin_fma(double(y[i]), double(y[i]), part[by_piece(FORM) ? 0 : i]);
       sums.groups(part, 1, it & 1, at);
 #pragma unroll
       for (int i = 0; i < S::kParts; ++i) inv[i] = inverse_root(r.live ? __builtin_fma(part[i], inv_d, double(a.eps)) : 1.0);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) y[i] = inv[WIDE ? 0 : i].times(y[i]);
+      for (int i = 0; i < kPiece; ++i) y[i] = inv[by_piece(FORM) ? 0 : i].times(y[i]);
     }
     if (a.dgate) {
       each_channel(a.act, [&](int i, auto kind) {
@@ -575,7 +596,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
         D[i] *= act_f32<kind()>(x);
       });
       none_behind(r, u);
-      if (r.inside) store_row<WIDE>(a.dgate, false, r.row * C, at, u, past_cache);
+      if (r.inside) store_row<FORM>(a.dgate, false, r.row * C, at, u, past_cache);
     }
     double part[S::kParts];
 #pragma unroll
@@ -584,18 +605,18 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
     for (int i = 0; i < kPiece; ++i) {
       A[i] = __builtin_fmaf(D[i], y[i], A[i]);
       D[i] *= aw[i];
-      part[WIDE ? 0 : i] = __builtin_fma(double(D[i]), double(y[i]), part[WIDE ? 0 : i]);
+      part[by_piece(FORM) ? 0 : i] = __builtin_fma(double(D[i]), double(y[i]), part[by_piece(FORM) ? 0 : i]);
     }
     if (a.post) {
       sums.groups(part, 2, it & 1, at);
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) {
-          const Inverse& v = inv[WIDE ? 0 : i];
-          D[i] = v.whole() * __builtin_fmaf(-y[i], float(part[WIDE ? 0 : i] * inv_d), D[i]);
+          const Inverse& v = inv[by_piece(FORM) ? 0 : i];
+          D[i] = v.whole() * __builtin_fmaf(-y[i], float(part[by_piece(FORM) ? 0 : i] * inv_d), D[i]);
         }
     }
     none_behind(r, D);
-    if (r.inside) store_row<WIDE>(a.dy, false, r.row * C, at, D, past_cache);
+    if (r.inside) store_row<FORM>(a.dy, false, r.row * C, at, D, past_cache);
   }
   if (!parts) return;
   // the workgroup's sums over its rows, in a fixed order: one row of partial sums, [C]
@@ -611,7 +632,7 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
         const int c = at.channel(i);
-        if (c < C) {
+        if (at.has(i)) {
           double s = 0.0;
           for (int m = 0; m < rows; ++m) s += shared[(m * threads_row + at.t) * kPiece + i];
           if (which) {
@@ -626,9 +647,11 @@ __global__ __launch_bounds__(MOST, (WIDE ? 4 : 2)) void residual_bwd_kernel(Resi
   }
 }
 
-bool wide(const ResidualArgs& a) {
-  const int64_t C = int64_t(a.G) * a.d;
-  return C % kPiece == 0 && (!a.post || a.d % kPiece == 0) && (!a.y || a.y_row % kPiece == 0) && (!a.gate || a.gate_row % kPiece == 0);
+Form form_of(const ResidualArgs& a) {
+  const int C = a.G * a.d;
+  if (C < kPiece) return kElements;
+  if (a.post && a.G > 1 && a.d % kPiece != 0) return kChannels;
+  return C % kPiece == 0 ? kPieces : kRagged;
 }
 
 Shape shape_of(const ResidualArgs& a, bool bwd) {
@@ -637,27 +660,33 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   s.threads_row = (C + 64 * kPiece - 1) / (64 * kPiece) * 64;
   s.rows_block = std::max(1, 256 / s.threads_row);
   const int64_t rows = int64_t(a.B) * a.T;
-  // as many workgroups as the CUs hold at a time, at four waves a SIMD: one more round of a
+  // as many workgroups as the CUs hold at a time, at three or four waves a SIMD: one more round of a
   // few costs what a whole one does (5555 rows of 2304, five waves each, gradients: 81 us
   // with two a CU, 111 us with three)
-  const int64_t most = 256 * (4 / ((s.rows_block * s.threads_row / 64 + 3) / 4));
+  const int simd = bwd && !by_piece(form_of(a)) ? 3 : 4, waves = (s.rows_block * s.threads_row / 64 + 3) / 4;
+  const int64_t most = 256 * std::max(1, simd / waves);
   const int64_t each = std::max<int64_t>(1, (rows + most * s.rows_block - 1) / (most * s.rows_block));
   s.rows_each = int(bwd ? std::min<int64_t>(each, kRowsEach) : each);
   s.blocks = (rows + int64_t(s.rows_each) * s.rows_block - 1) / (int64_t(s.rows_each) * s.rows_block);
-  const bool w = wide(a);
+  const bool pieces = by_piece(form_of(a));
   const int lanes = a.d / kPiece;
-  s.group_lanes = a.G == 1 || !a.post ? -1 : w && lanes <= 64 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-  const size_t row = size_t(s.threads_row / 64) * 12 + (s.group_lanes == 0 ? size_t(w ? C / kPiece : C) + a.G : 0);
+  s.group_lanes = a.G == 1 || !a.post ? -1 : pieces && lanes <= 64 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const size_t row = size_t(s.threads_row / 64) * 12 + (s.group_lanes == 0 ? size_t(pieces ? C / kPiece : C) + a.G : 0);
   s.lds = s.rows_block * row * sizeof(double);
   if (bwd) s.lds = std::max(s.lds, size_t(s.rows_block) * s.threads_row * kPiece * sizeof(float));
   return s;
 }
 
-// Calls go(most threads, wide) with compile-time values: a workgroup of 1024 threads has 128
+// Calls go(most threads, form) with compile-time values: a workgroup of 1024 threads has 128
 // registers a thread, one of 256 up to 512.
 template <typename Go>
 hipError_t by_shape(const ResidualArgs& a, const Shape& s, Go go) {
-  auto by_wide = [&](auto most) { return wide(a) ? go(most, std::true_type{}) : go(most, std::false_type{}); };
+  using std::integral_constant;
+  if (form_of(a) == kElements) return go(integral_constant<int, 256>{}, integral_constant<int, kElements>{});
+  auto by_wide = [&](auto most) {
+    if (form_of(a) == kPieces) return go(most, integral_constant<int, kPieces>{});
+    return form_of(a) == kRagged ? go(most, integral_constant<int, kRagged>{}) : go(most, integral_constant<int, kChannels>{});
+  };
   if (s.threads_row <= 256) return by_wide(std::integral_constant<int, 256>{});
   if (s.threads_row <= 512) return by_wide(std::integral_constant<int, 512>{});
   return by_wide(std::integral_constant<int, 1024>{});
@@ -673,8 +702,8 @@ hipError_t allow_lds(Kernel kernel, size_t lds) {
 
 hipError_t launch_residual_fwd(const ResidualArgs& a, hipStream_t st) {
   const Shape s = shape_of(a, false);
-  return by_shape(a, s, [&](auto most, auto w) {
-    auto* const kernel = residual_fwd_kernel<most(), w()>;
+  return by_shape(a, s, [&](auto most, auto form) {
+    auto* const kernel = residual_fwd_kernel<most(), form()>;
     const hipError_t e = allow_lds(kernel, s.lds);
     if (e != hipSuccess) return e;
     kernel<<<dim3(unsigned(s.blocks)), dim3(s.threads_row * s.rows_block), s.lds, st>>>(a, s.threads_row, s.rows_each, s.group_lanes);
@@ -690,8 +719,8 @@ hipError_t launch_residual_bwd(const ResidualArgs& a, hipStream_t st) {
   const Shape s = shape_of(a, true);
   const bool params = a.dalpha || a.dpost_weight || a.dpre_weight;
   if (s.blocks > 0) {
-    const hipError_t e = by_shape(a, s, [&](auto most, auto w) {
-      auto* const kernel = residual_bwd_kernel<most(), w()>;
+    const hipError_t e = by_shape(a, s, [&](auto most, auto form) {
+      auto* const kernel = residual_bwd_kernel<most(), form()>;
       const hipError_t e = allow_lds(kernel, s.lds);
       if (e != hipSuccess) return e;
       kernel<<<dim3(unsigned(s.blocks)), dim3(s.threads_row * s.rows_block), s.lds, st>>>(a, s.threads_row, s.rows_each, s.group_lanes, params ? a.workspace : nullptr);

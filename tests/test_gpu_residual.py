@@ -344,3 +344,29 @@ def test_zeros_behind_the_ends_whatever_the_weights(d):
     g = fb.falcon_residual_bwd(y, h, dh, dn, gate=gate, groups=2, post_weight=w, alpha=w, pre_weight=w, lengths=ends)
     for k in ("dy", "dgate", "dh"):
         assert torch.all(g[k][0, 4:] == 0) and torch.all(g[k][1] == 0)
+
+
+@pytest.mark.parametrize("C", [2, 7, 8, 9, 15, 17, 31, 65, 505, 511, 513, 519, 521, 1025, 2049, 4095, 4099])
+@pytest.mark.parametrize("post,io", [(True, "bf16"), (False, "f32")])
+def test_widths_around_a_piece(C, post, io):
+    """Rows whose last piece of 8 channels is short, alone in a wave among them, in place."""
+    n, T = draws(80 + C), 5
+    y, gate = n(2, T, C, dtype=IO[io]), n(2, T, C, dtype=IO[io])
+    h, dh, dn = n(2, T, C), n(2, T, C), n(2, T, C)
+    w = n(C, scale=0.3, mean=1.0)
+    a = dict(post_norm=post, eps=1e-5)
+    p = dict(post_weight=w if post else None, alpha=w, pre_weight=w)
+    stream = h.cuda()
+    h_out, normed, kept = fb.falcon_residual_fwd(y.cuda(), stream, gate=gate.cuda(), h_out=stream, save=True,
+                                                 **{k: cuda(v) for k, v in p.items()}, **a)
+    want, n_want = ro.residual_forward(f64(y), f64(h), gate=f64(gate), **{k: f64(v) for k, v in p.items()}, **a)
+    close(h_out, want, C, "h_out")
+    close(normed, n_want, 2 * C, "n")
+    into = dh.cuda()
+    g = fb.falcon_residual_bwd(None, h_out, into, dn.cuda(), saved=kept, grads={"dh": into}, **{k: cuda(v) for k, v in p.items()}, **a)
+    ref = ro.residual_backward(ro.eight_bits(f64(y)), f64(h_out), f64(dh), f64(dn), gate=ro.eight_bits(f64(gate)),
+                               **{k: f64(v) for k, v in p.items()}, **a)
+    for k in ("dh", "dgate", *(() if post and C == 2 else ("dy",))):
+        close(g[k], ref[k], 4 * C, k)
+    for k in ("dalpha", "dpre_weight", *(("dpost_weight",) if post else ())):
+        close(g[k], ref[k], 2 * T + 2 * C, k)
