@@ -121,6 +121,7 @@ struct LinearArgs {
   float scale;
   HeadSteps q_at, k_at, v_at, o_at;   // o_at: of o or dO; gradients lie as their inputs, dense
   HeadSteps dqk_at, dv_at;
+  bool zero_behind;
   const void* q;
   const void* k;
   const void* v;
@@ -168,6 +169,7 @@ struct LinearSweep {
   int sf, sc;              // a state's element (f, c) lies at f sf + c sc
   float read, write;       // factors of what is read and of what is written
   bool rev, bf16;
+  bool clear;              // zeros in the output rows behind the sequences' ends
 };
 // What the tiles of one or two sweeps of the same sizes add to a state; the outputs of one;
 // the gradients' sweeps, dv's first.  By the width of the (first sweep's) keys.
@@ -183,6 +185,7 @@ FALCON_LINEAR_OF(128)
 
 struct ResidualArgs {
   int B, T, G, d;
+  bool zero_behind;
   bool bf16, stream_bf16;
   int act;
   bool post, pre;

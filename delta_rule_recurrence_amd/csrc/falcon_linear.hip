@@ -264,28 +264,6 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
   }
 }
 
-// ---- zeros behind the sequences' ends --------------------------------------------------------
-struct Tail {
-  float* out;
-  HeadSteps at;
-  int d;
-};
-// A workgroup a head and a sequence's rows from its end on, all gradients.
-__global__ __launch_bounds__(256) void tails_kernel(Tail x, Tail y, Tail z, const int32_t* lengths, int H, int T) {
-  const int64_t bh = blockIdx.x;
-  const int b = int(bh / H), h = int(bh % H);
-  const int len = tokens_of(lengths, b, T);
-  auto clear = [&](const Tail& p) {
-    const int each = p.d / 4;
-    float* out = p.out + b * p.at.b + h * p.at.h;
-    for (int64_t i = threadIdx.x; i < int64_t(T - len) * each; i += 256)
-      *reinterpret_cast<float4*>(out + (len + i / each) * p.at.t + i % each * 4) = make_float4(0, 0, 0, 0);
-  };
-  clear(x);
-  clear(y);
-  clear(z);
-}
-
 // Workspace of the gradients: S slots, R slots (one more), rows of partial sums.
 struct BwdLayout {
   int64_t S, R, parts;   // floats
@@ -327,6 +305,7 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
   s.q = a.q; s.q_at = a.q_at;
   s.out = a.o; s.out_at = a.o_at;
   s.read = a.scale;
+  s.clear = a.zero_behind && a.lengths;
   return FALCON_BY_KEYS(outputs, a.dk, s, st);
 }
 
@@ -364,6 +343,7 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   r.sf = a.dv; r.sc = 1;
   r.slots = R; r.slots_each = t.tiles + 1; r.slot0 = 1;
   r.rev = true;
+  s.clear = r.clear = a.lengths != nullptr;
   r.write = a.scale;
   FALCON_TRY(FALCON_BY_KEYS(sums, a.dk, s, &r, st));
   const Carry back{R, t.tiles + 1, 1, a.dS_T, a.dS0, true};
@@ -390,11 +370,6 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   dq.read = a.scale;
   dq.out = a.dq; dq.out_at = a.dqk_at;
   FALCON_TRY(FALCON_BY_KEYS(gradients, a.dk, dv, dk, dq, st));
-  if (a.lengths) {
-    tails_kernel<<<dim3(unsigned(t.heads)), dim3(256), 0, st>>>({a.dq, a.dqk_at, a.dk}, {a.dk_out, a.dqk_at, a.dk}, {a.dv_out, a.dv_at, a.dv},
-                                                                a.lengths, a.H, a.T);
-    FALCON_TRY(hipGetLastError());
-  }
   if (a.dlog_decay) {
     const DecayGrad d{a.q, a.k, a.q_at, a.k_at, a.dqk_at, a.dq, a.dk_out, S, R, a.lengths, parts, a.H, a.T, a.dk, t.tiles, t.chunks, size};
     const dim3 grid(unsigned(t.heads * t.tiles));

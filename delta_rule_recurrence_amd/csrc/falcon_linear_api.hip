@@ -44,6 +44,7 @@ falcon_status check_linear(const falcon_linear_problem* p, bool step, LinearArgs
   a->B = p->B; a->H = p->H; a->T = T; a->dk = p->dk; a->dv = p->dv;
   a->bf16 = p->io_dtype == FALCON_BF16;
   a->scale = p->scale;
+  a->zero_behind = p->zero_behind != 0;
   a->q_at = steps(qk_heads, p->q_row, p->H, T, p->dk);
   a->k_at = steps(qk_heads, p->k_row, p->H, T, p->dk);
   a->v_at = steps(v_heads, p->v_row, p->H, T, p->dv);

@@ -267,10 +267,11 @@ template <typename IO, int DK, int DV>
 constexpr int waves() {
   return (sizeof(IO) == 4 && (DK >= 128 || DV >= 128)) || (DK >= 128 && DV >= 128) ? 8 : 4;
 }
-// Waves of a SIMD that the registers are to leave room for: as many as LDS does.
-template <int DK, int DV>
+// Waves of a SIMD that the registers leave room for: three (168 registers)
+// where LDS has room for three workgroups.
+template <typename IO, int DK, int DV>
 constexpr int waves_simd() {
-  return 2;
+  return sizeof(IO) == 2 && DK <= 64 && DV <= 64 ? 3 : 2;
 }
 // LDS: keys, values and, for outputs, queries and scores as fragments.
 template <typename IO, typename O, int DK, int DV, bool OUT>
@@ -328,6 +329,14 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   const int k_step = int(s.k_at.t), v_step = int(s.v_at.t), q_step = int(s.q_at.t), out_step = int(s.out_at.t);
   float* const slot = s.slots ? s.slots + (bh * s.slots_each + s.slot0 + tile) * (DK * DV) : nullptr;
 
+  if constexpr (OUT) {
+    if (s.clear) {   // the tile's rows behind the sequence's end
+      constexpr int kEach = DV * int(sizeof(O)) / 16;
+      const int from = max(len - first, 0), to = min(s.T - first, s.chunks * kChunk);
+      for (int64_t i = tid; i < int64_t(to - from) * kEach; i += kThreads)
+        *reinterpret_cast<uint4*>(out + (from + i / kEach) * s.out_at.t + i % kEach * (16 / int(sizeof(O)))) = make_uint4(0, 0, 0, 0);
+    }
+  }
   Rows<IO, DK, kThreads> kr;
   Rows<IO, DV, kThreads> vr;
   Exact qr[OUT ? kB : 1];
@@ -590,7 +599,7 @@ struct Sweeps2 {
   uint32_t blocks;     // of each
 };
 template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN>
-__global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<DK, DV>())) void sweep_kernel(Sweeps2 p) {
+__global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<IO, DK, DV>())) void sweep_kernel(Sweeps2 p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const uint32_t which = blockIdx.x >= p.blocks ? 1 : 0;
   sweep<IO, O, DK, DV, OUT, WRITTEN>(p.s[which], blockIdx.x - which * p.blocks, lds);
@@ -604,7 +613,7 @@ struct Sweeps3 {
   uint32_t blocks;
 };
 template <typename IO, int DK, int DV>
-__global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<DK, DV>())) void gradients_kernel(Sweeps3 p) {
+__global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<IO, DK, DV>())) void gradients_kernel(Sweeps3 p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const uint32_t which = blockIdx.x / 8 % 3, block = blockIdx.x / 24 * 8 + blockIdx.x % 8;
   if (block >= p.blocks) return;

@@ -222,7 +222,7 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 template <int FORM>
-__device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const Lane<FORM>& at, bool on, const float (&v)[kPiece]) {
+__device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const Lane<FORM>& at, bool on, bool live, const float (&v)[kPiece]) {
   if constexpr (FORM != kElements) {
     uint32_t largest = 0;
 #pragma unroll
@@ -244,7 +244,7 @@ __device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const La
           if (at.has(i)) codes[at.channel(i)] = int8_t(w[i / 4] >> (8 * (i % 4)));
         }
       }
-      if (at.t % (kBlock / kPiece) == 0) steps[at.t / (kBlock / kPiece)] = uint8_t(byte);
+      if (at.t % (kBlock / kPiece) == 0) steps[at.t / (kBlock / kPiece)] = live ? uint8_t(byte) : 0;
     }
   } else {
 #pragma unroll
@@ -253,7 +253,7 @@ __device__ __forceinline__ void pack_row(int8_t* codes, uint8_t* steps, const La
       const int c = at.channel(i);
       if (on && c < at.C) {
         codes[c] = byte == 255 ? int8_t(0) : int8_t(int(__builtin_rintf(v[i] * step_of(254 - byte))));
-        if (c % kBlock == 0) steps[c / kBlock] = uint8_t(byte);
+        if (c % kBlock == 0) steps[c / kBlock] = live ? uint8_t(byte) : 0;
       }
     }
   }
@@ -458,8 +458,8 @@ __global__ __launch_bounds__(MOST, (FORM == kElements ? 2 : 4)) void residual_fw
     }
     if (a.save) {
       const int64_t blocks = (C + kBlock - 1) / kBlock;
-      pack_row<FORM>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live, y);
-      if (a.gate) pack_row<FORM>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live, u);
+      pack_row<FORM>(a.y_codes + r.row * C, a.y_steps + r.row * blocks, at, r.live || (r.inside && a.zero_behind), r.live, y);
+      if (a.gate) pack_row<FORM>(a.gate_codes + r.row * C, a.gate_steps + r.row * blocks, at, r.live || (r.inside && a.zero_behind), r.live, u);
     }
     if (a.post) {
       double part[S::kParts];
@@ -486,13 +486,16 @@ __global__ __launch_bounds__(MOST, (FORM == kElements ? 2 : 4)) void residual_fw
         const double x = (by_piece(FORM) ? at.skip() < kPiece : at.has(i)) ? double(h[i]) : 0.0;
         squares = __builtin_fma(x, x, squares);
       }
-    if (r.live) store_row<FORM>(a.h_out, a.stream_bf16, r.row * C, at, h);
+    const bool cleared = r.inside && !r.live && a.zero_behind;
+    if (cleared) none_behind(r, h);
+    if (r.live || cleared) store_row<FORM>(a.h_out, a.stream_bf16, r.row * C, at, h);
     if (a.pre) {
       sums.template row<false>(squares, none, 1, it & 1, at);
       const Inverse inv = inverse_root(__builtin_fma(squares, inv_C, double(a.eps)));
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) h[i] = inv.times(h[i]) * wn[i];
-      if (r.live) store_row<FORM>(a.n, a.bf16, r.row * C, at, h);
+      none_behind(r, h);
+      if (r.live || cleared) store_row<FORM>(a.n, a.bf16, r.row * C, at, h);
     }
   }
 }

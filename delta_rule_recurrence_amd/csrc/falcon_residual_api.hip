@@ -33,6 +33,7 @@ falcon_status check_residual(const falcon_residual_problem* p, bool y_rows, bool
   a->post = p->post_norm != 0;
   a->pre = p->pre_norm != 0;
   a->eps = p->eps;
+  a->zero_behind = p->zero_behind != 0;
   a->y_row = p->y_row; a->gate_row = p->gate_row;
   return FALCON_OK;
 }

@@ -53,14 +53,15 @@ class FalconLinearProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("T", ctypes.c_int32), ("dk", ctypes.c_int32),
                 ("dv", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("qk_heads", ctypes.c_int32),
                 ("v_heads", ctypes.c_int32), ("o_heads", ctypes.c_int32), ("scale", ctypes.c_float),
-                ("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64)]
+                ("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64),
+                ("zero_behind", ctypes.c_int32)]
 
 
 class FalconResidualProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("G", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("io_dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
                 ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32), ("eps", ctypes.c_float),
-                ("y_row", ctypes.c_int64), ("gate_row", ctypes.c_int64)]
+                ("y_row", ctypes.c_int64), ("gate_row", ctypes.c_int64), ("zero_behind", ctypes.c_int32)]
 
 
 class FalconSavedPointers(ctypes.Structure):
@@ -916,7 +917,8 @@ def falcon_linear_fwd(q, k, v, log_decay, *, scale=1.0, S0=None, lengths=None, q
     _expect_bytes(workspace, "workspace", 0 if need == ctypes.c_size_t(-1).value else need, dev)
     with _on_stream(dev, stream) as st:
         if o is None:
-            o = _new(out, io, dev, lengths)
+            o = torch.empty(out, dtype=io, device=dev)
+            p.zero_behind = 1
         if S_T is None and return_state:
             S_T = torch.empty(state, dtype=torch.float32, device=dev)
         workspace, have = _workspace(workspace, need, dev)
@@ -1058,13 +1060,16 @@ def falcon_residual_fwd(y, h=None, *, gate=None, activation="silu", groups=1, po
     p = FalconResidualProblem(B, T, G, C // G, DTYPES[io], DTYPES[stream_type], act, int(bool(post_norm)),
                               int(bool(pre_norm)), eps, y_row, gate_row)
     with _on_stream(dev, stream) as st:
+        # rows behind the ends: cleared by the call, but where some outputs are given and others not
+        p.zero_behind = h_out is None and n is None and saved is None
+        fill = None if p.zero_behind else lengths
         if h_out is None:
-            h_out = _new(rows, stream_type, dev, lengths) if lengths is not None or h is None else torch.empty_like(h)
+            h_out = _new(rows, stream_type, dev, fill) if fill is not None or h is None else torch.empty_like(h)
         if n is None and pre_norm:
-            n = _new(rows, io, dev, lengths) if lengths is not None or stream_type != io else torch.empty_like(h_out)
+            n = _new(rows, io, dev, fill) if fill is not None or stream_type != io else torch.empty_like(h_out)
         if saved is None and save:
             parts = 2 if gate is not None else 1
-            saved = FalconSaved(*(_new(shape, dtype, dev, lengths) for _ in range(parts)
+            saved = FalconSaved(*(_new(shape, dtype, dev, fill) for _ in range(parts)
                                   for shape, dtype in ((rows, torch.int8), ((B, T, (C + 31) // 32), torch.uint8))))
         at = None if saved is None else ctypes.byref(_saved(saved, rows, gate is not None, dev))
         _check(load_library().falcon_residual_fwd(

@@ -315,8 +315,9 @@ size_t falcon_bwd_workspace_bytes(const falcon_problem* p);
  *    interleave among inputs, but an output may not lie between them.
  *  - lengths, [B] int32 or NULL, gives each sequence's number of tokens
  *    (clamped to [0, T]).  Rows behind a sequence's end are never read.
- *    Forward calls leave the output rows behind it as they were and take the
- *    carried state at the end; backward calls write zero gradients there.
+ *    Forward calls leave the output rows behind it as they were (where a problem
+ *    has zero_behind and it is not 0: clear them) and take the carried state at
+ *    the end; backward calls write zero gradients there.
  *  - Parameters (weights, biases, A, D) and states of the scan are float32;
  *    gradients are float32.  Incoming gradients dy have dy_dtype, a
  *    falcon_dtype of its own (falcon_bwd_chunked gives float32 ones).
@@ -552,6 +553,7 @@ typedef struct {
   int32_t qk_heads, v_heads, o_heads;   /* 0: rows, 1: heads */
   float scale;                          /* finite */
   int64_t q_row, k_row, v_row;
+  int32_t zero_behind;                  /* zeros in the rows of o behind the ends  */
 } falcon_linear_problem;
 
 falcon_status falcon_linear_fwd(const falcon_linear_problem* p, const void* q, const void* k,
@@ -623,6 +625,7 @@ typedef struct {
   int32_t post_norm, pre_norm;
   float eps;                  /* >= 0, finite */
   int64_t y_row, gate_row;
+  int32_t zero_behind;        /* zeros in the forward's rows behind the ends    */
 } falcon_residual_problem;
 
 typedef struct {

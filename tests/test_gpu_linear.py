@@ -265,3 +265,14 @@ def test_every_pair_of_widths_on_padded_batches(dk, dv, dtype):
     layouts = ("rows", "heads", "rows") if (dk + dv) % 48 else ("heads", "rows", "heads")
     check_forward(d, lengths=[197, 70, 3], layouts=layouts, what=f"{dk}x{dv} {dtype}")
     check_backward(d, lengths=[197, 70, 3], layouts=layouts, what=f"{dk}x{dv} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,layout", [(2100, "rows"), (2100, "heads"), (40, "heads")])
+def test_allocated_outputs_are_zero_behind_the_ends(T, layout, dtype):
+    """Through the tiles and their short ends, and in tiles that no token is left for."""
+    d = inputs(4, 3, T, 16, 16, IO[dtype], 230)
+    lengths = [T, T // 2 + 3, 0, 1]
+    o, _ = check_forward(d, lengths=lengths, layouts=(layout,) * 3, what=f"{T} {layout} {dtype}")
+    for b, n in enumerate(lengths):
+        assert torch.all(heads(o, layout, 3)[b, :, n:] == 0)

@@ -370,3 +370,21 @@ def test_widths_around_a_piece(C, post, io):
         close(g[k], ref[k], 4 * C, k)
     for k in ("dalpha", "dpre_weight", *(("dpost_weight",) if post else ())):
         close(g[k], ref[k], 2 * T + 2 * C, k)
+
+
+@pytest.mark.parametrize("C", [96, 77, 5])
+def test_outputs_given_and_allocated_on_padded_batches(C):
+    """Those given stay behind the ends, those allocated are zero there."""
+    n = draws(51)
+    y, h = n(3, 20, C).cuda(), n(3, 20, C).cuda()
+    ends = torch.tensor([20, 7, 0], dtype=torch.int32, device="cuda")
+    behind = torch.arange(20, device="cuda")[None] >= ends[:, None]
+    want = fb.falcon_residual_fwd(y, h, gate=y, lengths=ends, save=True)
+    assert all(torch.all(t[behind] == 0) for t in (*want[:2], *want[2]))
+    for given in ("h_out", "n", "saved"):
+        seven = lambda t: torch.full_like(t, 7)  # noqa: E731
+        into = {"h_out": seven(h), "n": seven(y), "saved": fb.FalconSaved(*(seven(t) for t in want[2]))}[given]
+        h_out, normed, kept = fb.falcon_residual_fwd(y, h, gate=y, lengths=ends, save=True, **{given: into})
+        for name, got, ref in (("h_out", h_out, want[0]), ("n", normed, want[1]), *(("saved", a, b) for a, b in zip(kept, want[2]))):
+            assert torch.equal(got[~behind], ref[~behind])
+            assert torch.all(got[behind] == (7 if name == given else 0)), (given, name)
