@@ -1005,6 +1005,12 @@ def _saved(saved, rows, gated, dev):
     return FalconSavedPointers(*(_ref(t) if gated or i < 2 else None for i, t in enumerate(saved)))
 
 
+def _incoming(t, name, rows, dev):
+    """``_expect`` for a gradient of either type, quick where all is well."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in DTYPES and _is(t, rows, t.dtype, dev)):
+        _expect(t, name, rows, tuple(DTYPES), dev)
+
+
 def _residual_weights(C, dev, **weights):
     for name, t in weights.items():
         if t is not None:
@@ -1067,11 +1073,15 @@ def falcon_residual_fwd(y, h=None, *, gate=None, activation="silu", groups=1, po
             h_out = _new(rows, stream_type, dev, fill) if fill is not None or h is None else torch.empty_like(h)
         if n is None and pre_norm:
             n = _new(rows, io, dev, fill) if fill is not None or stream_type != io else torch.empty_like(h_out)
-        if saved is None and save:
-            parts = 2 if gate is not None else 1
-            saved = FalconSaved(*(_new(shape, dtype, dev, fill) for _ in range(parts)
-                                  for shape, dtype in ((rows, torch.int8), ((B, T, (C + 31) // 32), torch.uint8))))
-        at = None if saved is None else ctypes.byref(_saved(saved, rows, gate is not None, dev))
+        at = None
+        if saved is not None:
+            at = ctypes.byref(_saved(saved, rows, gate is not None, dev))
+        elif save:
+            pair = [_new(rows, torch.int8, dev, fill), _new((B, T, (C + 31) // 32), torch.uint8, dev, fill)]
+            if gate is not None:
+                pair += [torch.empty_like(t) if fill is None else torch.zeros_like(t) for t in pair]
+            saved = FalconSaved(*pair)
+            at = ctypes.byref(FalconSavedPointers(*map(_ref, saved)))
         _check(load_library().falcon_residual_fwd(
             ctypes.byref(p), _ref(y), _ref(gate), _ref(h), _ref(post_weight), _ref(alpha), _ref(pre_weight),
             _ref(lengths), _ref(h_out), _ref(n), at, st))
@@ -1117,10 +1127,11 @@ def falcon_residual_bwd(y, h_out, dh_out, dn=None, *, gate=None, saved=None, act
     if pre_norm:
         stream_type = _io_dtype(h_out, "h_out") if isinstance(h_out, torch.Tensor) else None
         _need(h_out, "h_out", rows, stream_type, dev)
-        _expect(dn, "dn", rows, tuple(DTYPES), dev)
+        _incoming(dn, "dn", rows, dev)
     elif h_out is not None or dn is not None:
         raise ValueError("h_out, dn: there is no pre_norm")
-    _expect(dh_out, "dh_out", rows, tuple(DTYPES), dev, optional=True)
+    if dh_out is not None:
+        _incoming(dh_out, "dh_out", rows, dev)
     _residual_weights(C, dev, post_weight=post_weight, alpha=alpha, pre_weight=pre_weight)
     _need(lengths, "lengths", (B,), torch.int32, dev, optional=True)
     shapes = {"dy": rows, "dgate": rows, "dh": rows, "dalpha": (C,), "dpost_weight": (C,), "dpre_weight": (C,)}
