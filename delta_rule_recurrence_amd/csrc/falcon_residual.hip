@@ -407,10 +407,10 @@ template <int FORM>
 struct Block {
   Lane<FORM> at;
   Sums<FORM> sums;
-  int rows, mine;
+  int rows, mine, row_lds;   // row_lds: doubles
   __device__ __forceinline__ Block(const ResidualArgs& a, int threads_row, int group_lanes, double* lds) {
     const int C = a.G * a.d, waves = threads_row / 64;
-    const int row_lds = waves * 12 + (group_lanes == 0 ? C / (by_piece(FORM) ? kPiece : 1) + a.G : 0);
+    row_lds = waves * 12 + (group_lanes == 0 ? C / (by_piece(FORM) ? kPiece : 1) + a.G : 0);
     rows = int(blockDim.x) / threads_row;
     mine = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / threads_row);
     at = {int(threadIdx.x) - mine * threads_row, C, threads_row};
@@ -519,6 +519,28 @@ __global__ __launch_bounds__(MOST, (by_piece(FORM) ? 4 : FORM == kChannels ? 3 :
       A[i] = N[i] = 0.0f;
     }
   load_params<FORM>(a.pre_weight, 1.0f, at, wn);
+  // Of pieces the weights wait in LDS, [4][threads of a row] of 16 bytes: their registers are
+  // what four waves a SIMD lack.
+  float4* const weights = reinterpret_cast<float4*>(lds + (rows * block.row_lds + 1) / 2 * 2) + at.t;
+  if constexpr (by_piece(FORM)) {
+    if (mine == 0) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        weights[q * threads_row] = make_float4(aw[4 * q], aw[4 * q + 1], aw[4 * q + 2], aw[4 * q + 3]);
+        weights[(2 + q) * threads_row] = make_float4(wn[4 * q], wn[4 * q + 1], wn[4 * q + 2], wn[4 * q + 3]);
+      }
+    }
+    __syncthreads();
+  }
+  auto weights_at = [&](int first, float (&v)[kPiece]) {
+    if constexpr (by_piece(FORM)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 x = weights[(first + q) * threads_row];
+        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+      }
+    }
+  };
   // (with inputs from memory: gradients of 16384 rows of 768, 151 MB, 85.5 us past the cache,
   // 87.5 us through it; with the forward ahead of them, 122 and 128 us)
   const bool past_cache = int64_t(a.B) * a.T * C * (1 + (a.dgate != nullptr) + (a.dh != nullptr)) * 4 > kPastCache;
@@ -558,6 +580,7 @@ __global__ __launch_bounds__(MOST, (by_piece(FORM) ? 4 : FORM == kChannels ? 3 :
     hr.values(a.stream_bf16, at, h);
     tr.values(a.dn_bf16, at, t);
     if (a.pre) {
+      weights_at(2, wn);
       double squares = 0.0, dots = 0.0;
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) {
@@ -578,6 +601,7 @@ __global__ __launch_bounds__(MOST, (by_piece(FORM) ? 4 : FORM == kChannels ? 3 :
     }
     none_behind(r, D);
     if (a.dh && r.inside) store_row<FORM>(a.dh, false, r.row * C, at, D, past_cache);
+    weights_at(0, aw);
     // D becomes D f, and dgate is made next to it
     Inverse inv[S::kParts];
     if (a.post) {
@@ -676,6 +700,7 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   s.group_lanes = a.G == 1 || !a.post ? -1 : pieces && lanes <= 64 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   const size_t row = size_t(s.threads_row / 64) * 12 + (s.group_lanes == 0 ? size_t(pieces ? C / kPiece : C) + a.G : 0);
   s.lds = s.rows_block * row * sizeof(double);
+  if (bwd && pieces) s.lds = (s.lds + 15) / 16 * 16 + size_t(s.threads_row) * 4 * sizeof(float4);   // the weights
   if (bwd) s.lds = std::max(s.lds, size_t(s.rows_block) * s.threads_row * kPiece * sizeof(float));
   return s;
 }
