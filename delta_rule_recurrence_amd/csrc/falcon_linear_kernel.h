@@ -275,10 +275,22 @@ constexpr int waves_simd() {
 }
 // LDS: keys, values and, for outputs, queries and scores as fragments.
 template <typename IO, typename O, int DK, int DV, bool OUT>
-constexpr int lds_bytes() {
+constexpr int lds_once() {
   const int terms = sizeof(O) == 2 ? 2 : 3;
   const int scores = 8 * 64 * (sizeof(IO) == 2 ? terms * 16 : 32);
   return Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes + (OUT ? kChunk * Stage<IO, DK>::kWidth * int(sizeof(IO)) + scores : 0);
+}
+// Two places in turn for what is read up to a chunk's end (the keys; without outputs the
+// values, too) save the barrier there, where as many workgroups fit a CU all the same.
+template <typename IO, typename O, int DK, int DV, bool OUT>
+constexpr bool in_turn() {
+  const int once = lds_once<IO, O, DK, DV, OUT>(), more = Stage<IO, DK>::kBytes + (OUT ? 0 : Stage<IO, DV>::kBytes);
+  const int room = waves_simd<IO, DK, DV>() * 4 / waves<IO, DK, DV>(), before = 160 * 1024 / once, after = 160 * 1024 / (once + more);
+  return after >= (before < room ? before : room);
+}
+template <typename IO, typename O, int DK, int DV, bool OUT>
+constexpr int lds_bytes() {
+  return lds_once<IO, O, DK, DV, OUT>() + (in_turn<IO, O, DK, DV, OUT>() ? Stage<IO, DK>::kBytes + (OUT ? 0 : Stage<IO, DV>::kBytes) : 0);
 }
 
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
@@ -301,8 +313,10 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   using Exact = typename Ops::Exact;
   using Split = typename Ops::Split;
 
-  IO* const ks = reinterpret_cast<IO*>(lds);
-  IO* const vs = reinterpret_cast<IO*>(lds + Stage<IO, DK>::kBytes);
+  constexpr bool kInTurn = in_turn<IO, O, DK, DV, OUT>();
+  char* const second = lds + lds_once<IO, O, DK, DV, OUT>();
+  IO* ks = reinterpret_cast<IO*>(lds);
+  IO* vs = reinterpret_cast<IO*>(lds + Stage<IO, DK>::kBytes);
   char* const qs = lds + Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes;   // [4][kB] fragments
   char* const ps = qs + kChunk * Stage<IO, DK>::kWidth * int(sizeof(IO)); // [4][2] fragments
 
@@ -414,7 +428,10 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
     return;
   }
   if constexpr (DK < 32) {
-    for (int i = tid; i < kChunk * kPk; i += kThreads) ks[i] = IO{};
+    for (int i = tid; i < kChunk * kPk; i += kThreads) {
+      ks[i] = IO{};
+      if constexpr (kInTurn) reinterpret_cast<IO*>(second)[i] = IO{};
+    }
     __syncthreads();
   }
   // Decays, as products of a factor of the four rows 4 g + r of a block of 16 and one of
@@ -457,6 +474,10 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   for (int step = 0; step < chunks; ++step) {
     const int c = chunk_at(step), n = tokens_in(c);
     const bool more = step + 1 < chunks;
+    if constexpr (kInTurn) {
+      ks = reinterpret_cast<IO*>(step % 2 ? second : lds);
+      if constexpr (!OUT) vs = reinterpret_cast<IO*>((step % 2 ? second : lds) + Stage<IO, DK>::kBytes);
+    }
     const int shift = shift_of(n);
     kr.store(ks, n, shift, tid);
     vr.store(vs, n, shift, tid);
@@ -584,7 +605,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           }
         }
     }
-    __syncthreads();
+    if constexpr (!kInTurn) __syncthreads();
   }
   if constexpr (OUT) {
     if (s.last) keep(s.last + bh * (DK * DV));
