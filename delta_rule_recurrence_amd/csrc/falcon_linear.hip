@@ -30,7 +30,9 @@ struct Tiles {
 
 Tiles cut(const LinearArgs& a) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
-  // tiles of a head for three workgroups a CU, or for the two that wide heads leave room for
+  // tiles of a head for three workgroups a CU, or for the two or one that wide heads leave room
+  // for (8 x 2048 x 12 x 64: 768 tiles 36 us of sweeps and sums, 1536 the same and 3 us more
+  // between them; 16384 x 12 x 128 x 128: 256 tiles 105 us in all, 512 114 us, 768 119 us)
   const int64_t all_tiles = a.dk * a.dv > 64 * 128 ? 256 : a.dk * a.dv > 64 * 64 ? 512 : 768;
   const int64_t want = std::max<int64_t>(1, all_tiles / std::max<int64_t>(heads, 1));   // (one more would take a round of its own)
   const int64_t chunks = std::max<int64_t>(1, (all + want - 1) / want);
@@ -125,7 +127,7 @@ LinearSweep sweep_base(const LinearArgs& a, const Tiles& t) {
 // ---- single tokens ---------------------------------------------------------------------
 // A workgroup a head, four columns of the state and every (threads / (dv / 4))-th row a
 // thread; the threads' parts of the read meet in LDS.  Bound by the state, read and
-// written once.
+// written once (512 x 12 x 128 x 128: 162 us from memory, 5.0 TB/s).
 template <typename IO>
 __global__ __launch_bounds__(256) void linear_step_kernel(const IO* __restrict__ q, int64_t q_row, const IO* __restrict__ k, int64_t k_row,
                                                           const IO* __restrict__ v, int64_t v_row, const float* __restrict__ log_decay,

@@ -30,6 +30,14 @@
 // bits each: two for results in bfloat16 (2^-17 of the operand is lost, against
 // 2^-9 in the result), three where they are float32 and for the state.  float32
 // inputs use the float32 matrix instruction throughout.
+//
+// What bounds it, at 8 x 2048 x 12 x 64 in bfloat16: outputs of a prompt 25 us for the 113 MB
+// that they move (4.6 TB/s, a copy's rate), sums 14 us for 63 MB, gradients 70 us for 330 MB.
+// At 128 x 128 a state fills the registers of eight waves, one workgroup a CU, whose products,
+// vector instructions and LDS reads follow one another (20, 29 and 27 % of the time).  The
+// state as an operand from registers, where it passed through LDS before, and rows of the
+// next chunk ahead: outputs 35 -> 29 us; factored decays, which leave registers for a third
+// workgroup: 29 -> 25 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -262,7 +270,8 @@ __device__ __forceinline__ float power(float log2_a, int n) {
 }
 
 // Waves of a workgroup: eight where what four hold would not fit their registers, float32
-// operands of 128 columns and states of 128 x 128.
+// operands of 128 columns and states of 128 x 128 (16384 x 12 in bfloat16: outputs 63 us,
+// four waves 72 us with 48 registers in memory; halves of the values apart 70 us).
 template <typename IO, int DK, int DV>
 constexpr int waves() {
   return (sizeof(IO) == 4 && (DK >= 128 || DV >= 128)) || (DK >= 128 && DV >= 128) ? 8 : 4;
@@ -313,6 +322,13 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   using Exact = typename Ops::Exact;
   using Split = typename Ops::Split;
 
+  // Where registers are left the reads of LDS for several products are issued ahead of the
+  // first one: by itself the compiler waits for each in turn (heads of 128 x 128: outputs of
+  // a prompt 63 -> 62 us, gradients 124 -> 121 us; narrower heads have no registers left).
+  constexpr bool kAhead = kWaves == 8 && sizeof(IO) == 2;
+  auto issued = [&]() {
+    if constexpr (kAhead) asm volatile("" ::: "memory");
+  };
   constexpr bool kInTurn = in_turn<IO, O, DK, DV, OUT>();
   char* const second = lds + lds_once<IO, O, DK, DV, OUT>();
   IO* ks = reinterpret_cast<IO*>(lds);
@@ -501,11 +517,20 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
         const int m = pair(x);
         if (!(s.rev ? m == 1 || rw < 2 : m == 0 || rw >= 2)) continue;   // all behind (before) these tokens
         f32x4 p[2];
+        auto keys = [&](int u, int bb) __attribute__((always_inline)) { return row_frag<kPk>(ks, 32 * m + 16 * u + c16, bb, g); };
+        Exact kf[kAhead ? 2 : 1][kB];
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int bb = 0; bb < kB; ++bb) kf[u][bb] = keys(u, bb);
+          issued();
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           p[u] = frag::zero4();
 #pragma unroll
-          for (int bb = 0; bb < kB; ++bb) p[u] = mma(row_frag<kPk>(ks, 32 * m + 16 * u + c16, bb, g), qf[bb], p[u]);
+          for (int bb = 0; bb < kB; ++bb) p[u] = mma(kAhead ? kf[kAhead ? u : 0][bb] : keys(u, bb), qf[bb], p[u]);
           const int block = 2 * m + u;
           if (block == rw) {
             // (a product with the mask's zero would keep what is not finite)
@@ -528,18 +553,27 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) o[x][j] = frag::zero4();
       if (makes) {
+        Exact q[kAhead ? 2 : 1][kRows];
+        auto queries = [&](int bb, Exact (&to)[kRows]) __attribute__((always_inline)) {
+#pragma unroll
+          for (int x = 0; x < kRows; ++x) get(qs, tokens(x) * kB + bb, l, to[x]);
+        };
+        if constexpr (kAhead) queries(0, q[0]);
 #pragma unroll
         for (int bb = 0; bb < kB; ++bb) {
+          if constexpr (kAhead) {
+            if (bb + 1 < kB) queries(bb + 1, q[(bb + 1) % 2]);
+            issued();
+          } else {
+            queries(bb, q[0]);
+          }
           Split sf[kOwn];
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) split(S[j][bb][0], S[j][bb][1], sf[j]);
 #pragma unroll
-          for (int x = 0; x < kRows; ++x) {
-            Exact q;
-            get(qs, tokens(x) * kB + bb, l, q);
+          for (int x = 0; x < kRows; ++x)
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) o[x][j] = mma(sf[j], q, o[x][j]);
-          }
+            for (int j = 0; j < kOwn; ++j) o[x][j] = mma(sf[j], q[kAhead ? bb % 2 : 0][x], o[x][j]);
         }
       }
     }
@@ -551,19 +585,29 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
       __syncthreads();
       if (makes) {
         char* const to = reinterpret_cast<char*>(out + int64_t(c) * kChunk * out_step);
+        Split pf[kAhead ? 2 : 1][2];
+        // (of a pair that is all behind these tokens there are no scores, and none is used)
+        auto scores = [&](int x, Split (&to)[2]) __attribute__((always_inline)) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) get(ps, tokens(x) * 2 + m, l, to[m]);
+        };
+        if constexpr (kAhead) scores(0, pf[0]);
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
           const int rb = tokens(x), i = 16 * rb + c16 - shift;
+          if constexpr (kAhead) {
+            if (x + 1 < kRows) scores(x + 1, pf[(x + 1) % 2]);
+            issued();
+          }
           const float at_row = n == kChunk ? into[x] : power(e, max(s.rev ? n - 1 - i : i + 1, 0)) * s.read;
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) o[x][j] = o[x][j] * at_row;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (!(s.rev ? m == 1 || rb < 2 : m == 0 || rb >= 2)) continue;
-            Split pf;
-            get(ps, rb * 2 + m, l, pf);
+            if constexpr (!kAhead) get(ps, rb * 2 + m, l, pf[0][m]);
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) o[x][j] = mma(vf[j][m], pf, o[x][j]);
+            for (int j = 0; j < kOwn; ++j) o[x][j] = mma(vf[j][m], pf[kAhead ? x % 2 : 0][m], o[x][j]);
           }
           if (uint32_t(i) < uint32_t(n)) {
 #pragma unroll

@@ -14,7 +14,10 @@
 // thread keeps its channels' weights and walks over rows.  Sums of squares are made in
 // double, so that no row of float32 numbers leaves their range.  A group's sum is a sum
 // over lanes where a group is 1, 2, 4, ... 64 pieces of 8, else it goes through LDS; a
-// whole row's over the row's waves.
+// whole row's over the row's waves.  Rows are dealt out one after the other to all
+// workgroups, which so work on neighbouring memory at a time (8 x 2048 x 768 in bfloat16,
+// gradients: 81 us with a run of rows a workgroup, 78 us so; 5555 x 2304: 96 and 81 us).
+// Measured there: forward 34 us (176 MB, 5.2 TB/s), gradients 69 us (330 MB, 4.8 TB/s).
 //
 // In 8 bits, 32 adjacent channels of a row share a step, the smallest power of two of which
 // 127 reach the largest of them: a value is off by at most half a step, 2^-7 of the
