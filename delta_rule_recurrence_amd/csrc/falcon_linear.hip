@@ -31,8 +31,8 @@ struct Tiles {
 Tiles cut(const LinearArgs& a) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
   // tiles of a head for three workgroups a CU, or for the two or one that wide heads leave room
-  // for (8 x 2048 x 12 x 64: 768 tiles 36 us of sweeps and sums, 1536 the same and 3 us more
-  // between them; 16384 x 12 x 128 x 128: 256 tiles 105 us in all, 512 114 us, 768 119 us)
+  // for (kernels of a prompt together, when this was chosen: 8 x 2048 x 12 x 64, 384 tiles 60 us,
+  // 768 56 us, 1536 62 us; 16384 x 12 x 128 x 128, 256 tiles 105 us, 512 113 us, 768 119 us)
   const int64_t all_tiles = a.dk * a.dv > 64 * 128 ? 256 : a.dk * a.dv > 64 * 64 ? 512 : 768;
   const int64_t want = std::max<int64_t>(1, all_tiles / std::max<int64_t>(heads, 1));   // (one more would take a round of its own)
   const int64_t chunks = std::max<int64_t>(1, (all + want - 1) / want);
