@@ -603,7 +603,8 @@ size_t falcon_linear_bwd_workspace_bytes(const falcon_linear_problem* p);
  * projection; without post_norm and gate, the plain pre-norm residual.  A group of zeros
  * needs eps > 0 to stay finite.
  *
- *  y, gate    : [B, T, C] io dtype, rows of y_row and gate_row elements; gate may be NULL.
+ *  y, gate    : [B, T, C] io dtype, rows of y_row and gate_row elements; gate may be NULL
+ *               (gate_row is then ignored).
  *  h          : [B, T, C] stream dtype, or NULL for zero.
  *  post_weight, alpha, pre_weight : [C] float32, or NULL for one.
  *  h_out      : [B, T, C] stream dtype; may alias h exactly.

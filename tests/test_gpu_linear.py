@@ -276,3 +276,18 @@ def test_allocated_outputs_are_zero_behind_the_ends(T, layout, dtype):
     o, _ = check_forward(d, lengths=lengths, layouts=(layout,) * 3, what=f"{T} {layout} {dtype}")
     for b, n in enumerate(lengths):
         assert torch.all(heads(o, layout, 3)[b, :, n:] == 0)
+
+
+def test_more_states_than_one_grid():
+    """Single tokens of 2^19 + 3 heads of 64 x 64, whose states' elements pass 2^32 threads
+    with both carries: the gradients in closed form."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GiB of device memory")
+    B = (1 << 19) + 3
+    q, k, v, dO = (torch.empty(B, 1, 1, 64, device="cuda").uniform_(-1, 1) for _ in range(4))
+    g = fb.falcon_linear_bwd(q, k, v, torch.zeros(1, device="cuda"), dO, scale=0.5)
+    dot = lambda a, b: (a.double() * b.double()).sum(-1, keepdim=True)  # noqa: E731
+    for name, want in (("dq", 0.5 * dot(dO, v) * k), ("dk", 0.5 * dot(dO, v) * q), ("dv", 0.5 * dot(q, k) * dO)):
+        err = float((g[name].double() - want).norm() / want.norm())
+        assert err <= 4 * (16 + depth(1, 64)) * 2.0 ** -24, name
+    torch.cuda.empty_cache()
