@@ -691,10 +691,11 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   s.rows_block = std::max(1, 256 / s.threads_row);
   const int64_t rows = int64_t(a.B) * a.T;
   // as many workgroups as the CUs hold at a time, at three or four waves a SIMD: one more round of a
-  // few costs what a whole one does (5555 rows of 2304, five waves each, gradients: 81 us
-  // with two a CU, 111 us with three)
-  const int simd = bwd && !by_piece(form_of(a)) ? 3 : 4, waves = (s.rows_block * s.threads_row / 64 + 3) / 4;
-  const int64_t most = 256 * std::max(1, simd / waves);
+  // few costs what a whole one does (5555 rows of 2304, five waves each, gradients: 72 us
+  // with two a CU, 96 us with three).  Workgroups of three waves fit five times (16384 rows of
+  // 1536: forward 36.6 us, 39.8 us with four; gradients of 8192 rows: 76 and 74 us).
+  const int waves = s.rows_block * s.threads_row / 64, simd = bwd && !by_piece(form_of(a)) ? 3 : 4;
+  const int64_t most = 256 * (waves == 3 && !bwd ? 5 : std::max(1, simd / ((waves + 3) / 4)));
   const int64_t each = std::max<int64_t>(1, (rows + most * s.rows_block - 1) / (most * s.rows_block));
   s.rows_each = int(bwd ? std::min<int64_t>(each, kRowsEach) : each);
   s.blocks = (rows + int64_t(s.rows_each) * s.rows_block - 1) / (int64_t(s.rows_each) * s.rows_block);
