@@ -28,14 +28,20 @@ struct Tiles {
   int chunks, tiles;   // chunks of a tile; tiles of a head
 };
 
-Tiles cut(const LinearArgs& a) {
+Tiles cut(const LinearArgs& a, bool forward) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
   // tiles of a head for three workgroups a CU, or for the two or one that wide heads leave room
   // for (kernels of a prompt together, when this was chosen: 8 x 2048 x 12 x 64, 384 tiles 60 us,
   // 768 56 us, 1536 62 us; 16384 x 12 x 128 x 128, 256 tiles 105 us, 512 113 us, 768 119 us)
   const int64_t all_tiles = a.dk * a.dv > 64 * 128 ? 256 : a.dk * a.dv > 64 * 64 ? 512 : 768;
   const int64_t want = std::max<int64_t>(1, all_tiles / std::max<int64_t>(heads, 1));   // (one more would take a round of its own)
-  const int64_t chunks = std::max<int64_t>(1, (all + want - 1) / want);
+  // A short prompt's heads take one tile each: one launch for three.  (us of a call, one tile and
+  // several: 8 heads of 64 x 64 in bfloat16, 4 chunks 14 and 21, 8 chunks 24 and 21; 96 heads,
+  // 8 chunks 25 and 26, 12 chunks 35 and 29, of 128 x 128 8 chunks 36 and 50; float32, 8 heads, 2
+  // chunks 14 and 21, 4 chunks 25 and 21; 96 heads, 4 chunks 26 and 27, 8 chunks 47 and 38.  In a
+  // graph, without the host, 8 heads' 4 chunks take 14 and 11.  Gradients gain nothing.)
+  const int64_t few = forward ? (heads >= 64 ? 2 : 1) * (a.bf16 ? 4 : 2) : 0;
+  const int64_t chunks = all <= few ? std::max<int64_t>(all, 1) : std::max<int64_t>(1, (all + want - 1) / want);
   return {heads, int(chunks), int(std::max<int64_t>(1, (all + chunks - 1) / chunks))};
 }
 
@@ -286,13 +292,13 @@ struct BwdLayout {
 }  // namespace
 
 size_t linear_workspace_bytes(const LinearArgs& a) {
-  const Tiles t = cut(a);
+  const Tiles t = cut(a, true);
   return t.tiles > 1 ? size_t(t.heads) * t.tiles * a.dk * a.dv * sizeof(float) : 0;
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
   if (a.T == 0) return launch_state_copy(a.S0, a.S_T, int64_t(a.B) * a.H * a.dk * a.dv, st);
-  const Tiles t = cut(a);
+  const Tiles t = cut(a, true);
   LinearSweep s = sweep_base(a, t);
   s.k = a.k; s.v = a.v;
   s.k_at = a.k_at; s.v_at = a.v_at;
@@ -320,12 +326,12 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
 hipError_t launch_linear_step(const LinearArgs& a, hipStream_t st) { return a.bf16 ? step_of<bf16_t>(a, st) : step_of<float>(a, st); }
 
 size_t linear_bwd_workspace_bytes(const LinearArgs& a) {
-  const BwdLayout l(a, cut(a));
+  const BwdLayout l(a, cut(a, false));
   return size_t(l.S + l.R + l.parts) * sizeof(float);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
-  const Tiles t = cut(a);
+  const Tiles t = cut(a, false);
   const BwdLayout l(a, t);
   float* const S = a.workspace;
   float* const R = S + l.S;

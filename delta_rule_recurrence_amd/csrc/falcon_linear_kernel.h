@@ -741,7 +741,8 @@ template <int DK>
 hipError_t outputs_of(const LinearSweep& s, hipStream_t st) {
   return by_width(s.dv, [&](auto dv) {
     if (!s.bf16) return launch_sweep<float, float, DK, dv(), true>(s, nullptr, st);
-    return s.last ? launch_sweep<bf16_t, bf16_t, DK, dv(), true>(s, nullptr, st) : launch_sweep<bf16_t, bf16_t, DK, dv(), true, 2>(s, nullptr, st);
+    // (a head of one tile by the three terms that its last state takes, asked for or not)
+    return s.slots ? launch_sweep<bf16_t, bf16_t, DK, dv(), true, 2>(s, nullptr, st) : launch_sweep<bf16_t, bf16_t, DK, dv(), true>(s, nullptr, st);
   });
 }
 template <int DK>

@@ -291,3 +291,13 @@ def test_more_states_than_one_grid():
         err = float((g[name].double() - want).norm() / want.norm())
         assert err <= 4 * (16 + depth(1, 64)) * 2.0 ** -24, name
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [3, 32])
+@pytest.mark.parametrize("T", [128, 129, 256, 257, 512, 513])
+def test_prompts_of_one_tile_and_of_several(T, H, dtype):
+    """On both sides of the lengths up to which a head is one tile, with states."""
+    d = inputs(2, H, T, 16, 32, IO[dtype], 240 + T)
+    check_forward(d, what=f"{T} {H} {dtype}")
+    check_forward(d, lengths=[T - 1, T // 2], what=f"padded {T} {H} {dtype}")
