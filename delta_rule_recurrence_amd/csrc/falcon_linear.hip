@@ -61,19 +61,18 @@ struct Carry {
 };
 struct Carries {
   Carry c[2];              // one or two of the same sizes
-  uint32_t blocks;         // of each
-  uint32_t count;
   const float* log_decay;
   const int32_t* lengths;
-  int64_t heads;
   int H, T, tiles, chunks, size;   // size: elements of a state
 };
 
-// The elements `block` 256 .. + 255 of a carry's states.
-__device__ __forceinline__ void carry(const Carries& a, const Carry& c, uint32_t block) {
-  const int64_t at = int64_t(block) * 256 + threadIdx.x;
-  const uint32_t bh = block / uint32_t(a.size / 256);   // (256 divides the size)
-  const int e = int(at - int64_t(bh) * a.size);
+// A workgroup a head, 256 elements of its state and a carry.  (2^21 heads of 128 x 128 have more
+// of these threads than a grid has in one direction.)
+__global__ __launch_bounds__(256) void carry_kernel(Carries a) {
+  const Carry c = a.c[blockIdx.z];
+  const uint32_t bh = blockIdx.x;
+  const int e = int(blockIdx.y * 256 + threadIdx.x);
+  const int64_t at = int64_t(bh) * a.size + e;
   const int b = int(bh / uint32_t(a.H)), h = int(bh % uint32_t(a.H));
   const int len = tokens_of(a.lengths, b, a.T), tokens = a.chunks * kChunk;
   const float log2_a = a.log_decay[h] * kLog2e;
@@ -101,17 +100,10 @@ __device__ __forceinline__ void carry(const Carries& a, const Carry& c, uint32_t
   if (c.last) c.last[at] = s;
 }
 
-__global__ __launch_bounds__(256) void carry_kernel(Carries a) {
-  for (uint32_t block = blockIdx.x; block < a.blocks * a.count; block += gridDim.x)
-    carry(a, a.c[block >= a.blocks ? 1 : 0], block >= a.blocks ? block - a.blocks : block);
-}
-
 hipError_t launch_carry(const LinearArgs& l, const Tiles& t, const Carry& c, const Carry* second, hipStream_t st) {
   const int size = l.dk * l.dv;
-  const uint32_t blocks = uint32_t(t.heads * (size / 256)), count = second ? 2 : 1;   // 2^28 at most
-  // (a grid holds 2^24 workgroups of 256; 2^21 heads of 64 x 64 have more)
-  carry_kernel<<<dim3(std::min<uint32_t>(blocks * count, 1 << 22)), dim3(256), 0, st>>>(
-      {{c, second ? *second : c}, blocks, count, l.log_decay, l.lengths, t.heads, l.H, l.T, t.tiles, t.chunks, size});
+  carry_kernel<<<dim3(unsigned(t.heads), unsigned(size / 256), second ? 2 : 1), dim3(256), 0, st>>>(
+      {{c, second ? *second : c}, l.log_decay, l.lengths, l.H, l.T, t.tiles, t.chunks, size});
   return hipGetLastError();
 }
 
