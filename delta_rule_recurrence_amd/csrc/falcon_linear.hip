@@ -28,19 +28,21 @@ struct Tiles {
   int chunks, tiles;   // chunks of a tile; tiles of a head
 };
 
-Tiles cut(const LinearArgs& a, bool forward) {
+Tiles cut(const LinearArgs& a) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
   // tiles of a head for three workgroups a CU, or for the two or one that wide heads leave room
   // for (kernels of a prompt together, when this was chosen: 8 x 2048 x 12 x 64, 384 tiles 60 us,
   // 768 56 us, 1536 62 us; 16384 x 12 x 128 x 128, 256 tiles 105 us, 512 113 us, 768 119 us)
   const int64_t all_tiles = a.dk * a.dv > 64 * 128 ? 256 : a.dk * a.dv > 64 * 64 ? 512 : 768;
   const int64_t want = std::max<int64_t>(1, all_tiles / std::max<int64_t>(heads, 1));   // (one more would take a round of its own)
-  // A short prompt's heads take one tile each: one launch for three.  (us of a call, one tile and
-  // several: 8 heads of 64 x 64 in bfloat16, 4 chunks 14 and 21, 8 chunks 24 and 21; 96 heads,
-  // 8 chunks 25 and 26, 12 chunks 35 and 29, of 128 x 128 8 chunks 36 and 50; float32, 8 heads, 2
-  // chunks 14 and 21, 4 chunks 25 and 21; 96 heads, 4 chunks 26 and 27, 8 chunks 47 and 38.  In a
-  // graph, without the host, 8 heads' 4 chunks take 14 and 11.  Gradients gain nothing.)
-  const int64_t few = forward ? (heads >= 64 ? 2 : 1) * (a.bf16 ? 4 : 2) : 0;
+  // A short prompt's heads take one tile each: one launch for three, and no states between
+  // tiles.  (us of a call, one tile and several.  Outputs: 8 heads of 64 x 64 in bfloat16, 4 chunks
+  // 14 and 21, 8 chunks 24 and 21; 96 heads, 8 chunks 25 and 26, 12 chunks 35 and 29, of 128 x 128
+  // 8 chunks 36 and 50; float32, 8 heads, 2 chunks 14 and 21, 4 chunks 25 and 21; 96 heads, 4 chunks
+  // 26 and 27, 8 chunks 47 and 38.  Gradients: 8 heads, bfloat16, 4 chunks 19 and 24; 96 heads
+  // 19 and 31; float32, 8 heads, 2 chunks 18 and 24, 4 chunks of 64 x 128 39 and 25; 96 heads 72
+  // and 82.  In a graph, without the host, 8 heads' 4 chunks take 14 and 11.)
+  const int64_t few = (heads >= 64 ? 2 : 1) * (a.bf16 ? 4 : 2);
   const int64_t chunks = all <= few ? std::max<int64_t>(all, 1) : std::max<int64_t>(1, (all + want - 1) / want);
   return {heads, int(chunks), int(std::max<int64_t>(1, (all + chunks - 1) / chunks))};
 }
@@ -212,11 +214,11 @@ struct DecayGrad {
   HeadSteps q_at, k_at, d_at;
   const float* dq;
   const float* dk;
-  const float* S;          // [heads][tiles] states that enter the tiles
-  const float* R;          // [heads][tiles + 1]: slot t, the adjoint before tile t's first token
+  const float* S;          // [heads][tiles] states that enter the tiles; may be null (zero)
+  const float* R;          // [heads][r_each]: slot t, the adjoint before tile t's first token
   const int32_t* lengths;
   float* parts;
-  int H, T, d, tiles, chunks, size;
+  int H, T, d, tiles, chunks, size, r_each;
 };
 
 template <typename IO>
@@ -230,10 +232,10 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
   double sum = 0.0;
   if (n > 0) {
     const float* s = a.S + (bh * a.tiles + tile) * a.size;
-    const float* r = a.R + (bh * (a.tiles + 1) + tile) * a.size;
+    const float* r = a.R + (bh * a.r_each + tile) * a.size;
     // (the size is a multiple of 256, of 1024 but for 16 x 16)
 #pragma unroll 4
-    for (int e = threadIdx.x * 4; e < a.size; e += 1024) {
+    for (int e = threadIdx.x * 4; e < (a.S ? a.size : 0); e += 1024) {
       float sv[4], rv[4];
       load_vec<float, 4>(s + e, sv);
       load_vec<float, 4>(r + e, rv);
@@ -270,13 +272,14 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
   }
 }
 
-// Workspace of the gradients: S slots, R slots (one more), rows of partial sums.
+// Workspace of the gradients: S slots, R slots (one more; of heads of one tile the adjoint
+// before the first token alone), rows of partial sums.
 struct BwdLayout {
   int64_t S, R, parts;   // floats
   BwdLayout(const LinearArgs& a, const Tiles& t) {
     const int64_t size = int64_t(a.dk) * a.dv;
-    S = t.heads * t.tiles * size;
-    R = t.heads * (t.tiles + 1) * size;
+    S = t.tiles > 1 ? t.heads * t.tiles * size : 0;
+    R = t.heads * (t.tiles > 1 ? t.tiles + 1 : 1) * size;
     parts = int64_t(a.B) * t.tiles * a.H;
   }
 };
@@ -284,13 +287,13 @@ struct BwdLayout {
 }  // namespace
 
 size_t linear_workspace_bytes(const LinearArgs& a) {
-  const Tiles t = cut(a, true);
+  const Tiles t = cut(a);
   return t.tiles > 1 ? size_t(t.heads) * t.tiles * a.dk * a.dv * sizeof(float) : 0;
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
   if (a.T == 0) return launch_state_copy(a.S0, a.S_T, int64_t(a.B) * a.H * a.dk * a.dv, st);
-  const Tiles t = cut(a, true);
+  const Tiles t = cut(a);
   LinearSweep s = sweep_base(a, t);
   s.k = a.k; s.v = a.v;
   s.k_at = a.k_at; s.v_at = a.v_at;
@@ -318,12 +321,12 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
 hipError_t launch_linear_step(const LinearArgs& a, hipStream_t st) { return a.bf16 ? step_of<bf16_t>(a, st) : step_of<float>(a, st); }
 
 size_t linear_bwd_workspace_bytes(const LinearArgs& a) {
-  const BwdLayout l(a, cut(a, false));
+  const BwdLayout l(a, cut(a));
   return size_t(l.S + l.R + l.parts) * sizeof(float);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
-  const Tiles t = cut(a, false);
+  const Tiles t = cut(a);
   const BwdLayout l(a, t);
   float* const S = a.workspace;
   float* const R = S + l.S;
@@ -335,29 +338,38 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
     const hipError_t e_ = (call);          \
     if (e_ != hipSuccess) return e_;       \
   } while (0)
-  // what each tile adds to the state, and to its adjoint
+  // what each tile adds to the state, and to its adjoint, where a head has several
+  const bool several = t.tiles > 1;
   LinearSweep s = sweep_base(a, t);
   s.k = a.k; s.v = a.v;
   s.k_at = a.k_at; s.v_at = a.v_at;
   s.dv = a.dv;
   s.sf = a.dv; s.sc = 1;
-  s.slots = S; s.slots_each = t.tiles;
+  if (several) s.slots = S, s.slots_each = t.tiles;
   LinearSweep r = sweep_base(a, t);
   r.k = a.q; r.v = a.dO;
   r.k_at = a.q_at; r.v_at = a.o_at;
   r.dv = a.dv;
   r.sf = a.dv; r.sc = 1;
-  r.slots = R; r.slots_each = t.tiles + 1; r.slot0 = 1;
+  if (several) r.slots = R, r.slots_each = t.tiles + 1, r.slot0 = 1;
   r.rev = true;
   s.clear = r.clear = a.lengths != nullptr;
   r.write = a.scale;
-  FALCON_TRY(FALCON_BY_KEYS(sums, a.dk, s, &r, st));
-  const Carry back{R, t.tiles + 1, 1, a.dS_T, a.dS0, true};
-  FALCON_TRY(launch_carry(a, t, {S, t.tiles, 0, a.S0, nullptr, false}, &back, st));
+  float* before = R;     // the adjoint before the first token, where it lies by itself
+  if (several) {
+    FALCON_TRY(FALCON_BY_KEYS(sums, a.dk, s, &r, st));
+    const Carry back{R, t.tiles + 1, 1, a.dS_T, a.dS0, true};
+    FALCON_TRY(launch_carry(a, t, {S, t.tiles, 0, a.S0, nullptr, false}, &back, st));
+  } else {
+    s.start = a.S0;
+    r.start = a.dS_T;
+    if (a.dS0) before = a.dS0;
+  }
   // dv = (k, q, dO) against time
   LinearSweep dv = r;
   dv.q = a.k; dv.q_at = a.k_at;
   dv.out = a.dv_out; dv.out_at = a.dv_at;
+  if (!several && (a.dS0 || a.dlog_decay)) dv.last = before;
   // dk = (v, dO, q) against time, from the transposed adjoint
   LinearSweep dk = r;
   dk.q = a.v; dk.q_at = a.v_at;
@@ -377,7 +389,8 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   dq.out = a.dq; dq.out_at = a.dqk_at;
   FALCON_TRY(FALCON_BY_KEYS(gradients, a.dk, dv, dk, dq, st));
   if (a.dlog_decay) {
-    const DecayGrad d{a.q, a.k, a.q_at, a.k_at, a.dqk_at, a.dq, a.dk_out, S, R, a.lengths, parts, a.H, a.T, a.dk, t.tiles, t.chunks, size};
+    const DecayGrad d{a.q, a.k, a.q_at, a.k_at, a.dqk_at, a.dq, a.dk_out, several ? S : a.S0, before, a.lengths, parts,
+                      a.H, a.T, a.dk, t.tiles, t.chunks, size, several ? t.tiles + 1 : 1};
     const dim3 grid(unsigned(t.heads * t.tiles));
     if (a.bf16) {
       decay_grad_kernel<bf16_t><<<grid, dim3(256), 0, st>>>(d);

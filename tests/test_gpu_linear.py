@@ -301,3 +301,20 @@ def test_prompts_of_one_tile_and_of_several(T, H, dtype):
     d = inputs(2, H, T, 16, 32, IO[dtype], 240 + T)
     check_forward(d, what=f"{T} {H} {dtype}")
     check_forward(d, lengths=[T - 1, T // 2], what=f"padded {T} {H} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [3, 32])
+@pytest.mark.parametrize("T", [64, 128, 129, 256, 257, 512, 513])
+@pytest.mark.parametrize("carry", [False, True])
+def test_gradients_of_one_tile_and_of_several(T, H, dtype, carry):
+    """The same of the gradients, with those of states and decays, asked for or not."""
+    d = inputs(2, H, T, 16, 32, IO[dtype], 260 + T, carry=carry)
+    check_backward(d, what=f"{T} {H} {dtype}")
+    g = check_backward(d, lengths=[T - 1, T // 2], learned=False, what=f"padded {T} {H} {dtype}")
+    assert g["dlog_decay"] is None and (g["dS0"] is None) == (not carry)
+    if not carry:   # a state's gradient without a state
+        asked = {"dS0": torch.empty(2, H, 16, 32, device="cuda")}
+        check_backward(d, learned=False, grads=asked)
+        want = lo.linear_backward(*(f64(d[n]) for n in ("q", "k", "v", "log_decay", "dO")), scale=0.3)["dS0"]
+        close(asked["dS0"], want, depth(T, 32), "dS0")
