@@ -26,10 +26,9 @@
 // bfloat16).  The rows of the next chunk are on their way while one is worked on.
 //
 // bfloat16 inputs enter the products as they are.  What is float32 (decayed
-// scores, states, decayed values) enters as a sum of bfloat16 terms, which keep 8
-// bits each: two for results in bfloat16 (2^-17 of the operand is lost, against
-// 2^-9 in the result), three where they are float32 and for the state.  float32
-// inputs use the float32 matrix instruction throughout.
+// scores, states, decayed values) enters as a sum of three bfloat16 terms, which keep
+// 8 bits each and so all of float32's.  float32 inputs use the float32 matrix
+// instruction throughout.
 //
 // What bounds it, at 8 x 2048 x 12 x 64 in bfloat16: outputs of a prompt 25 us for the 113 MB
 // that they move (4.6 TB/s, a copy's rate), sums 14 us for 63 MB, gradients 70 us for 330 MB.
@@ -64,21 +63,21 @@ constexpr int kChunk = 64;
 struct f32x8 {
   f32x4 lo, hi;
 };
-template <int N>
+constexpr int kTerms = 3;
 struct Terms {
-  bf16x8 t[N];
+  bf16x8 t[kTerms];
 };
 
 // The exact operand of an input, and the operand of float32 values.
-template <typename IO, int TERMS>
+template <typename IO>
 struct Operands;
-template <int TERMS>
-struct Operands<bf16_t, TERMS> {
+template <>
+struct Operands<bf16_t> {
   using Exact = bf16x8;
-  using Split = Terms<TERMS>;
+  using Split = Terms;
 };
-template <int TERMS>
-struct Operands<float, TERMS> {
+template <>
+struct Operands<float> {
   using Exact = f32x8;
   using Split = f32x8;
 };
@@ -92,11 +91,10 @@ __device__ __forceinline__ uint32_t split2(float& x, float& y) {
   y -= __uint_as_float(t & 0xffff0000u);
   return t;
 }
-template <int N>
-__device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Terms<N>& out) {
+__device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Terms& out) {
   float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
+  for (int n = 0; n < kTerms; ++n) {
     uint4 t;
     t.x = split2(v[0], v[1]);
     t.y = split2(v[2], v[3]);
@@ -108,16 +106,14 @@ __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Terms<N>& out) {
 __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, f32x8& out) { out = {lo, hi}; }
 
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) { return frag::mfma32(a, b, c); }
-template <int N>
-__device__ __forceinline__ f32x4 mma(bf16x8 a, const Terms<N>& b, f32x4 c) {
+__device__ __forceinline__ f32x4 mma(bf16x8 a, const Terms& b, f32x4 c) {
 #pragma unroll
-  for (int n = N - 1; n >= 0; --n) c = frag::mfma32(a, b.t[n], c);
+  for (int n = kTerms - 1; n >= 0; --n) c = frag::mfma32(a, b.t[n], c);
   return c;
 }
-template <int N>
-__device__ __forceinline__ f32x4 mma(const Terms<N>& a, bf16x8 b, f32x4 c) {
+__device__ __forceinline__ f32x4 mma(const Terms& a, bf16x8 b, f32x4 c) {
 #pragma unroll
-  for (int n = N - 1; n >= 0; --n) c = frag::mfma32(a.t[n], b, c);
+  for (int n = kTerms - 1; n >= 0; --n) c = frag::mfma32(a.t[n], b, c);
   return c;
 }
 // v_mfma_f32_16x16x4_f32 sums one value of each of the four lane groups, so eight
@@ -187,15 +183,13 @@ __device__ __forceinline__ f32x4 widened(const f32x8& v, int half) { return half
 // Operand fragments in LDS, 64 lanes' parts of 16 bytes next to each other.
 __device__ __forceinline__ void put(char* lds, int frag, int l, bf16x8 v) { reinterpret_cast<bf16x8*>(lds)[frag * 64 + l] = v; }
 __device__ __forceinline__ void get(const char* lds, int frag, int l, bf16x8& v) { v = reinterpret_cast<const bf16x8*>(lds)[frag * 64 + l]; }
-template <int N>
-__device__ __forceinline__ void put(char* lds, int frag, int l, const Terms<N>& v) {
+__device__ __forceinline__ void put(char* lds, int frag, int l, const Terms& v) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) put(lds, frag * N + n, l, v.t[n]);
+  for (int n = 0; n < kTerms; ++n) put(lds, frag * kTerms + n, l, v.t[n]);
 }
-template <int N>
-__device__ __forceinline__ void get(const char* lds, int frag, int l, Terms<N>& v) {
+__device__ __forceinline__ void get(const char* lds, int frag, int l, Terms& v) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) get(lds, frag * N + n, l, v.t[n]);
+  for (int n = 0; n < kTerms; ++n) get(lds, frag * kTerms + n, l, v.t[n]);
 }
 __device__ __forceinline__ void put(char* lds, int frag, int l, const f32x8& v) {
   f32x4* p = reinterpret_cast<f32x4*>(lds) + frag * 128 + l;
@@ -283,34 +277,31 @@ constexpr int waves_simd() {
   return sizeof(IO) == 2 && DK <= 64 && DV <= 64 ? 3 : 2;
 }
 // LDS: keys, values and, for outputs, queries and scores as fragments.
-template <typename IO, typename O, int DK, int DV, bool OUT>
+template <typename IO, int DK, int DV, bool OUT>
 constexpr int lds_once() {
-  const int terms = sizeof(O) == 2 ? 2 : 3;
-  const int scores = 8 * 64 * (sizeof(IO) == 2 ? terms * 16 : 32);
+  const int scores = 8 * 64 * (sizeof(IO) == 2 ? kTerms * 16 : 32);
   return Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes + (OUT ? kChunk * Stage<IO, DK>::kWidth * int(sizeof(IO)) + scores : 0);
 }
 // Two places in turn for what is read up to a chunk's end (the keys; without outputs the
 // values, too) save the barrier there, where as many workgroups fit a CU all the same.
-template <typename IO, typename O, int DK, int DV, bool OUT>
+template <typename IO, int DK, int DV, bool OUT>
 constexpr bool in_turn() {
-  const int once = lds_once<IO, O, DK, DV, OUT>(), more = Stage<IO, DK>::kBytes + (OUT ? 0 : Stage<IO, DV>::kBytes);
+  const int once = lds_once<IO, DK, DV, OUT>(), more = Stage<IO, DK>::kBytes + (OUT ? 0 : Stage<IO, DV>::kBytes);
   const int room = waves_simd<IO, DK, DV>() * 4 / waves<IO, DK, DV>(), before = 160 * 1024 / once, after = 160 * 1024 / (once + more);
   return after >= (before < room ? before : room);
 }
-template <typename IO, typename O, int DK, int DV, bool OUT>
+template <typename IO, int DK, int DV, bool OUT>
 constexpr int lds_bytes() {
-  return lds_once<IO, O, DK, DV, OUT>() + (in_turn<IO, O, DK, DV, OUT>() ? Stage<IO, DK>::kBytes + (OUT ? 0 : Stage<IO, DV>::kBytes) : 0);
+  return lds_once<IO, DK, DV, OUT>() + (in_turn<IO, DK, DV, OUT>() ? Stage<IO, DK>::kBytes + (OUT ? 0 : Stage<IO, DV>::kBytes) : 0);
 }
 
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void store4(bf16_t* p, f32x4 v) { frag::store_half(reinterpret_cast<uint16_t*>(p), v); }
 
 // The tile `block` of a sweep.  OUT false: only what the tile's chunks add to a state,
-// from zero, into the tile's slot.  WRITTEN: terms of what is written into the state, two
-// where only outputs in bfloat16 come of it.
-template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN>
+// from zero, into the tile's slot.
+template <typename IO, typename O, int DK, int DV, bool OUT>
 __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char* lds) {
-  constexpr int kTerms = sizeof(O) == 2 ? 2 : 3;
   constexpr int kWaves = waves<IO, DK, DV>(), kThreads = 64 * kWaves;
   constexpr int kB = Stage<IO, DK>::kWidth / 32;           // 32-wide blocks of the key axis
   constexpr int kCols = DV / 16;                           // 16-wide blocks of the value axis
@@ -318,7 +309,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   constexpr int kShare = kCols >= kWaves ? 1 : kWaves / kCols; // waves that share a block of columns
   constexpr int kRows = kShare >= 4 ? 1 : 4 / kShare;      // blocks of 16 tokens whose outputs a wave makes
   constexpr int kPk = Stage<IO, DK>::kPitch, kPv = Stage<IO, DV>::kPitch;
-  using Ops = Operands<IO, kTerms>;
+  using Ops = Operands<IO>;
   using Exact = typename Ops::Exact;
   using Split = typename Ops::Split;
 
@@ -329,8 +320,8 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   auto issued = [&]() {
     if constexpr (kAhead) asm volatile("" ::: "memory");
   };
-  constexpr bool kInTurn = in_turn<IO, O, DK, DV, OUT>();
-  char* const second = lds + lds_once<IO, O, DK, DV, OUT>();
+  constexpr bool kInTurn = in_turn<IO, DK, DV, OUT>();
+  char* const second = lds + lds_once<IO, DK, DV, OUT>();
   IO* ks = reinterpret_cast<IO*>(lds);
   IO* vs = reinterpret_cast<IO*>(lds + Stage<IO, DK>::kBytes);
   char* const qs = lds + Stage<IO, DK>::kBytes + Stage<IO, DV>::kBytes;   // [4][kB] fragments
@@ -619,7 +610,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
     }
     if (!OUT || more || s.last) {
       const float across = n < kChunk ? power(e, n) : whole;
-      typename Operands<IO, WRITTEN>::Split wf[kOwn][2];
+      Split wf[kOwn][2];
 #pragma unroll
       for (int j = 0; j < kOwn; ++j)
 #pragma unroll
@@ -663,11 +654,11 @@ struct Sweeps2 {
   LinearSweep s[2];
   uint32_t blocks;     // of each
 };
-template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN>
+template <typename IO, typename O, int DK, int DV, bool OUT>
 __global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<IO, DK, DV>())) void sweep_kernel(Sweeps2 p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const uint32_t which = blockIdx.x >= p.blocks ? 1 : 0;
-  sweep<IO, O, DK, DV, OUT, WRITTEN>(p.s[which], blockIdx.x - which * p.blocks, lds);
+  sweep<IO, O, DK, DV, OUT>(p.s[which], blockIdx.x - which * p.blocks, lds);
 }
 
 // The three gradients' sweeps, dv's over keys of DK, dk's and dq's over keys of DV.  The
@@ -683,11 +674,11 @@ __global__ __launch_bounds__((64 * waves<IO, DK, DV>()), (waves_simd<IO, DK, DV>
   const uint32_t which = blockIdx.x / 8 % 3, block = blockIdx.x / 24 * 8 + blockIdx.x % 8;
   if (block >= p.blocks) return;
   if constexpr (DK == DV) {
-    sweep<IO, float, DK, DV, true, 3>(p.s[which], block, lds);
+    sweep<IO, float, DK, DV, true>(p.s[which], block, lds);
   } else if (which == 0) {
-    sweep<IO, float, DK, DV, true, 3>(p.s[0], block, lds);
+    sweep<IO, float, DK, DV, true>(p.s[0], block, lds);
   } else {
-    sweep<IO, float, DV, DK, true, 3>(p.s[which], block, lds);
+    sweep<IO, float, DV, DK, true>(p.s[which], block, lds);
   }
 }
 
@@ -701,18 +692,18 @@ hipError_t launch(Kernel kernel, uint32_t blocks, int threads, int lds, const Ar
   return hipGetLastError();
 }
 
-template <typename IO, typename O, int DK, int DV, bool OUT, int WRITTEN = 3>
+template <typename IO, typename O, int DK, int DV, bool OUT>
 hipError_t launch_sweep(const LinearSweep& s, const LinearSweep* second, hipStream_t st) {
-  constexpr int lds = lds_bytes<IO, O, DK, DV, OUT>();
+  constexpr int lds = lds_bytes<IO, DK, DV, OUT>();
   static_assert(lds <= 160 * 1024);
   const uint32_t blocks = uint32_t(s.heads * s.tiles);
-  return launch(sweep_kernel<IO, O, DK, DV, OUT, WRITTEN>, blocks * (second ? 2 : 1), 64 * waves<IO, DK, DV>(), lds,
+  return launch(sweep_kernel<IO, O, DK, DV, OUT>, blocks * (second ? 2 : 1), 64 * waves<IO, DK, DV>(), lds,
                 Sweeps2{{s, second ? *second : s}, blocks}, st);
 }
 
 template <typename IO, int DK, int DV>
 hipError_t launch_gradients(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st) {
-  constexpr int a = lds_bytes<IO, float, DK, DV, true>(), b = lds_bytes<IO, float, DV, DK, true>(), lds = a > b ? a : b;
+  constexpr int a = lds_bytes<IO, DK, DV, true>(), b = lds_bytes<IO, DV, DK, true>(), lds = a > b ? a : b;
   static_assert(lds <= 160 * 1024);
   const uint32_t blocks = uint32_t(dv.heads * dv.tiles);
   return launch(gradients_kernel<IO, DK, DV>, (blocks + 7) / 8 * 24, 64 * waves<IO, DK, DV>(), lds, Sweeps3{{dv, dk, dq}, blocks}, st);
@@ -740,9 +731,7 @@ hipError_t sums_of(const LinearSweep& s, const LinearSweep* second, hipStream_t 
 template <int DK>
 hipError_t outputs_of(const LinearSweep& s, hipStream_t st) {
   return by_width(s.dv, [&](auto dv) {
-    if (!s.bf16) return launch_sweep<float, float, DK, dv(), true>(s, nullptr, st);
-    // (a head of one tile by the three terms that its last state takes, asked for or not)
-    return s.slots ? launch_sweep<bf16_t, bf16_t, DK, dv(), true, 2>(s, nullptr, st) : launch_sweep<bf16_t, bf16_t, DK, dv(), true>(s, nullptr, st);
+    return s.bf16 ? launch_sweep<bf16_t, bf16_t, DK, dv(), true>(s, nullptr, st) : launch_sweep<float, float, DK, dv(), true>(s, nullptr, st);
   });
 }
 template <int DK>

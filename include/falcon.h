@@ -542,9 +542,9 @@ size_t falcon_scan_bwd_workspace_bytes(const falcon_scan_problem* p);
  * dk, dv in {16, 32, 64, 128}; at most 2^21 heads (B H) and 2^22 elements of a
  * row.  The prompt is worked on in
  * chunks of 64 tokens: float32 throughout with float32 inputs, and with bf16 inputs
- * by bf16 products with float32 sums in which every float32 operand is a sum of two
- * bf16 numbers (three for the state and for gradients), so results are those of
- * float32 arithmetic, rounded once.  A token whose values are not finite reaches the
+ * by bf16 products with float32 sums in which every float32 operand is a sum of three
+ * bf16 numbers, which hold all its bits, so results are those of float32 arithmetic,
+ * rounded once.  A token whose values are not finite reaches the
  * outputs of its sequence from the start of its chunk on.
  */
 typedef struct {
