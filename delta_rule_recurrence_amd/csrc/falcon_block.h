@@ -171,12 +171,33 @@ struct LinearSweep {
   bool rev, bf16;
   bool clear;              // zeros in the output rows behind the sequences' ends
 };
+// Every tile's part of the decays' gradient: see falcon_linear_decay.h.
+struct LinearDecays {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* dO;
+  HeadSteps q_at, k_at, v_at, o_at;
+  const float* log_decay;
+  const int32_t* lengths;  // may be null
+  const float* S;          // [heads][s_each] states: tile t's at t, the one that enters it; may be null (zero)
+  const float* R;          // [heads][r_each] adjoints: tile t's at t, from behind it; may be null (zero)
+  int64_t s_each, r_each;
+  float* parts;            // [B][tiles][H]
+  int64_t heads;
+  int H, T, dv, tiles, chunks;   // chunks: of a tile
+  float read;              // factor of what is read
+  bool bf16;
+};
+
 // What the tiles of one or two sweeps of the same sizes add to a state; the outputs of one;
-// the gradients' sweeps, dv's first.  By the width of the (first sweep's) keys.
+// the gradients' sweeps, dv's first; the decays' gradient.  By the width of the (first sweep's)
+// keys.
 #define FALCON_LINEAR_OF(DK)                                                                                          \
   hipError_t launch_linear_sums_##DK(const LinearSweep& s, const LinearSweep* second, hipStream_t st);                \
   hipError_t launch_linear_outputs_##DK(const LinearSweep& s, hipStream_t st);                                        \
-  hipError_t launch_linear_gradients_##DK(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st);
+  hipError_t launch_linear_gradients_##DK(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st); \
+  hipError_t launch_linear_decays_##DK(const LinearDecays& a, hipStream_t st);
 FALCON_LINEAR_OF(16)
 FALCON_LINEAR_OF(32)
 FALCON_LINEAR_OF(64)

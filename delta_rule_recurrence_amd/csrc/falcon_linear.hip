@@ -1,5 +1,5 @@
 // Linear attention with a decay for each head (gfx950): how its sweeps follow one
-// another, the states between tiles, single tokens and the decays' gradient.
+// another, the states between tiles and single tokens.
 //
 //   S_t = exp(log_decay) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
 //
@@ -200,86 +200,15 @@ hipError_t step_of(const LinearArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// ---- the decays' gradient ------------------------------------------------------------------
-// With R_t the adjoint of S_t, d log_decay = sum over t of X_t = a <S_(t-1), R_t>, and
-//
-//   X_(t+1) = <S_t, R_t> - q_t . dq_t = X_t + k_t . dk_t - q_t . dq_t
-//
-// so a tile of n tokens gives n X_1 + sum_j (n - 1 - j) (k_j . dk_j - q_j . dq_j), j from
-// 0, with X_1 the product of the two states at its start.  Summed in double; a row of
-// partial sums for each sequence and tile, a column for each head.
-struct DecayGrad {
-  const void* q;
-  const void* k;
-  HeadSteps q_at, k_at, d_at;
-  const float* dq;
-  const float* dk;
-  const float* S;          // [heads][tiles] states that enter the tiles; may be null (zero)
-  const float* R;          // [heads][r_each]: slot t, the adjoint before tile t's first token
-  const int32_t* lengths;
-  float* parts;
-  int H, T, d, tiles, chunks, size, r_each;
-};
-
-template <typename IO>
-__global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
-  __shared__ double sums[256];
-  const int64_t bh = blockIdx.x / a.tiles;
-  const int tile = int(blockIdx.x % a.tiles);
-  const int b = int(bh / a.H), h = int(bh % a.H);
-  const int first = tile * a.chunks * kChunk;
-  const int n = min(tokens_of(a.lengths, b, a.T) - first, a.chunks * kChunk);
-  double sum = 0.0;
-  if (n > 0) {
-    const float* s = a.S + (bh * a.tiles + tile) * a.size;
-    const float* r = a.R + (bh * a.r_each + tile) * a.size;
-    // (the size is a multiple of 256, of 1024 but for 16 x 16)
-#pragma unroll 4
-    for (int e = threadIdx.x * 4; e < (a.S ? a.size : 0); e += 1024) {
-      float sv[4], rv[4];
-      load_vec<float, 4>(s + e, sv);
-      load_vec<float, 4>(r + e, rv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum = __builtin_fma(double(sv[i]), double(rv[i]), sum);
-    }
-    sum *= n;
-    // d / 4 threads a token
-    const int each = a.d / 4, part = threadIdx.x % each * 4;
-    const int64_t at = b * a.d_at.b + h * a.d_at.h + part;
-    const IO* q = static_cast<const IO*>(a.q) + b * a.q_at.b + h * a.q_at.h + part;
-    const IO* k = static_cast<const IO*>(a.k) + b * a.k_at.b + h * a.k_at.h + part;
-#pragma unroll 4
-    for (int j = threadIdx.x / each; j < n; j += 256 / each) {
-      const int64_t t = first + j;
-      float qv[4], kv[4], dqv[4], dkv[4];
-      load_vec<IO, 4>(q + t * a.q_at.t, qv);
-      load_vec<IO, 4>(k + t * a.k_at.t, kv);
-      load_vec<float, 4>(a.dq + at + t * a.d_at.t, dqv);
-      load_vec<float, 4>(a.dk + at + t * a.d_at.t, dkv);
-      double u = 0.0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u = __builtin_fma(double(kv[e]), double(dkv[e]), __builtin_fma(-double(qv[e]), double(dqv[e]), u));
-      sum += u * (n - 1 - j);
-    }
-  }
-  sums[threadIdx.x] = sum;
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    sum = (sums[threadIdx.x] + sums[threadIdx.x + 64]) + (sums[threadIdx.x + 128] + sums[threadIdx.x + 192]);
-#pragma unroll
-    for (int m = 32; m > 0; m /= 2) sum += __shfl_xor(sum, m);
-    if (threadIdx.x == 0) a.parts[(int64_t(b) * a.tiles + tile) * a.H + h] = float(sum);
-  }
-}
-
-// Workspace of the gradients: S slots, R slots (one more; of heads of one tile the adjoint
-// before the first token alone), rows of partial sums.
+// ---- gradients -------------------------------------------------------------------------
+// Workspace of the gradients: S slots and R slots (one more) where heads have several tiles,
+// rows of partial sums of the decays' gradient.
 struct BwdLayout {
   int64_t S, R, parts;   // floats
   BwdLayout(const LinearArgs& a, const Tiles& t) {
     const int64_t size = int64_t(a.dk) * a.dv;
     S = t.tiles > 1 ? t.heads * t.tiles * size : 0;
-    R = t.heads * (t.tiles > 1 ? t.tiles + 1 : 1) * size;
+    R = t.tiles > 1 ? t.heads * (t.tiles + 1) * size : 0;
     parts = int64_t(a.B) * t.tiles * a.H;
   }
 };
@@ -355,7 +284,6 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   r.rev = true;
   s.clear = r.clear = a.lengths != nullptr;
   r.write = a.scale;
-  float* before = R;     // the adjoint before the first token, where it lies by itself
   if (several) {
     FALCON_TRY(FALCON_BY_KEYS(sums, a.dk, s, &r, st));
     const Carry back{R, t.tiles + 1, 1, a.dS_T, a.dS0, true};
@@ -363,13 +291,12 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   } else {
     s.start = a.S0;
     r.start = a.dS_T;
-    if (a.dS0) before = a.dS0;
   }
   // dv = (k, q, dO) against time
   LinearSweep dv = r;
   dv.q = a.k; dv.q_at = a.k_at;
   dv.out = a.dv_out; dv.out_at = a.dv_at;
-  if (!several && (a.dS0 || a.dlog_decay)) dv.last = before;
+  if (!several) dv.last = a.dS0;
   // dk = (v, dO, q) against time, from the transposed adjoint
   LinearSweep dk = r;
   dk.q = a.v; dk.q_at = a.v_at;
@@ -389,15 +316,21 @@ hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
   dq.out = a.dq; dq.out_at = a.dqk_at;
   FALCON_TRY(FALCON_BY_KEYS(gradients, a.dk, dv, dk, dq, st));
   if (a.dlog_decay) {
-    const DecayGrad d{a.q, a.k, a.q_at, a.k_at, a.dqk_at, a.dq, a.dk_out, several ? S : a.S0, before, a.lengths, parts,
-                      a.H, a.T, a.dk, t.tiles, t.chunks, size, several ? t.tiles + 1 : 1};
-    const dim3 grid(unsigned(t.heads * t.tiles));
-    if (a.bf16) {
-      decay_grad_kernel<bf16_t><<<grid, dim3(256), 0, st>>>(d);
-    } else {
-      decay_grad_kernel<float><<<grid, dim3(256), 0, st>>>(d);
-    }
-    FALCON_TRY(hipGetLastError());
+    LinearDecays d{};
+    d.q = a.q; d.k = a.k; d.v = a.v; d.dO = a.dO;
+    d.q_at = a.q_at; d.k_at = a.k_at; d.v_at = a.v_at; d.o_at = a.o_at;
+    d.log_decay = a.log_decay;
+    d.lengths = a.lengths;
+    d.S = several ? S : a.S0;
+    d.R = several ? R + size : a.dS_T;
+    d.s_each = t.tiles;
+    d.r_each = several ? t.tiles + 1 : 1;
+    d.parts = parts;
+    d.heads = t.heads;
+    d.H = a.H; d.T = a.T; d.dv = a.dv; d.tiles = t.tiles; d.chunks = t.chunks;
+    d.read = a.scale;
+    d.bf16 = a.bf16;
+    FALCON_TRY(FALCON_BY_KEYS(decays, a.dk, d, st));
     FALCON_TRY(launch_sum_parts({parts, int64_t(a.B) * t.tiles, a.H, a.H, {a.dlog_decay, nullptr, nullptr}, {a.H, a.H}}, st));
   }
 #undef FALCON_TRY

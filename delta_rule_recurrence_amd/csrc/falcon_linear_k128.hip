@@ -1,5 +1,5 @@
 // Sweeps of linear attention over keys of 128.
-#include "falcon_linear_kernel.h"
+#include "falcon_linear_decay.h"
 
 namespace falcon {
 
@@ -10,5 +10,6 @@ hipError_t launch_linear_outputs_128(const LinearSweep& s, hipStream_t st) { ret
 hipError_t launch_linear_gradients_128(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st) {
   return linear::gradients_of<128>(dv, dk, dq, st);
 }
+hipError_t launch_linear_decays_128(const LinearDecays& a, hipStream_t st) { return linear::decays_of<128>(a, st); }
 
 }  // namespace falcon

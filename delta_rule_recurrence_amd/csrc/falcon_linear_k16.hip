@@ -1,5 +1,5 @@
 // Sweeps of linear attention over keys of 16.
-#include "falcon_linear_kernel.h"
+#include "falcon_linear_decay.h"
 
 namespace falcon {
 
@@ -10,5 +10,6 @@ hipError_t launch_linear_outputs_16(const LinearSweep& s, hipStream_t st) { retu
 hipError_t launch_linear_gradients_16(const LinearSweep& dv, const LinearSweep& dk, const LinearSweep& dq, hipStream_t st) {
   return linear::gradients_of<16>(dv, dk, dq, st);
 }
+hipError_t launch_linear_decays_16(const LinearDecays& a, hipStream_t st) { return linear::decays_of<16>(a, st); }
 
 }  // namespace falcon

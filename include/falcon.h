@@ -578,7 +578,9 @@ falcon_status falcon_linear_step(const falcon_linear_problem* p, const void* q, 
  * falcon_linear_bwd -- gradients of <dO, o> + <dS_T, S_T>; the states are recomputed.
  *  dO         : io dtype, in o's layout;  dS_T : [B, H, dk, dv] float32 or NULL.
  *  dq, dk, dv : float32, contiguous, in the layouts of q and k, and of v.
- *  dlog_decay : [H] float32, or NULL to skip.
+ *  dlog_decay : [H] float32, or NULL to skip.  A sum of terms each decayed as often as it
+ *               counts, so a head's error is float32's of its own terms, however fast it
+ *               forgets; 0 for -infinity.
  *  dS0        : [B, H, dk, dv] float32, or NULL to skip.
  *  workspace  : at least falcon_linear_bwd_workspace_bytes(p) bytes.
  */
