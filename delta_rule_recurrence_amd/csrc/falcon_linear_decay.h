@@ -43,15 +43,16 @@ constexpr float kLog2eRest = 1.92596299112661747e-8f;   // log2(e) less kLog2e
 struct Base {
   float hi, lo;
   __device__ __forceinline__ explicit Base(float log_a) {
+#pragma clang fp contract(off)   // (the rounded product, also where a power takes it times one)
     log_a = log_a < -1000.0f ? -1000.0f : log_a;   // (zero from the first power on)
     hi = log_a * kLog2e;
     lo = __builtin_fmaf(log_a, kLog2e, -hi) + log_a * kLog2eRest;
   }
 };
-__device__ __forceinline__ float power(const Base& b, int n) {
-  if (n == 0) return 1.0f;
-  const float x = b.hi * float(n), rest = __builtin_fmaf(b.hi, float(n), -x) + b.lo * float(n), whole = __builtin_rintf(x);
-  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((x - whole) + rest), int(whole));
+__device__ __forceinline__ float power(const Base& a, int n) {
+  const float whole = __builtin_rintf(a.hi * float(n));
+  const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(a.hi, float(n), -whole) + a.lo * float(n));
+  return __builtin_amdgcn_ldexpf(p, int(whole));
 }
 
 // Eight waves where four would own twice 32 registers of states, as in the sweeps with float32.
