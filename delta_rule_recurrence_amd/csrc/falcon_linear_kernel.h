@@ -201,6 +201,32 @@ __device__ __forceinline__ void get(const char* lds, int frag, int l, f32x8& v) 
   v = {p[0], p[64]};
 }
 
+// One number of a fragment that was put as float32.
+template <typename IO>
+__device__ __forceinline__ float got(const char* lds, int frag, int l, int e) {
+  if constexpr (sizeof(IO) == 4) {
+    return reinterpret_cast<const float*>(lds)[(frag * 128 + (e >> 2) * 64 + l) * 4 + (e & 3)];
+  } else {
+    float sum = 0.0f;
+    for (int n = kTerms - 1; n >= 0; --n) sum += io<bf16_t>::load(reinterpret_cast<const bf16_t*>(lds), ((frag * kTerms + n) * 64 + l) * 8 + e);
+    return sum;
+  }
+}
+
+// Whether an operand holds an infinity or a NaN: an exponent of ones carries into the sign.
+__device__ __forceinline__ bool not_finite(bf16x8 v) {
+  const uint4 u = __builtin_bit_cast(uint4, v);
+  auto carry = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
+  return ((carry(u.x) | carry(u.y) | carry(u.z) | carry(u.w)) & 0x80008000u) != 0;
+}
+__device__ __forceinline__ bool not_finite(const f32x8& v) {
+  uint32_t all = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    all |= ((__float_as_uint(v.lo[e]) & 0x7f800000u) + 0x00800000u) | ((__float_as_uint(v.hi[e]) & 0x7f800000u) + 0x00800000u);
+  return (all & 0x80000000u) != 0;
+}
+
 // Columns 8 g .. + 7 of a row, the lane's own, to where the fragment has them.
 __device__ __forceinline__ void put_row(char* lds, int frag, int g, int c16, bf16x8 v) {
   uint2* p = reinterpret_cast<uint2*>(lds) + (frag * 64 + 32 * (g & 1) + c16) * 2 + (g >> 1);
@@ -583,6 +609,7 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           for (int m = 0; m < 2; ++m) get(ps, tokens(x) * 2 + m, l, to[m]);
         };
         if constexpr (kAhead) scores(0, pf[0]);
+        float noticed = 0.0f;   // NaN, once there is an output that is not finite
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
           const int rb = tokens(x), i = 16 * rb + c16 - shift;
@@ -600,10 +627,56 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) o[x][j] = mma(vf[j][m], pf[kAhead ? x % 2 : 0][m], o[x][j]);
           }
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) noticed = __builtin_fmaf(o[x][j][r], 0.0f, noticed);
           if (uint32_t(i) < uint32_t(n)) {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
               store4(reinterpret_cast<O*>(to + (uint32_t(i) * uint32_t(out_step) + 16 * column(j) + 4 * g) * uint32_t(sizeof(O))), o[x][j]);
+          }
+        }
+        // A value that is not finite times a score that the mask has made zero is not zero: the
+        // columns that hold one once more, by the terms that each token has.  (Rows from memory: LDS
+        // may hold the next chunk's.)  The branch costs 2 of 31 us at 8 x 2048 x 12 x 64 and 4 of 75 us
+        // of the gradients by what it keeps the compiler from moving across; values cleaned
+        // where they are staged, or such tiles once more behind the loop, cost more.
+        if (__any(noticed != 0.0f)) {
+          __threadfence();   // behind what other lanes have stored there
+          const IO* const queries = Q + int64_t(c) * kChunk * q_step;
+          const IO* const values = V + int64_t(c) * kChunk * v_step;
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            int bad = not_finite(vf[j][0]) || not_finite(vf[j][1]);
+            bad |= __shfl_xor(bad, 16);
+            bad |= __shfl_xor(bad, 32);
+            if (!__any(bad)) continue;
+            const int col = 16 * column(j) + c16;
+#pragma unroll 1
+            for (int x = 0; x < 16 * kRows; ++x) {
+              const int row = 16 * tokens(x / 16) + x % 16, i = row - shift;
+              if (uint32_t(i) >= uint32_t(n)) continue;
+              float sum = 0.0f;
+#pragma unroll
+              for (int bb = 0; bb < kB; ++bb)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                  if (32 * bb + 16 * t < DK)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                      sum = __builtin_fmaf(S[j][bb][t][r], io<IO>::load(queries, i * q_step + 32 * bb + 16 * t + 4 * g + r), sum);
+              sum += __shfl_xor(sum, 16);
+              sum += __shfl_xor(sum, 32);
+              sum *= power(e, s.rev ? n - 1 - i : i + 1) * s.read;
+#pragma unroll 1
+              for (int k = s.rev ? i : 0; k < (s.rev ? n : i + 1); ++k) {
+                const int key = k + shift;
+                sum = __builtin_fmaf(got<IO>(ps, row / 16 * 2 + key / 32, (key & 12) * 4 + row % 16, (key & 3) + (key & 16) / 4),
+                                     io<IO>::load(values, k * v_step + col), sum);
+              }
+              if (bad && g == 0) io<O>::store(reinterpret_cast<O*>(to), i * out_step + col, sum);
+            }
           }
         }
       }

@@ -544,8 +544,9 @@ size_t falcon_scan_bwd_workspace_bytes(const falcon_scan_problem* p);
  * chunks of 64 tokens: float32 throughout with float32 inputs, and with bf16 inputs
  * by bf16 products with float32 sums in which every float32 operand is a sum of three
  * bf16 numbers, which hold all its bits, so results are those of float32 arithmetic,
- * rounded once.  A token whose values are not finite reaches the
- * outputs of its sequence from the start of its chunk on.
+ * rounded once.  A value that is not finite reaches what depends on it and nothing else:
+ * the outputs of its own and of later tokens, the state at the end; gradients the other
+ * way round (dlog_decay, a sum over all of a head's tokens, from any of them).
  */
 typedef struct {
   int32_t B, H, T, dk, dv;
