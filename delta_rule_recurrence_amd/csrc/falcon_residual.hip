@@ -20,8 +20,8 @@
 // Measured there: forward 34 us (176 MB, 5.2 TB/s), gradients 69 us (330 MB, 4.8 TB/s).
 //
 // In 8 bits, 32 adjacent channels of a row share a step, the smallest power of two of which
-// 127 reach the largest of them: a value is off by at most half a step, 2^-7 of the
-// largest, and dividing by and multiplying with the step is exact.
+// 127 reach the largest of them: a value is off by at most half a step, less than 1/127 of
+// the largest (but at the smallest step, 2^-126), and dividing by and multiplying with the step is exact.
 
 #include <algorithm>
 
@@ -692,8 +692,9 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   const int64_t rows = int64_t(a.B) * a.T;
   // as many workgroups as the CUs hold at a time, at three or four waves a SIMD: one more round of a
   // few costs what a whole one does (5555 rows of 2304, five waves each, gradients: 72 us
-  // with two a CU, 96 us with three).  Workgroups of three waves fit five times (16384 rows of
-  // 1536: forward 36.6 us, 39.8 us with four; gradients of 8192 rows: 76 and 74 us).
+  // with two a CU, 96 us with three; forward 8001 rows 62 and 75 us).  Workgroups of three waves fit
+  // five times: forward, 16384 rows from memory, of 1536 70.5 us and 72 with four, of 1280 60 and 64, of 1100
+  // 64 and 69; but gradients of 8192 rows of 1536 76 us and 74 with four.
   const int waves = s.rows_block * s.threads_row / 64, simd = bwd && !by_piece(form_of(a)) ? 3 : 4;
   const int64_t most = 256 * (waves == 3 && !bwd ? 5 : std::max(1, simd / ((waves + 3) / 4)));
   const int64_t each = std::max<int64_t>(1, (rows + most * s.rows_block - 1) / (most * s.rows_block));
@@ -709,19 +710,23 @@ Shape shape_of(const ResidualArgs& a, bool bwd) {
   return s;
 }
 
-// Calls go(most threads, form) with compile-time values: a workgroup of 1024 threads has 128
-// registers a thread, one of 256 up to 512.
-template <typename Go>
+// Calls go(most threads, form) with compile-time values.  Four waves a SIMD, 128 registers a
+// thread, is what a workgroup of 1024 threads has and what the forms of pieces are held to, so
+// these come for any width at once; the gradients of channels take 167 where three waves a
+// SIMD do (12 of them in memory, 56 at 128).
+template <bool BWD, typename Go>
 hipError_t by_shape(const ResidualArgs& a, const Shape& s, Go go) {
   using std::integral_constant;
-  if (form_of(a) == kElements) return go(integral_constant<int, 256>{}, integral_constant<int, kElements>{});
-  auto by_wide = [&](auto most) {
-    if (form_of(a) == kPieces) return go(most, integral_constant<int, kPieces>{});
-    return form_of(a) == kRagged ? go(most, integral_constant<int, kRagged>{}) : go(most, integral_constant<int, kChannels>{});
-  };
-  if (s.threads_row <= 256) return by_wide(std::integral_constant<int, 256>{});
-  if (s.threads_row <= 512) return by_wide(std::integral_constant<int, 512>{});
-  return by_wide(std::integral_constant<int, 1024>{});
+  switch (form_of(a)) {
+    case kElements: return go(integral_constant<int, 256>{}, integral_constant<int, kElements>{});
+    case kChannels:
+      if constexpr (BWD) {
+        if (s.threads_row <= 512) return go(integral_constant<int, 512>{}, integral_constant<int, kChannels>{});
+      }
+      return go(integral_constant<int, 1024>{}, integral_constant<int, kChannels>{});
+    case kRagged: return go(integral_constant<int, 1024>{}, integral_constant<int, kRagged>{});
+    default: return go(integral_constant<int, 1024>{}, integral_constant<int, kPieces>{});
+  }
 }
 
 template <typename Kernel>
@@ -734,7 +739,7 @@ hipError_t allow_lds(Kernel kernel, size_t lds) {
 
 hipError_t launch_residual_fwd(const ResidualArgs& a, hipStream_t st) {
   const Shape s = shape_of(a, false);
-  return by_shape(a, s, [&](auto most, auto form) {
+  return by_shape<false>(a, s, [&](auto most, auto form) {
     auto* const kernel = residual_fwd_kernel<most(), form()>;
     const hipError_t e = allow_lds(kernel, s.lds);
     if (e != hipSuccess) return e;
@@ -751,7 +756,7 @@ hipError_t launch_residual_bwd(const ResidualArgs& a, hipStream_t st) {
   const Shape s = shape_of(a, true);
   const bool params = a.dalpha || a.dpost_weight || a.dpre_weight;
   if (s.blocks > 0) {
-    const hipError_t e = by_shape(a, s, [&](auto most, auto form) {
+    const hipError_t e = by_shape<true>(a, s, [&](auto most, auto form) {
       auto* const kernel = residual_bwd_kernel<most(), form()>;
       const hipError_t e = allow_lds(kernel, s.lds);
       if (e != hipSuccess) return e;
