@@ -28,7 +28,7 @@ struct Tiles {
   int chunks, tiles;   // chunks of a tile; tiles of a head
 };
 
-Tiles cut(const LinearArgs& a) {
+Tiles cut(const LinearArgs& a, bool bwd) {
   const int64_t heads = int64_t(a.B) * a.H, all = (int64_t(a.T) + kChunk - 1) / kChunk;
   // tiles of a head for three workgroups a CU, or for the two or one that wide heads leave room
   // for (kernels of a prompt together, when this was chosen: 8 x 2048 x 12 x 64, 384 tiles 60 us,
@@ -36,13 +36,18 @@ Tiles cut(const LinearArgs& a) {
   const int64_t all_tiles = a.dk * a.dv > 64 * 128 ? 256 : a.dk * a.dv > 64 * 64 ? 512 : 768;
   const int64_t want = std::max<int64_t>(1, all_tiles / std::max<int64_t>(heads, 1));   // (one more would take a round of its own)
   // A short prompt's heads take one tile each: one launch for three, and no states between
-  // tiles.  (us of a call, one tile and several.  Outputs: 8 heads of 64 x 64 in bfloat16, 4 chunks
-  // 14 and 21, 8 chunks 24 and 21; 96 heads, 8 chunks 25 and 26, 12 chunks 35 and 29, of 128 x 128
-  // 8 chunks 36 and 50; float32, 8 heads, 2 chunks 14 and 21, 4 chunks 25 and 21; 96 heads, 4 chunks
-  // 26 and 27, 8 chunks 47 and 38.  Gradients: 8 heads, bfloat16, 4 chunks 19 and 24; 96 heads
-  // 19 and 31; float32, 8 heads, 2 chunks 18 and 24, 4 chunks of 64 x 128 39 and 25; 96 heads 72
-  // and 82.  In a graph, without the host, 8 heads' 4 chunks take 14 and 11.)
-  const int64_t few = (heads >= 64 ? 2 : 1) * (a.bf16 ? 4 : 2);
+  // tiles.  us of a call / of a replay, one tile and several.  Outputs in bfloat16, 8 heads: 4 chunks
+  // of 64 x 64 16/16 and 21/12, of 64 x 128 19/19 and 21/14, of 128 x 128 22/22 and 21/16 (2 chunks 14/13 and
+  // 21/16); 96 heads: 4 chunks of 64 x 64 17/17 and 21/21, 8 chunks 30/30 and 25/26, of 64 x 128 34/35 and
+  // 35/35, of 128 x 128 41/42 and 49/50.  float32, 8 heads: 2 chunks of 64 x 64 14/14 and 21/14, of 128 x
+  // 128 31/31 and 26/25 (1 chunk 18 both); 96 heads: 4 chunks 25/26 and 26/26, of 128 x 128 59/60 and 61/61,
+  // 8 chunks 47/48 and 37/38.  Gradients in bfloat16, 8 heads: 4 chunks of 64 x 64 18/15 and 24/12; 96
+  // heads: 8 chunks 35/35 and 44/44, of 128 x 128 76/76 and 106/106; float32, 8 heads: 2 chunks of 128 x 128
+  // 26/26 and 28/27; 96 heads: 4 chunks of 64 x 64 38/37 and 44/45.  (So a call by itself decides for few heads:
+  // a replay of 4 chunks would rather have several tiles.)
+  const int64_t base = a.bf16 ? 4 : 2, size = a.dk * a.dv;
+  const bool twice = heads >= 64 && (bwd || !a.bf16 || size >= 64 * 128), half = heads < 64 && !bwd && size > 64 * 128;
+  const int64_t few = twice ? 2 * base : half ? base / 2 : base;
   const int64_t chunks = all <= few ? std::max<int64_t>(all, 1) : std::max<int64_t>(1, (all + want - 1) / want);
   return {heads, int(chunks), int(std::max<int64_t>(1, (all + chunks - 1) / chunks))};
 }
@@ -68,8 +73,8 @@ struct Carries {
   int H, T, tiles, chunks, size;   // size: elements of a state
 };
 
-// A workgroup a head, 256 elements of its state and a carry.  (2^21 heads of 128 x 128 have more
-// of these threads than a grid has in one direction.)
+// A workgroup a head, 256 elements of its state and a carry.  (Heads of several tiles are at
+// most 384: more are a tile each.)
 __global__ __launch_bounds__(256) void carry_kernel(Carries a) {
   const Carry c = a.c[blockIdx.z];
   const uint32_t bh = blockIdx.x;
@@ -216,13 +221,13 @@ struct BwdLayout {
 }  // namespace
 
 size_t linear_workspace_bytes(const LinearArgs& a) {
-  const Tiles t = cut(a);
+  const Tiles t = cut(a, false);
   return t.tiles > 1 ? size_t(t.heads) * t.tiles * a.dk * a.dv * sizeof(float) : 0;
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
   if (a.T == 0) return launch_state_copy(a.S0, a.S_T, int64_t(a.B) * a.H * a.dk * a.dv, st);
-  const Tiles t = cut(a);
+  const Tiles t = cut(a, false);
   LinearSweep s = sweep_base(a, t);
   s.k = a.k; s.v = a.v;
   s.k_at = a.k_at; s.v_at = a.v_at;
@@ -250,12 +255,12 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t st) {
 hipError_t launch_linear_step(const LinearArgs& a, hipStream_t st) { return a.bf16 ? step_of<bf16_t>(a, st) : step_of<float>(a, st); }
 
 size_t linear_bwd_workspace_bytes(const LinearArgs& a) {
-  const BwdLayout l(a, cut(a));
+  const BwdLayout l(a, cut(a, true));
   return size_t(l.S + l.R + l.parts) * sizeof(float);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t st) {
-  const Tiles t = cut(a);
+  const Tiles t = cut(a, true);
   const BwdLayout l(a, t);
   float* const S = a.workspace;
   float* const R = S + l.S;
