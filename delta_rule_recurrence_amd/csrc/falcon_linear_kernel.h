@@ -30,12 +30,13 @@
 // 8 bits each and so all of float32's.  float32 inputs use the float32 matrix
 // instruction throughout.
 //
-// What bounds it, at 8 x 2048 x 12 x 64 in bfloat16: outputs of a prompt 25 us for the 113 MB
-// that they move (4.6 TB/s, a copy's rate), sums 14 us for 63 MB, gradients 70 us for 330 MB.
-// At 128 x 128 a state fills the registers of eight waves, one workgroup a CU, whose products,
-// vector instructions and LDS reads follow one another (20, 29 and 27 % of the time).  The
-// state as an operand from registers, where it passed through LDS before, and rows of the
-// next chunk ahead: outputs 35 -> 29 us; factored decays, which leave registers for a third
+// What bounds it, at 8 x 2048 x 12 x 64 in bfloat16: sums 13 us for 63 MB and gradients 75 us for
+// 330 MB, about a copy's rate; outputs of a prompt 31 us for 116 MB (3.7 TB/s), of which the third
+// term of float32 operands takes 3 and values that are not finite, looked for, 2.  At 128 x 128 a
+// state fills the registers of eight waves, one workgroup a CU, whose products, vector
+// instructions and LDS reads follow one another (25, 35 and 26 % of the time).  The state as
+// an operand from registers, where it passed through LDS before, and rows of the next chunk
+// ahead: outputs (with two terms) 35 -> 29 us; factored decays, which leave registers for a third
 // workgroup: 29 -> 25 us.
 #pragma once
 
@@ -290,8 +291,8 @@ __device__ __forceinline__ float power(float log2_a, int n) {
 }
 
 // Waves of a workgroup: eight where what four hold would not fit their registers, float32
-// operands of 128 columns and states of 128 x 128 (16384 x 12 in bfloat16: outputs 63 us,
-// four waves 72 us with 48 registers in memory; halves of the values apart 70 us).
+// operands of 128 columns and states of 128 x 128 (16384 x 12 in bfloat16 by two terms: outputs
+// 63 us, four waves 72 us with 48 registers in memory; halves of the values apart 70 us).
 template <typename IO, int DK, int DV>
 constexpr int waves() {
   return (sizeof(IO) == 4 && (DK >= 128 || DV >= 128)) || (DK >= 128 && DV >= 128) ? 8 : 4;
@@ -340,8 +341,8 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
   using Split = typename Ops::Split;
 
   // Where registers are left the reads of LDS for several products are issued ahead of the
-  // first one: by itself the compiler waits for each in turn (heads of 128 x 128: outputs of
-  // a prompt 63 -> 62 us, gradients 124 -> 121 us; narrower heads have no registers left).
+  // first one: by itself the compiler waits for each in turn (heads of 128 x 128 by two terms: outputs
+  // of a prompt 63 -> 62 us, gradients 124 -> 121 us; narrower heads have no registers left).
   constexpr bool kAhead = kWaves == 8 && sizeof(IO) == 2;
   auto issued = [&]() {
     if constexpr (kAhead) asm volatile("" ::: "memory");
