@@ -263,24 +263,22 @@ __global__ __launch_bounds__((64 * decay_waves<DK, DV>()), 2) void decay_kernel(
             }
           }
         }
-        // (also where no one reads the result: a branch around it costs copies of both states)
+        // (also where no one reads the result: a branch around it costs copies of both states.  The
+        // chunk's sums are made from zero and added once: a product added to the states would be
+        // rounded at their size each time, 16 times a chunk in float32.)
         const float whole = n == kChunk ? across : power(e, n), tokens = float(n);
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j)
+        for (int j = 0; j < kOwn; ++j) {
+          f32x4 s0[kMine], s1[kMine];
 #pragma unroll
-          for (int y = 0; y < kMine; ++y) {
-            D[j][y] = (D[j][y] + S[j][y] * tokens) * whole;
-            S[j][y] = S[j][y] * whole;
-          }
+          for (int y = 0; y < kMine; ++y) s0[y] = s1[y] = frag::zero4();
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          f32x4 weight[2];
+          for (int m = 0; m < 2; ++m) {
+            f32x4 weight[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) weight[u][r] = to_end[m][u] * down[r];
-#pragma unroll
-          for (int j = 0; j < kOwn; ++j) {
+              for (int r = 0; r < 4; ++r) weight[u][r] = to_end[m][u] * down[r];
             Split plain, counted;
             operands(vs, m, j, weight, float(kChunk - 1 - 32 * m) - base, -1.0f, plain, counted);
             Exact x = turned_frag<kPk>(ks, m, 16 * row_tile(0), g, c16);
@@ -288,10 +286,15 @@ __global__ __launch_bounds__((64 * decay_waves<DK, DV>()), 2) void decay_kernel(
             for (int y = 0; y < kMine; ++y) {
               const Exact next = turned_frag<kPk>(ks, m, 16 * row_tile(y + 1 < kMine ? y + 1 : y), g, c16);
               issued();
-              S[j][y] = mma(x, plain, S[j][y]);
-              D[j][y] = mma(x, counted, D[j][y]);
+              s0[y] = mma(x, plain, s0[y]);
+              s1[y] = mma(x, counted, s1[y]);
               x = next;
             }
+          }
+#pragma unroll
+          for (int y = 0; y < kMine; ++y) {
+            D[j][y] = (D[j][y] + S[j][y] * tokens) * whole + s1[y];
+            S[j][y] = S[j][y] * whole + s0[y];
           }
         }
       }

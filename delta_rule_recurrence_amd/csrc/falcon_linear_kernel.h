@@ -707,10 +707,12 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           for (int m = 0; m < 2; ++m) kf[m] = turned_frag<kPk>(ks, m, 32 * bb + 16 * t, g, c16);
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
-            f32x4 acc = S[j][bb][t] * across;
+            // (In float32 a chunk's 16 products are summed from zero and added once: each added to the
+            // state would be rounded at its size.  bfloat16's are six, and registers are short.)
+            f32x4 acc = sizeof(IO) == 4 ? frag::zero4() : S[j][bb][t] * across;
 #pragma unroll
             for (int m = 0; m < 2; ++m) acc = mma(kf[m], wf[j][m], acc);
-            S[j][bb][t] = acc;
+            S[j][bb][t] = sizeof(IO) == 4 ? S[j][bb][t] * across + acc : acc;
           }
         }
     }
