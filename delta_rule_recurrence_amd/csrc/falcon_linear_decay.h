@@ -286,8 +286,13 @@ __global__ __launch_bounds__((64 * decay_waves<DK, DV>()), 2) void decay_kernel(
             for (int y = 0; y < kMine; ++y) {
               const Exact next = turned_frag<kPk>(ks, m, 16 * row_tile(y + 1 < kMine ? y + 1 : y), g, c16);
               issued();
-              s0[y] = mma(x, plain, s0[y]);
-              s1[y] = mma(x, counted, s1[y]);
+              if (sizeof(IO) == 2 || m == 0) {
+                s0[y] = mma(x, plain, s0[y]);
+                s1[y] = mma(x, counted, s1[y]);
+              } else {   // (16 products in a row are rounded more than two halves)
+                s0[y] = s0[y] + mma(x, plain, frag::zero4());
+                s1[y] = s1[y] + mma(x, counted, frag::zero4());
+              }
               x = next;
             }
           }

@@ -707,12 +707,17 @@ __device__ __forceinline__ void sweep(const LinearSweep& s, uint32_t block, char
           for (int m = 0; m < 2; ++m) kf[m] = turned_frag<kPk>(ks, m, 32 * bb + 16 * t, g, c16);
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
-            // (In float32 a chunk's 16 products are summed from zero and added once: each added to the
-            // state would be rounded at its size.  bfloat16's are six, and registers are short.)
-            f32x4 acc = sizeof(IO) == 4 ? frag::zero4() : S[j][bb][t] * across;
+            if constexpr (sizeof(IO) == 4) {
+              // A chunk's 16 products in two halves from zero, added once: each added to the state would
+              // be rounded at its size.  (bfloat16's are six, and registers are short.)
+              const f32x4 first = mma(kf[0], wf[j][0], frag::zero4()), second = mma(kf[1], wf[j][1], frag::zero4());
+              S[j][bb][t] = S[j][bb][t] * across + (first + second);
+            } else {
+              f32x4 acc = S[j][bb][t] * across;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) acc = mma(kf[m], wf[j][m], acc);
-            S[j][bb][t] = sizeof(IO) == 4 ? S[j][bb][t] * across + acc : acc;
+              for (int m = 0; m < 2; ++m) acc = mma(kf[m], wf[j][m], acc);
+              S[j][bb][t] = acc;
+            }
           }
         }
     }
