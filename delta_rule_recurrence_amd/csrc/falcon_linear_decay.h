@@ -27,8 +27,8 @@
 //
 // A chunk's rows are loaded where they are needed: workgroups that share a CU hide it better
 // than loads a chunk ahead, whose registers they lack (8 x 2048 x 12 x 64 x 64 in bfloat16 36 us,
-// ahead 43 us; 4096 x 8 x 128 x 128 in float32 57 and 70 us, 2 x 4096 x 12 x 128 x 128 in bfloat16 64
-// and 61 us).
+// ahead 43 us; 2 x 4096 x 12 x 128 x 128 in bfloat16 64 and 61 us; 4096 x 8 x 128 x 128 in float32 57
+// and 70 us, 60 now that its chunks' sums come in halves).
 #pragma once
 
 #include "falcon_linear_kernel.h"
